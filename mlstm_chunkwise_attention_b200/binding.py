@@ -41,8 +41,29 @@ class SavedLayout(ctypes.Structure):
         "state_n_bytes", "tile_table_bytes", "total")]
 
 
+class Rows(ctypes.Structure):
+    """mlstm_rows_t: a strided activation (batch, token and head strides in elements)."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_longlong),
+                ("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
+class ScanProblem(ctypes.Structure):
+    """mlstm_scan_t: the inputs of a selective scan call."""
+    _fields_ = ([(n, Rows) for n in ("x", "dt", "z", "b", "c")] +
+                [(n, ctypes.c_void_p) for n in ("a", "skip", "dt_bias", "state_in")] +
+                [(n, ctypes.c_int) for n in ("B", "T", "D", "G", "N", "softplus", "dtype")])
+
+
+class ScanGrads(ctypes.Structure):
+    """mlstm_scan_grads_t: the outputs of a selective scan's backward."""
+    _fields_ = ([(n, Rows) for n in ("dx", "ddt", "dz", "db", "dc")] +
+                [(n, ctypes.c_void_p) for n in ("da", "dskip", "ddt_bias", "dstate_in")])
+
+
 _SIZES = [ctypes.c_int] * 8  # B, NH, T, d_qk, d_hv, chunk, variant, dtype
 _P = ctypes.c_void_p
+_ROWS = ctypes.POINTER(Rows)
+_I = ctypes.c_int
 
 EXPORTS = {
     "mlstm_saved_layout": (ctypes.c_int, _SIZES + [ctypes.POINTER(SavedLayout)]),
@@ -70,6 +91,24 @@ EXPORTS = {
     "mlstm_log_decay": (ctypes.c_int, [_P, _P] + [ctypes.c_int] * 4 + [_P]),
     "mlstm_state_chain": (ctypes.c_int, [_P] * 4 + [ctypes.c_int] * 5 + [_P]),
     "mlstm_dstate_chain": (ctypes.c_int, [_P] * 6 + [ctypes.c_int] * 5 + [_P]),
+    # include/mlstm_block.h
+    "mlstm_conv_fwd": (_I, [_ROWS, _P, _P, _P, _ROWS, _P] + [_I] * 7 + [_P]),
+    "mlstm_conv_bwd_workspace_size": (ctypes.c_size_t, [_I] * 6),
+    "mlstm_conv_bwd": (_I, [_ROWS, _P, _P, _P, _ROWS, _P, _ROWS, _P, _P, _P, _P, ctypes.c_size_t] +
+                       [_I] * 7 + [_P]),
+    "mlstm_conv_step": (_I, [_ROWS, _P, _P, _P, _ROWS, _P] + [_I] * 6 + [_P]),
+    "mlstm_scan_saved_size": (ctypes.c_size_t, [_I] * 6),
+    "mlstm_scan_fwd": (_I, [ctypes.POINTER(ScanProblem), _ROWS, _P, _P, _P]),
+    "mlstm_scan_bwd_workspace_size": (ctypes.c_size_t, [_I] * 6),
+    "mlstm_scan_bwd": (_I, [ctypes.POINTER(ScanProblem), _ROWS, _P, _P, ctypes.POINTER(ScanGrads), _P,
+                            ctypes.c_size_t, _P]),
+    "mlstm_scan_step": (_I, [ctypes.POINTER(ScanProblem), _ROWS, _P, _P]),
+    "mlstm_group_norm_stats_size": (ctypes.c_size_t, [_I] * 5),
+    "mlstm_group_norm_workspace_size": (ctypes.c_size_t, [_I] * 7),
+    "mlstm_group_norm_fwd": (_I, [_ROWS, _P, _P, _ROWS, _ROWS, _P, _P, ctypes.c_size_t] + [_I] * 6 +
+                             [ctypes.c_float, _I, _P]),
+    "mlstm_group_norm_bwd": (_I, [_ROWS, _P, _P, _ROWS, _ROWS, _P, _ROWS, _ROWS, _P, _P, _P,
+                                  ctypes.c_size_t] + [_I] * 7 + [_P]),
 }
 
 

@@ -1,0 +1,434 @@
+"""The operators around the recurrence, for torch tensors (``include/mlstm_block.h``).
+
+* ``causal_conv_forward`` / ``_backward`` / ``_step``: the short causal convolution before the
+  cell or the scan;
+* ``selective_scan_forward`` / ``_backward`` / ``_step``: the selective state space scan;
+* ``group_norm_forward`` / ``_backward``: group norm with an activation or an output gate, after
+  the cell (statistics per token and head) or over a whole sequence.
+
+Like ``binding``, these functions allocate through PyTorch and call the CUDA library, which does
+all of the computation.  Activations are bfloat16 or float32, channels last ([B, T, D], any batch
+and token strides) or head-major ([B, NH, T, d], as the cell takes and returns them); parameters,
+their gradients and the scan's states are float32.  Work is enqueued on the current stream of the
+tensors' device, or on ``stream``: outputs and workspaces are then allocated for that stream.
+"""
+
+import contextlib
+import ctypes
+
+from .binding import (
+    BF16, FP32, STATUS_OK, STATUS_UNSUPPORTED, MLSTMError, Rows, ScanGrads, ScanProblem, load)
+
+ACT_NONE = 0
+ACT_SILU = 1
+ACT_SIGMOID = 2
+SCOPE_TOKEN = 0
+SCOPE_SEQUENCE = 1
+
+
+# --------------------------------------------------------------------------
+# argument checks and plumbing
+# --------------------------------------------------------------------------
+
+def _dtype_code(t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return FP32
+    raise TypeError(f"unsupported dtype {t.dtype}: use bfloat16 or float32")
+
+
+def _activation(name, t, shape, like):
+    """An activation of `like`'s dtype and device, last dimension contiguous, of this shape."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _fp32(name, t, shape, like):
+    """A contiguous float32 parameter or state (None passes)."""
+    import torch
+    if t is None:
+        return
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _contiguous(name, t, shape, like):
+    if t is None:
+        return
+    _activation(name, t, shape, like)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _dims(name, t, n):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t):
+    """[B, T, D] (or [B, D], one token) as mlstm_rows_t."""
+    if t is None:
+        return Rows(None, 0, 0, 0)
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0, 0)
+
+
+def _head_rows(t, layout, d):
+    """A tensor by heads: [B, NH, T, d] ("heads"), [B, T, NH, d] or [B, T, NH d] ("last"), or one
+    token, [B, NH, d] / [B, NH d]."""
+    if t is None:
+        return Rows(None, 0, 0, 0)
+    if layout == "heads":
+        return Rows(t.data_ptr(), t.stride(0), t.stride(2) if t.dim() == 4 else 0, t.stride(1))
+    head = t.stride(2) if t.dim() == 4 else d
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1), head)
+
+
+@contextlib.contextmanager
+def _launch(stream, like, *tensors):
+    """The stream handle to launch on, with `like`'s device current.  With an explicit stream,
+    allocations inside belong to it, and the inputs are kept from reuse until its work is done."""
+    import torch
+    with contextlib.ExitStack() as stack:
+        if like.device.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(like.device))
+        if stream is None:
+            s = torch.cuda.current_stream()
+        else:
+            if stream.device != like.device:
+                raise ValueError(f"stream is on {stream.device}, tensors on {like.device}")
+            s = stream
+            stack.enter_context(torch.cuda.stream(s))
+            for t in (like, *tensors):
+                if t is not None:
+                    t.record_stream(s)
+        yield ctypes.c_void_p(s.cuda_stream)
+
+
+def _check(status, where):
+    if status != STATUS_OK:
+        raise MLSTMError(status, where)
+
+
+def _bytes(n, device):
+    import torch
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+# --------------------------------------------------------------------------
+# short causal convolution
+# --------------------------------------------------------------------------
+
+def _conv_args(x, weight, bias, state, act, tokens):
+    _activation("x", x, x.shape, x)
+    D = x.shape[-1]
+    _dims("weight", weight, 2)
+    W = weight.shape[1]
+    _fp32("weight", weight, (D, W), x)
+    _fp32("bias", bias, (D,), x)
+    _contiguous("state", state, (x.shape[0], W - 1, D), x)
+    if act not in (ACT_NONE, ACT_SILU):
+        raise ValueError("act must be ACT_NONE or ACT_SILU")
+    if not 2 <= W <= 4:
+        raise MLSTMError(STATUS_UNSUPPORTED, f"causal convolution of {W} taps")
+    return x.shape[0], tokens, D, W, _dtype_code(x)
+
+
+def _heads_of(D, heads):
+    if heads is None:
+        return 1, D
+    if heads <= 0 or D % heads:
+        raise ValueError(f"{heads} heads do not divide {D} channels")
+    return heads, D // heads
+
+
+def causal_conv_forward(x, weight, bias=None, *, act=ACT_SILU, state_in=None, want_state=False,
+                        heads=None, stream=None):
+    """y = act(bias + causal convolution of x) per channel; returns (y, state_out).
+
+    x [B, T, D]; weight [D, W] with 2 to 4 taps, the last one on the current token; state_in
+    [B, W - 1, D]: the inputs before the first token (None: zeros).  y is [B, T, D], or with
+    ``heads`` head-major, [B, heads, T, D / heads].  state_out: the last W - 1 inputs, for a later
+    call or ``causal_conv_step`` (None unless want_state).
+    """
+    import torch
+    _dims("x", x, 3)
+    B, T, D, W, dt = _conv_args(x, weight, bias, state_in, act, x.shape[1])
+    NH, d = _heads_of(D, heads)
+    with _launch(stream, x, weight, bias, state_in) as s:
+        y = torch.empty((B, T, D) if heads is None else (B, NH, T, d), dtype=x.dtype, device=x.device)
+        state_out = (torch.empty((B, W - 1, D), dtype=x.dtype, device=x.device) if want_state
+                     else None)
+        _check(load().mlstm_conv_fwd(_rows(x), weight.data_ptr(), _ptr(bias), _ptr(state_in),
+                                     _head_rows(y, "last" if heads is None else "heads", d),
+                                     _ptr(state_out), B, T, NH, d, W, act, dt, s), "mlstm_conv_fwd")
+    return y, state_out
+
+
+def causal_conv_backward(x, weight, bias, dy, *, act=ACT_SILU, state_in=None, dstate_out=None,
+                         want_dstate=False, stream=None):
+    """Gradients of sum(dy y) + sum(dstate_out state_out): dict of dx [B, T, D], dweight, dbias
+    (None without a bias) and dstate_in (None unless want_dstate).  dy is laid out like the
+    forward's y: [B, T, D], or head-major [B, NH, T, d]."""
+    import torch
+    _dims("x", x, 3)
+    B, T, D, W, dt = _conv_args(x, weight, bias, state_in, act, x.shape[1])
+    NH = 1
+    if dy.dim() == 4:
+        NH = dy.shape[1]
+        NH, d = _heads_of(D, NH)
+        _activation("dy", dy, (B, NH, T, d), x)
+    else:
+        d = D
+        _activation("dy", dy, (B, T, D), x)
+    _contiguous("dstate_out", dstate_out, (B, W - 1, D), x)
+    with _launch(stream, x, weight, bias, state_in, dy, dstate_out) as s:
+        out = {"dx": torch.empty((B, T, D), dtype=x.dtype, device=x.device),
+               "dweight": torch.empty_like(weight),
+               "dbias": torch.empty_like(bias) if bias is not None else None,
+               "dstate_in": (torch.empty((B, W - 1, D), dtype=x.dtype, device=x.device)
+                             if want_dstate else None)}
+        ws = _bytes(load().mlstm_conv_bwd_workspace_size(B, T, NH, d, W, dt), x.device)
+        _check(load().mlstm_conv_bwd(_rows(x), weight.data_ptr(), _ptr(bias), _ptr(state_in),
+                                     _head_rows(dy, "heads" if dy.dim() == 4 else "last", d),
+                                     _ptr(dstate_out), _rows(out["dx"]), out["dweight"].data_ptr(),
+                                     _ptr(out["dbias"]), _ptr(out["dstate_in"]), ws.data_ptr(),
+                                     ws.numel(), B, T, NH, d, W, act, dt, s), "mlstm_conv_bwd")
+    return out
+
+
+def causal_conv_step(x, weight, bias, state, *, act=ACT_SILU, heads=None, stream=None):
+    """One token: x [B, D]; returns y [B, D] (with ``heads``: [B, heads, D / heads]) and updates
+    ``state`` [B, W - 1, D] in place."""
+    import torch
+    _dims("x", x, 2)
+    if state is None:
+        raise ValueError("state is required")
+    B, _, D, W, dt = _conv_args(x, weight, bias, state, act, 1)
+    NH, d = _heads_of(D, heads)
+    with _launch(stream, x, weight, bias, state) as s:
+        y = torch.empty((B, D) if heads is None else (B, NH, d), dtype=x.dtype, device=x.device)
+        _check(load().mlstm_conv_step(_rows(x), weight.data_ptr(), _ptr(bias), state.data_ptr(),
+                                      Rows(y.data_ptr(), D, 0, d), state.data_ptr(), B, NH, d, W, act,
+                                      dt, s), "mlstm_conv_step")
+    return y
+
+
+# --------------------------------------------------------------------------
+# selective state space scan
+# --------------------------------------------------------------------------
+
+def _scan_problem(x, dt, A, Bm, Cm, skip, z, dt_bias, softplus, state):
+    """mlstm_scan_t of a call on [B, T, D] tensors (or [B, D]: one token)."""
+    _activation("x", x, x.shape, x)
+    D = x.shape[-1]
+    _activation("dt", dt, x.shape, x)
+    if z is not None:
+        _activation("z", z, x.shape, x)
+    _dims("A", A, 2)
+    N = A.shape[1]
+    _fp32("A", A, (D, N), x)
+    _fp32("skip", skip, (D,), x)
+    _fp32("dt_bias", dt_bias, (D,), x)
+    lead = tuple(x.shape[:-1])
+    if Bm.dim() == x.dim() + 1:
+        G = Bm.shape[-2]
+        shape = (*lead, G, N)
+    else:
+        G = 1
+        shape = (*lead, N)
+    _activation("B", Bm, shape, x)
+    _activation("C", Cm, shape, x)
+    if G <= 0 or D % G:
+        raise ValueError(f"{G} groups do not divide {D} channels")
+    _fp32("state", state, (x.shape[0], D, N), x)
+    p = ScanProblem()
+    p.x, p.dt, p.z = _rows(x), _rows(dt), _rows(z)
+    p.b, p.c = _group_rows(Bm, x.dim(), G), _group_rows(Cm, x.dim(), G)
+    p.a, p.skip, p.dt_bias, p.state_in = A.data_ptr(), _ptr(skip), _ptr(dt_bias), _ptr(state)
+    p.B, p.T, p.D, p.G, p.N = x.shape[0], x.shape[1] if x.dim() == 3 else 1, D, G, N
+    p.softplus, p.dtype = int(bool(softplus)), _dtype_code(x)
+    return p
+
+
+def _group_rows(t, xdim, G):
+    """B or C: [B, T, N], [B, T, G, N], or one token of either."""
+    head = t.stride(-2) if t.dim() == xdim + 1 else 0
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1) if xdim == 3 else 0, head)
+
+
+def selective_scan_forward(x, dt, A, B, C, *, skip=None, z=None, dt_bias=None, softplus=True,
+                           state_in=None, keep_saved=True, want_state=False, stream=None):
+    """y = (sum_n C[n] s[n] + skip x) silu(z) with s[n] <- exp(delta A[n]) s[n] + delta x B[n] and
+    delta = softplus(dt + dt_bias); returns (y, saved, state_out).
+
+    x, dt, z [B, T, D]; A [D, N], up to 64 states; B, C [B, T, N], or [B, T, G, N] where each of G
+    groups of D / G channels has its own; skip, dt_bias [D]; state_in [B, D, N] (None: zeros).
+    ``saved`` is what the backward needs (None unless keep_saved); state_out [B, D, N] is None
+    unless want_state.
+    """
+    import torch
+    _dims("x", x, 3)
+    p = _scan_problem(x, dt, A, B, C, skip, z, dt_bias, softplus, state_in)
+    with _launch(stream, x, dt, A, B, C, skip, z, dt_bias, state_in) as s:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        saved = None
+        if keep_saved:
+            saved = _bytes(load().mlstm_scan_saved_size(p.B, p.T, p.D, p.G, p.N, p.dtype), x.device)
+        state_out = (torch.empty((p.B, p.D, p.N), dtype=torch.float32, device=x.device)
+                     if want_state else None)
+        _check(load().mlstm_scan_fwd(p, _rows(y), _ptr(saved), _ptr(state_out), s), "mlstm_scan_fwd")
+    return y, saved, state_out
+
+
+def selective_scan_backward(x, dt, A, B, C, dy, saved, *, skip=None, z=None, dt_bias=None,
+                            softplus=True, state_in=None, dstate_out=None, want_dstate=False,
+                            stream=None):
+    """Gradients of sum(dy y) + sum(dstate_out state_out): dict of dx, ddt, dA, dB, dC, dskip,
+    ddt_bias, dz and dstate_in (None where the input was not given, or not want_dstate)."""
+    import torch
+    _dims("x", x, 3)
+    p = _scan_problem(x, dt, A, B, C, skip, z, dt_bias, softplus, state_in)
+    _activation("dy", dy, x.shape, x)
+    _fp32("dstate_out", dstate_out, (p.B, p.D, p.N), x)
+    need = load().mlstm_scan_saved_size(p.B, p.T, p.D, p.G, p.N, p.dtype)
+    if saved is None or saved.device != x.device or saved.numel() * saved.element_size() < need:
+        raise ValueError(f"saved must hold the {need} bytes of the forward of the same inputs")
+    with _launch(stream, x, dt, A, B, C, skip, z, dt_bias, state_in, dy, saved, dstate_out) as s:
+        new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        out = {"dx": new(x), "ddt": new(x), "dA": new(A), "dB": new(B), "dC": new(C),
+               "dskip": new(skip) if skip is not None else None,
+               "ddt_bias": new(dt_bias) if dt_bias is not None else None,
+               "dz": new(x) if z is not None else None,
+               "dstate_in": (torch.empty((p.B, p.D, p.N), dtype=torch.float32, device=x.device)
+                             if want_dstate else None)}
+        g = ScanGrads()
+        g.dx, g.ddt, g.dz = _rows(out["dx"]), _rows(out["ddt"]), _rows(out["dz"])
+        g.db, g.dc = _group_rows(out["dB"], 3, p.G), _group_rows(out["dC"], 3, p.G)
+        g.da, g.dskip, g.ddt_bias = _ptr(out["dA"]), _ptr(out["dskip"]), _ptr(out["ddt_bias"])
+        g.dstate_in = _ptr(out["dstate_in"])
+        ws = _bytes(load().mlstm_scan_bwd_workspace_size(p.B, p.T, p.D, p.G, p.N, p.dtype), x.device)
+        _check(load().mlstm_scan_bwd(p, _rows(dy), saved.data_ptr(), _ptr(dstate_out), g, ws.data_ptr(),
+                                     ws.numel(), s), "mlstm_scan_bwd")
+    return out
+
+
+def selective_scan_step(x, dt, A, B, C, state, *, skip=None, z=None, dt_bias=None, softplus=True,
+                        stream=None):
+    """One token: x, dt, z [B, D]; B, C [B, N] or [B, G, N]; returns y [B, D] and updates ``state``
+    [B, D, N] in place."""
+    import torch
+    _dims("x", x, 2)
+    if state is None:
+        raise ValueError("state is required")
+    p = _scan_problem(x, dt, A, B, C, skip, z, dt_bias, softplus, state)
+    with _launch(stream, x, dt, A, B, C, skip, z, dt_bias, state) as s:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _check(load().mlstm_scan_step(p, _rows(y), state.data_ptr(), s), "mlstm_scan_step")
+    return y
+
+
+# --------------------------------------------------------------------------
+# group norm with an activation or an output gate
+# --------------------------------------------------------------------------
+
+def _norm_args(x, weight, bias, gate, act, scope, groups):
+    """(layout of x, B, T, NH, d) of a group norm call."""
+    if x.dim() == 4:
+        B, NH, T, d = x.shape
+        if groups is not None and groups != NH:
+            raise ValueError(f"x has {NH} heads, groups is {groups}")
+        layout = "heads"
+    else:
+        _dims("x", x, 3)
+        B, T, D = x.shape
+        if groups is None or groups <= 0 or D % groups:
+            raise ValueError(f"{groups} groups do not divide {D} channels")
+        NH, d = groups, D // groups
+        layout = "last"
+    _activation("x", x, x.shape, x)
+    _fp32("weight", weight, (NH * d,), x)
+    _fp32("bias", bias, (NH * d,), x)
+    if gate is not None:
+        _activation("gate", gate, (B, T, NH * d), x)
+    if act not in (ACT_NONE, ACT_SILU, ACT_SIGMOID):
+        raise ValueError("act must be ACT_NONE, ACT_SILU or ACT_SIGMOID")
+    if scope not in (SCOPE_TOKEN, SCOPE_SEQUENCE):
+        raise ValueError("scope must be SCOPE_TOKEN or SCOPE_SEQUENCE")
+    return layout, B, T, NH, d, _dtype_code(x)
+
+
+def _stats_shape(B, T, NH, scope):
+    return (B, T, NH, 2) if scope == SCOPE_TOKEN else (B, NH, 2)
+
+
+def group_norm_forward(x, weight=None, bias=None, *, gate=None, act=ACT_NONE, scope=SCOPE_TOKEN,
+                       groups=None, eps=1e-5, keep_stats=True, stream=None):
+    """Group norm, then the activation (or, with ``gate``, times the gate's activation).
+
+    x is head-major [B, NH, T, d], as the cell returns it (a group per head), or [B, T, C] with
+    ``groups``; weight, bias [NH d] or None; gate [B, T, NH d].  The mean and variance are over the d
+    channels of each token and group (SCOPE_TOKEN, d <= 512) or over all T tokens of the group
+    (SCOPE_SEQUENCE).  Returns (y [B, T, NH d], stats): stats are what the backward needs (None
+    unless keep_stats).
+    """
+    import torch
+    layout, B, T, NH, d, dt = _norm_args(x, weight, bias, gate, act, scope, groups)
+    with _launch(stream, x, weight, bias, gate) as s:
+        y = torch.empty((B, T, NH * d), dtype=x.dtype, device=x.device)
+        stats = (torch.empty(_stats_shape(B, T, NH, scope), dtype=torch.float32, device=x.device)
+                 if keep_stats else None)
+        need = load().mlstm_group_norm_workspace_size(B, T, NH, d, scope, dt, 0)
+        ws = _bytes(need, x.device) if need else None
+        _check(load().mlstm_group_norm_fwd(_head_rows(x, layout, d), _ptr(weight), _ptr(bias),
+                                           _head_rows(gate, "last", d), _head_rows(y, "last", d),
+                                           _ptr(stats), _ptr(ws), need, B, T, NH, d, scope, act, eps,
+                                           dt, s), "mlstm_group_norm_fwd")
+    return y, stats
+
+
+def group_norm_backward(x, weight, bias, dy, stats, *, gate=None, act=ACT_NONE, scope=SCOPE_TOKEN,
+                        groups=None, stream=None):
+    """Gradients of sum(dy y): dict of dx (laid out like x), dweight, dbias and dgate (None where
+    the input was not given)."""
+    import torch
+    layout, B, T, NH, d, dt = _norm_args(x, weight, bias, gate, act, scope, groups)
+    _activation("dy", dy, (B, T, NH * d), x)
+    if stats is None:
+        raise ValueError("stats of the forward are required")
+    _fp32("stats", stats, _stats_shape(B, T, NH, scope), x)
+    with _launch(stream, x, weight, bias, gate, dy, stats) as s:
+        new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        out = {"dx": new(x), "dweight": new(weight) if weight is not None else None,
+               "dbias": new(bias) if bias is not None else None,
+               "dgate": new(gate) if gate is not None else None}
+        need = load().mlstm_group_norm_workspace_size(B, T, NH, d, scope, dt, 1)
+        ws = _bytes(need, x.device) if need else None
+        _check(load().mlstm_group_norm_bwd(_head_rows(x, layout, d), _ptr(weight), _ptr(bias),
+                                           _head_rows(gate, "last", d), _head_rows(dy, "last", d),
+                                           stats.data_ptr(), _head_rows(out["dx"], layout, d),
+                                           _head_rows(out["dgate"], "last", d), _ptr(out["dweight"]),
+                                           _ptr(out["dbias"]), _ptr(ws), need, B, T, NH, d, scope, act,
+                                           dt, s), "mlstm_group_norm_bwd")
+    return out

@@ -1,0 +1,91 @@
+// Internal interfaces of the operators around the recurrence (block_api.cu to
+// conv.cu, scan_fwd.cu, scan_bwd.cu, group_norm.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mlstm {
+
+// A strided tensor, as mlstm_rows_t: element (b, t, g, j) at p[b sb + t st + g sh + j].
+struct Rows {
+  void* p = nullptr;
+  long long sb = 0, st = 0, sh = 0;
+};
+
+enum { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };
+
+// MLSTM_OK, or MLSTM_ERR_CUDA with the error's text kept for mlstm_last_error.
+int cuda_result(cudaError_t e, const char* where);
+
+// dw[c, j] = sum over rows of partial[row, j, c] for j < W, dbias[c] = that of j = W; partial is
+// [rows, W + 1, D].  Either output may be null.
+cudaError_t launch_param_sums(const float* partial, int rows, int D, int W, float* dw, float* dbias,
+                              cudaStream_t s);
+
+// ---- causal convolution ----------------------------------------------------
+struct ConvArgs {
+  Rows x, y;                    // y: dy in the backward
+  const float *w, *bias;        // [D, W], [D] or null
+  const void* state_in;         // [B, W - 1, D] or null
+  void* state_out;              // forward: or null
+  Rows dx;                      // backward
+  const void* dstate_out;       // backward: or null
+  void* dstate_in;              // backward: or null
+  float *dw, *dbias;            // backward; dbias or null
+  float* partial;               // backward: [conv_bwd_rows, W + 1, D]
+  int B, T, NH, d, W, act, dtype;
+  bool wide;                    // 16-byte accesses are possible everywhere
+  __host__ __device__ int D() const { return NH * d; }
+};
+int conv_bwd_rows(int B, int T, int D);  // rows of partial sums
+cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t s);
+cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s);
+cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t s);
+
+// ---- selective scan ----------------------------------------------------------
+struct ScanArgs {
+  Rows x, dt, z, b, c;          // z.p null: no gate
+  const float *A, *skip, *dt_bias;
+  const float* state_in;
+  Rows y;                       // forward output, or dy
+  float* state_out;
+  float* saved;                 // [B, ceil(T / 8), D, scan_pad(N)]; forward: or null
+  // backward
+  Rows dx, ddt, dz, db, dc;
+  float *dA, *dskip, *ddt_bias, *dstate_in;
+  const float* dstate_out;
+  float *part_bc, *part_a, *part_d;
+  int B, T, D, G, N, softplus, dtype;
+  bool wide, wide_bc;           // 16-byte accesses of the [B, T, D] tensors / of B and C
+};
+constexpr int kScanEvery = 8;  // tokens between two saved states
+// States per channel as the kernels hold them: four to a lane, 2, 4, 8 or 16 lanes to a channel.
+inline int scan_pad(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
+struct ScanBwdSizes {
+  int tiles;                    // channel tiles of one group
+  size_t part_bc, part_a, part_d;  // floats
+};
+ScanBwdSizes scan_bwd_sizes(int B, int T, int D, int G, int N);
+cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s);
+cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
+cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t s);
+
+// ---- group norm --------------------------------------------------------------
+struct NormArgs {
+  Rows x, gate, y;              // y: dy in the backward
+  Rows dx, dgate;
+  const float *w, *bias;        // [NH d] or null
+  float* stats;                 // (mean, rstd) pairs; forward: or null
+  float *dw, *dbias;            // or null
+  float* ws;
+  int B, T, NH, d, scope, act, dtype;
+  float eps;
+  bool wide;
+};
+size_t norm_workspace(int B, int T, int NH, int d, int scope, int dtype, bool backward);  // bytes
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s);
+
+}  // namespace mlstm

@@ -1,0 +1,633 @@
+// Group norm of channels-last (or head-major) activations with an activation or
+// an output gate, forward and backward.  With n = xhat w + bias over groups of d
+// channels, xhat = (x - mean) rstd:
+//
+//   y = act(n)  or  y = n act(gate)
+//   dn = dy act'(n)  or  dn = dy act(gate), dgate = dy n act'(gate)
+//   dx = rstd (dn w - mean(dn w) - xhat mean(dn w xhat))   means over what x's mean is over
+//   dw = sum dn xhat, dbias = sum dn                        over batches and tokens
+//
+// Bound by HBM.  Token scope (d <= 512, the widest head of the recurrence): 4 to 32 lanes hold
+// one (token, group) row in registers, so every tensor moves once.  Sequence scope: a first
+// pass writes each CTA's share of the sums and a second pass joins them and applies the norm.
+// Means and variances are joined as (count, mean, sum of squared distances), never as a
+// difference of squares.
+#include "block_common.cuh"
+
+namespace mlstm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSMs = 148;
+
+__device__ __forceinline__ float act_run(int act, float v) {
+  return act == kActSilu ? act_value<kActSilu>(v) : act == kActSigmoid ? act_value<kActSigmoid>(v) : v;
+}
+__device__ __forceinline__ void slope_run(int act, float v, float* value, float* slope) {
+  if (act == kActSilu)
+    act_slope<kActSilu>(v, value, slope);
+  else if (act == kActSigmoid)
+    act_slope<kActSigmoid>(v, value, slope);
+  else
+    act_slope<kActNone>(v, value, slope);
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Channels c .. c + n - 1 of the weight and bias (1 and 0 where there is none).
+template <bool WIDE>
+__device__ __forceinline__ void load_affine(const NormArgs& a, int c, int n, float* w, float* b) {
+  if (a.w != nullptr && n > 0)
+    load8<WIDE>(a.w + c, w, n);
+  else
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+  if (a.bias != nullptr && n > 0)
+    load8<WIDE>(a.bias + c, b, n);
+  else
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = 0.f;
+}
+
+// ---------------------------------------------------------------------------
+// Token scope: LANES lanes to a row, K vectors of eight channels to a lane
+// (LANES 8 K >= d).  A CTA stays with one head, so its weights stay in registers, and takes
+// every gridDim-th block of tokens; heads are the fastest grid dimension, so CTAs that run
+// together write neighbouring parts of the same tokens.
+// ---------------------------------------------------------------------------
+
+template <typename T, int LANES, int K, bool GATED, bool WIDE>
+__global__ void __launch_bounds__(kThreads) norm_token_fwd_kernel(NormArgs a, int blocks) {
+  constexpr int ROWS = kThreads / LANES;
+  const int head = blockIdx.x % a.NH, lane = threadIdx.x % LANES;
+  const int tokens = a.B * a.T, d = a.d;
+  int c[K], n[K];
+  float w[K][8], bias[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    c[k] = (k * LANES + lane) * 8;
+    n[k] = max(0, min(8, d - c[k]));
+    load_affine<WIDE>(a, head * d + c[k], n[k], w[k], bias[k]);
+  }
+  const float inv_d = 1.f / d;
+  // whole warps stay in the loop together: rows past the end repeat the last one unstored
+  for (int r0 = (blockIdx.x / a.NH) * ROWS; r0 < tokens; r0 += blocks * ROWS) {
+    const int r = r0 + threadIdx.x / LANES;
+    const bool live = r < tokens;
+    const int tok = live ? r : tokens - 1, b = tok / a.T, t = tok % a.T;
+    const T* x = (const T*)a.x.p + b * a.x.sb + t * a.x.st + head * a.x.sh;
+    float v[K][8], g[K][8], s = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (n[k] > 0) {
+        load8<WIDE>(x + c[k], v[k], n[k]);
+        if (GATED)
+          load8<WIDE>((const T*)a.gate.p + b * a.gate.sb + t * a.gate.st + head * a.gate.sh + c[k], g[k],
+                      n[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[k][i];
+    }
+    const float mean = lanes_sum<LANES>(s) * inv_d;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[k][i] -= mean;
+        if (WIDE ? n[k] > 0 : i < n[k]) s = fmaf(v[k][i], v[k][i], s);
+      }
+    const float rstd = rsqrtf(fmaf(lanes_sum<LANES>(s), inv_d, a.eps));
+    if (!live) continue;
+    T* y = (T*)a.y.p + b * a.y.sb + t * a.y.st + head * a.y.sh;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (n[k] > 0) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[i] = fmaf(v[k][i] * rstd, w[k][i], bias[k][i]);
+          if (GATED)
+            o[i] *= act_run(a.act, g[k][i]);
+          else
+            o[i] = act_run(a.act, o[i]);
+        }
+        store8<WIDE>(y + c[k], o, n[k]);
+      }
+    }
+    if (a.stats != nullptr && lane == 0)
+      reinterpret_cast<float2*>(a.stats)[(long long)tok * a.NH + head] = make_float2(mean, rstd);
+  }
+}
+
+// ws: rows of partial sums [blocks, 2, NH d] (dw, then dbias).
+template <typename T, int LANES, int K, bool GATED, bool WIDE>
+__global__ void __launch_bounds__(kThreads) norm_token_bwd_kernel(NormArgs a, int blocks) {
+  constexpr int ROWS = kThreads / LANES, CH = LANES * K * 8;
+  __shared__ float red[kThreads / 32][2][CH];
+  const int head = blockIdx.x % a.NH, block = blockIdx.x / a.NH, lane = threadIdx.x % LANES;
+  const int tokens = a.B * a.T, d = a.d;
+  int c[K], n[K];
+  float w[K][8], bias[K][8], dw[K][8], db[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    c[k] = (k * LANES + lane) * 8;
+    n[k] = max(0, min(8, d - c[k]));
+    load_affine<WIDE>(a, head * d + c[k], n[k], w[k], bias[k]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.f;
+  }
+  const float inv_d = 1.f / d;
+  for (int r0 = block * ROWS; r0 < tokens; r0 += blocks * ROWS) {
+    const int r = r0 + threadIdx.x / LANES;
+    const bool live = r < tokens;
+    const int tok = live ? r : tokens - 1, b = tok / a.T, t = tok % a.T;
+    const float2 ms = reinterpret_cast<const float2*>(a.stats)[(long long)tok * a.NH + head];
+    const T* x = (const T*)a.x.p + b * a.x.sb + t * a.x.st + head * a.x.sh;
+    const T* dy = (const T*)a.y.p + b * a.y.sb + t * a.y.st + head * a.y.sh;
+    const T* gp = GATED ? (const T*)a.gate.p + b * a.gate.sb + t * a.gate.st + head * a.gate.sh : nullptr;
+    float v[K][8], q[K][8], g[K][8], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (n[k] > 0) {
+        load8<WIDE>(x + c[k], v[k], n[k]);
+        load8<WIDE>(dy + c[k], q[k], n[k]);
+        if (GATED) load8<WIDE>(gp + c[k], g[k], n[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float dg[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (WIDE ? n[k] > 0 : i < n[k]) {
+          const float xh = (v[k][i] - ms.x) * ms.y, nn = fmaf(xh, w[k][i], bias[k][i]);
+          float val, slope, dn;
+          if (GATED) {
+            slope_run(a.act, g[k][i], &val, &slope);
+            dg[i] = q[k][i] * nn * slope;
+            dn = q[k][i] * val;
+          } else {
+            slope_run(a.act, nn, &val, &slope);
+            dn = q[k][i] * slope;
+          }
+          if (live) {
+            dw[k][i] = fmaf(dn, xh, dw[k][i]);
+            db[k][i] += dn;
+          }
+          const float dxh = dn * w[k][i];
+          s1 += dxh;
+          s2 = fmaf(dxh, xh, s2);
+          v[k][i] = xh;
+          q[k][i] = dxh;
+        }
+      }
+      if (GATED && live && n[k] > 0)
+        store8<WIDE>((T*)a.dgate.p + b * a.dgate.sb + t * a.dgate.st + head * a.dgate.sh + c[k], dg, n[k]);
+    }
+    const float m1 = lanes_sum<LANES>(s1) * inv_d, m2 = lanes_sum<LANES>(s2) * inv_d;
+    if (!live) continue;
+    T* dx = (T*)a.dx.p + b * a.dx.sb + t * a.dx.st + head * a.dx.sh;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (n[k] > 0) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = ms.y * (q[k][i] - m1 - v[k][i] * m2);
+        store8<WIDE>(dx + c[k], o, n[k]);
+      }
+    }
+  }
+  if (a.dw == nullptr && a.dbias == nullptr) return;
+  // the rows of a warp, then the warps, in a fixed order
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int o = LANES; o < 32; o <<= 1) {
+        dw[k][i] += __shfl_xor_sync(0xffffffffu, dw[k][i], o);
+        db[k][i] += __shfl_xor_sync(0xffffffffu, db[k][i], o);
+      }
+      if ((threadIdx.x & 31) < LANES) {
+        red[threadIdx.x / 32][0][c[k] + i] = dw[k][i];
+        red[threadIdx.x / 32][1][c[k] + i] = db[k][i];
+      }
+    }
+  __syncthreads();
+  const int D = a.NH * d;
+  for (int e = threadIdx.x; e < 2 * d; e += kThreads) {
+    const int p = e / d, ch = e % d;
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < kThreads / 32; ++q) s += red[q][p][ch];
+    a.ws[((long long)block * 2 + p) * D + head * d + ch] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sequence scope.  A CTA takes one slab of tokens and one block of up to 2048 channels of a
+// (batch, group): lanes along the channels, eight to a lane, and the CTA's other threads
+// along tokens.
+// ---------------------------------------------------------------------------
+
+struct Spread {
+  int lanes, rows;         // threads along channels / tokens of a CTA
+  int slab, slabs;         // tokens of a CTA, CTAs along a sequence
+  int cblocks;             // channel blocks of a group
+  __host__ __device__ int parts() const { return slabs * cblocks; }
+  long long ctas(int B, int NH) const { return (long long)B * NH * parts(); }
+};
+
+struct Cta {
+  int b, head, part, slab, c0, n, t0, t1;  // n channels from c0 for this thread (0: idle)
+  int row;                                   // thread's first token, relative to t0
+};
+
+__device__ __forceinline__ Cta cta_of(const NormArgs& a, const Spread& p) {
+  Cta q;
+  long long i = blockIdx.x;
+  q.head = (int)(i % a.NH); i /= a.NH;
+  q.part = (int)(i % p.parts());
+  q.b = (int)(i / p.parts());
+  q.slab = q.part / p.cblocks;
+  q.c0 = (q.part % p.cblocks) * p.lanes * 8 + (threadIdx.x % p.lanes) * 8;
+  q.n = max(0, min(8, a.d - q.c0));
+  q.t0 = q.slab * p.slab;
+  q.t1 = min(q.t0 + p.slab, a.T);
+  q.row = threadIdx.x / p.lanes;
+  return q;
+}
+
+// Offset of the thread's channels of token t in a strided tensor.
+__device__ __forceinline__ long long at(const Rows& r, const Cta& q, int t) {
+  return q.b * r.sb + t * r.st + q.head * r.sh + q.c0;
+}
+
+// Joins (count, mean, m2) pairs: Chan, Golub and LeVeque's pairwise update.
+template <typename F>
+__device__ __forceinline__ void join(F& n, F& mean, F& m2, F nb, F meanb, F m2b) {
+  const F tot = n + nb;
+  if (tot == F(0)) return;
+  const F d = meanb - mean, f = nb / tot;
+  mean += d * f;
+  m2 += m2b + d * d * n * f;
+  n = tot;
+}
+
+// Pass 1 of the forward: each CTA's (count, mean, m2) to ws[batch, head, part].
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kThreads) norm_stats_kernel(NormArgs a, Spread p) {
+  const Cta q = cta_of(a, p);
+  float cnt = 0.f, mean = 0.f, m2 = 0.f;
+  if (q.n > 0) {
+    const T* x = (const T*)a.x.p;
+    const float len = (float)q.n, inv = 1.f / len;
+#pragma unroll 4
+    for (int t = q.t0 + q.row; t < q.t1; t += p.rows) {
+      float v[8], s = 0.f, e = 0.f;
+      load8<WIDE>(x + at(a.x, q, t), v, q.n);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+      s *= inv;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (WIDE || i < q.n) e = fmaf(v[i] - s, v[i] - s, e);
+      join(cnt, mean, m2, len, s, e);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float nb = __shfl_down_sync(0xffffffffu, cnt, o), mb = __shfl_down_sync(0xffffffffu, mean, o),
+                sb = __shfl_down_sync(0xffffffffu, m2, o);
+    join(cnt, mean, m2, nb, mb, sb);
+  }
+  __shared__ float red[kThreads / 32][3];
+  if ((threadIdx.x & 31) == 0) {
+    red[threadIdx.x / 32][0] = cnt;
+    red[threadIdx.x / 32][1] = mean;
+    red[threadIdx.x / 32][2] = m2;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kThreads / 32; ++w) join(cnt, mean, m2, red[w][0], red[w][1], red[w][2]);
+    float* o = a.ws + (((long long)q.b * a.NH + q.head) * p.parts() + q.part) * 3;
+    o[0] = cnt;
+    o[1] = mean;
+    o[2] = m2;
+  }
+}
+
+// Pass 2 of the forward: join the parts (every CTA for itself, in fp64), apply.
+template <typename T, bool GATED, bool WIDE>
+__global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs a, Spread p) {
+  const Cta q = cta_of(a, p);
+  __shared__ float sh[2];
+  const long long group = (long long)q.b * a.NH + q.head;
+  if (threadIdx.x < 32) {
+    double cnt = 0, mean = 0, m2 = 0;
+    const float* w = a.ws + group * p.parts() * 3;
+    for (int i = threadIdx.x; i < p.parts(); i += 32)
+      join(cnt, mean, m2, (double)w[3 * i], (double)w[3 * i + 1], (double)w[3 * i + 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double nb = __shfl_down_sync(0xffffffffu, cnt, o), mb = __shfl_down_sync(0xffffffffu, mean, o),
+                   sb = __shfl_down_sync(0xffffffffu, m2, o);
+      join(cnt, mean, m2, nb, mb, sb);
+    }
+    if (threadIdx.x == 0) {
+      sh[0] = (float)mean;
+      sh[1] = (float)(1.0 / sqrt(m2 / cnt + (double)a.eps));
+      if (a.stats != nullptr && q.part == 0)
+        reinterpret_cast<float2*>(a.stats)[group] = make_float2(sh[0], sh[1]);
+    }
+  }
+  __syncthreads();
+  if (q.n == 0) return;
+  const float mean = sh[0], rstd = sh[1];
+  float w[8], bias[8];
+  load_affine<WIDE>(a, q.head * a.d + q.c0, q.n, w, bias);
+  const T* x = (const T*)a.x.p;
+#pragma unroll 4
+  for (int t = q.t0 + q.row; t < q.t1; t += p.rows) {
+    float v[8], g[8];
+    load8<WIDE>(x + at(a.x, q, t), v, q.n);
+    if (GATED) load8<WIDE>((const T*)a.gate.p + at(a.gate, q, t), g, q.n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = fmaf((v[i] - mean) * rstd, w[i], bias[i]);
+      if (GATED)
+        v[i] *= act_run(a.act, g[i]);
+      else
+        v[i] = act_run(a.act, v[i]);
+    }
+    store8<WIDE>((T*)a.y.p + at(a.y, q, t), v, q.n);
+  }
+}
+
+// What one vector contributes to the backward: dxh = dn w into q, xhat into v, dgate into g.
+template <bool GATED, bool WIDE>
+__device__ __forceinline__ void dxhat8(const NormArgs& a, float mean, float rstd, const float* w,
+                                       const float* bias, float* v, float* q, float* g, float* dn) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float xh = (v[i] - mean) * rstd, nn = fmaf(xh, w[i], bias[i]);
+    float val, slope;
+    if (GATED) {
+      slope_run(a.act, g[i], &val, &slope);
+      g[i] = q[i] * nn * slope;
+      dn[i] = q[i] * val;
+    } else {
+      slope_run(a.act, nn, &val, &slope);
+      dn[i] = q[i] * slope;
+    }
+    v[i] = xh;
+    q[i] = dn[i] * w[i];
+  }
+}
+
+// Pass 1 of the backward: sums of dxh and dxh xhat to ws[batch, head, part, 2], and each
+// channel's sums of dn xhat and dn to the rows [batch slabs, 2, NH d] behind them.
+template <typename T, bool GATED, bool WIDE>
+__global__ void __launch_bounds__(kThreads) norm_dsums_kernel(NormArgs a, Spread p, float* param) {
+  extern __shared__ float cols[];  // [rows][2][lanes][8]
+  const Cta q = cta_of(a, p);
+  const long long group = (long long)q.b * a.NH + q.head;
+  float s1 = 0.f, s2 = 0.f, dw[8], db[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.f;
+  if (q.n > 0) {
+    const float2 ms = reinterpret_cast<const float2*>(a.stats)[group];
+    float w[8], bias[8];
+    load_affine<WIDE>(a, q.head * a.d + q.c0, q.n, w, bias);
+#pragma unroll 2
+    for (int t = q.t0 + q.row; t < q.t1; t += p.rows) {
+      float v[8], r[8], g[8], dn[8];
+      load8<WIDE>((const T*)a.x.p + at(a.x, q, t), v, q.n);
+      load8<WIDE>((const T*)a.y.p + at(a.y, q, t), r, q.n);
+      if (GATED) load8<WIDE>((const T*)a.gate.p + at(a.gate, q, t), g, q.n);
+      dxhat8<GATED, WIDE>(a, ms.x, ms.y, w, bias, v, r, g, dn);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (WIDE || i < q.n) {
+          s1 += r[i];
+          s2 = fmaf(r[i], v[i], s2);
+          dw[i] = fmaf(dn[i], v[i], dw[i]);
+          db[i] += dn[i];
+        }
+    }
+  }
+  const int lane = threadIdx.x % p.lanes;
+  if (param != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cols[((q.row * 2 + 0) * p.lanes + lane) * 8 + i] = dw[i];
+      cols[((q.row * 2 + 1) * p.lanes + lane) * 8 + i] = db[i];
+    }
+  }
+  __shared__ float red[kThreads / 32][2];
+  s1 = warp_sum(s1);
+  s2 = warp_sum(s2);
+  if ((threadIdx.x & 31) == 0) {
+    red[threadIdx.x / 32][0] = s1;
+    red[threadIdx.x / 32][1] = s2;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    float s = 0.f;
+    for (int w = 0; w < kThreads / 32; ++w) s += red[w][threadIdx.x];
+    a.ws[(group * p.parts() + q.part) * 2 + threadIdx.x] = s;
+  }
+  if (param != nullptr) {
+    const int cb = (q.part % p.cblocks) * p.lanes * 8, width = p.lanes * 8, D = a.NH * a.d;
+    float* out = param + ((long long)q.b * p.slabs + q.slab) * 2 * D + q.head * a.d + cb;
+    for (int e = threadIdx.x; e < 2 * width; e += kThreads) {
+      const int which = e / width, c = e % width;
+      if (cb + c < a.d) {
+        float s = 0.f;
+        for (int r = 0; r < p.rows; ++r) s += cols[(r * 2 + which) * width + c];
+        out[(long long)which * D + c] = s;
+      }
+    }
+  }
+}
+
+// Pass 2 of the backward.
+template <typename T, bool GATED, bool WIDE>
+__global__ void __launch_bounds__(kThreads) norm_dx_kernel(NormArgs a, Spread p) {
+  const Cta q = cta_of(a, p);
+  __shared__ float sh[2];
+  const long long group = (long long)q.b * a.NH + q.head;
+  if (threadIdx.x < 32) {
+    double s1 = 0, s2 = 0;
+    const float* w = a.ws + group * p.parts() * 2;
+    for (int i = threadIdx.x; i < p.parts(); i += 32) {
+      s1 += w[2 * i];
+      s2 += w[2 * i + 1];
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (threadIdx.x == 0) {
+      const double inv = 1.0 / ((double)a.T * a.d);
+      sh[0] = (float)(s1 * inv);
+      sh[1] = (float)(s2 * inv);
+    }
+  }
+  __syncthreads();
+  if (q.n == 0) return;
+  const float m1 = sh[0], m2 = sh[1];
+  const float2 ms = reinterpret_cast<const float2*>(a.stats)[group];
+  float w[8], bias[8];
+  load_affine<WIDE>(a, q.head * a.d + q.c0, q.n, w, bias);
+#pragma unroll 2
+  for (int t = q.t0 + q.row; t < q.t1; t += p.rows) {
+    float v[8], r[8], g[8], dn[8];
+    load8<WIDE>((const T*)a.x.p + at(a.x, q, t), v, q.n);
+    load8<WIDE>((const T*)a.y.p + at(a.y, q, t), r, q.n);
+    if (GATED) load8<WIDE>((const T*)a.gate.p + at(a.gate, q, t), g, q.n);
+    dxhat8<GATED, WIDE>(a, ms.x, ms.y, w, bias, v, r, g, dn);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = ms.y * (r[i] - m1 - v[i] * m2);
+    store8<WIDE>((T*)a.dx.p + at(a.dx, q, t), r, q.n);
+    if (GATED) store8<WIDE>((T*)a.dgate.p + at(a.dgate, q, t), g, q.n);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+int lanes_for(int d) {
+  const int v = (d + 7) / 8;
+  return v <= 4 ? 4 : v <= 8 ? 8 : v <= 16 ? 16 : 32;
+}
+
+// Token blocks of the token-scope kernels: enough CTAs for `waves` per SM, no more than rows need.
+int token_blocks(long long tokens, int NH, int d, int waves) {
+  const int rows = kThreads / lanes_for(d);
+  const long long need = (tokens + rows - 1) / rows;
+  const long long want = ((long long)kSMs * waves + NH - 1) / NH;
+  return (int)(need < want ? need : want);
+}
+constexpr int kFwdWaves = 16, kBwdWaves = 6;
+
+Spread spread_for(int B, int T, int NH, int d) {
+  Spread p;
+  const int v = (d + 7) / 8;
+  p.lanes = 1;
+  while (p.lanes < v && p.lanes < kThreads) p.lanes *= 2;
+  p.rows = kThreads / p.lanes;
+  p.cblocks = (v + p.lanes - 1) / p.lanes;
+  // Slabs of at least 8 tokens to a thread, more where that already gives 16 CTAs per SM.
+  const long long groups = (long long)B * NH * p.cblocks;
+  long long slabs = ((long long)kSMs * 16 + groups - 1) / groups;
+  const long long most = (T + p.rows * 8 - 1) / (p.rows * 8);
+  if (slabs > most) slabs = most;
+  if (slabs < 1) slabs = 1;
+  p.slab = (int)((T + slabs - 1) / slabs);
+  p.slabs = (T + p.slab - 1) / p.slab;
+  return p;
+}
+
+template <typename T, int LANES, int K>
+cudaError_t token_fwd(const NormArgs& a, cudaStream_t s) {
+  const int blocks = token_blocks((long long)a.B * a.T, a.NH, a.d, kFwdWaves);
+  const unsigned grid = (unsigned)blocks * a.NH;
+  if (a.gate.p != nullptr) {
+    if (a.wide) norm_token_fwd_kernel<T, LANES, K, true, true><<<grid, kThreads, 0, s>>>(a, blocks);
+    else norm_token_fwd_kernel<T, LANES, K, true, false><<<grid, kThreads, 0, s>>>(a, blocks);
+  } else {
+    if (a.wide) norm_token_fwd_kernel<T, LANES, K, false, true><<<grid, kThreads, 0, s>>>(a, blocks);
+    else norm_token_fwd_kernel<T, LANES, K, false, false><<<grid, kThreads, 0, s>>>(a, blocks);
+  }
+  return cudaGetLastError();
+}
+template <typename T, int LANES, int K>
+cudaError_t token_bwd(const NormArgs& a, cudaStream_t s) {
+  const int blocks = token_blocks((long long)a.B * a.T, a.NH, a.d, kBwdWaves);
+  const unsigned grid = (unsigned)blocks * a.NH;
+  if (a.gate.p != nullptr) {
+    if (a.wide) norm_token_bwd_kernel<T, LANES, K, true, true><<<grid, kThreads, 0, s>>>(a, blocks);
+    else norm_token_bwd_kernel<T, LANES, K, true, false><<<grid, kThreads, 0, s>>>(a, blocks);
+  } else {
+    if (a.wide) norm_token_bwd_kernel<T, LANES, K, false, true><<<grid, kThreads, 0, s>>>(a, blocks);
+    else norm_token_bwd_kernel<T, LANES, K, false, false><<<grid, kThreads, 0, s>>>(a, blocks);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || (a.dw == nullptr && a.dbias == nullptr)) return e;
+  return launch_param_sums(a.ws, blocks, a.NH * a.d, 1, a.dw, a.dbias, s);
+}
+template <typename T, bool BWD>
+cudaError_t by_lanes(const NormArgs& a, cudaStream_t s) {
+  const int lanes = lanes_for(a.d);
+  if (lanes == 4) return BWD ? token_bwd<T, 4, 1>(a, s) : token_fwd<T, 4, 1>(a, s);
+  if (lanes == 8) return BWD ? token_bwd<T, 8, 1>(a, s) : token_fwd<T, 8, 1>(a, s);
+  if (lanes == 16) return BWD ? token_bwd<T, 16, 1>(a, s) : token_fwd<T, 16, 1>(a, s);
+  if (a.d <= 256) return BWD ? token_bwd<T, 32, 1>(a, s) : token_fwd<T, 32, 1>(a, s);
+  return BWD ? token_bwd<T, 32, 2>(a, s) : token_fwd<T, 32, 2>(a, s);
+}
+
+template <typename T, bool GATED, bool WIDE>
+cudaError_t spread_fwd(const NormArgs& a, cudaStream_t s) {
+  const Spread p = spread_for(a.B, a.T, a.NH, a.d);
+  const unsigned grid = (unsigned)p.ctas(a.B, a.NH);
+  norm_stats_kernel<T, WIDE><<<grid, kThreads, 0, s>>>(a, p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  norm_apply_kernel<T, GATED, WIDE><<<grid, kThreads, 0, s>>>(a, p);
+  return cudaGetLastError();
+}
+template <typename T, bool GATED, bool WIDE>
+cudaError_t spread_bwd(const NormArgs& a, cudaStream_t s) {
+  const Spread p = spread_for(a.B, a.T, a.NH, a.d);
+  const unsigned grid = (unsigned)p.ctas(a.B, a.NH);
+  const bool params = a.dw != nullptr || a.dbias != nullptr;
+  float* rows = params ? a.ws + p.ctas(a.B, a.NH) * 2 : nullptr;
+  norm_dsums_kernel<T, GATED, WIDE><<<grid, kThreads, kThreads * 16 * sizeof(float), s>>>(a, p, rows);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  norm_dx_kernel<T, GATED, WIDE><<<grid, kThreads, 0, s>>>(a, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !params) return e;
+  return launch_param_sums(rows, a.B * p.slabs, a.NH * a.d, 1, a.dw, a.dbias, s);
+}
+template <typename T, bool BWD>
+cudaError_t spread_pass(const NormArgs& a, cudaStream_t s) {
+  if (a.gate.p != nullptr) {
+    if (a.wide) return BWD ? spread_bwd<T, true, true>(a, s) : spread_fwd<T, true, true>(a, s);
+    return BWD ? spread_bwd<T, true, false>(a, s) : spread_fwd<T, true, false>(a, s);
+  }
+  if (a.wide) return BWD ? spread_bwd<T, false, true>(a, s) : spread_fwd<T, false, true>(a, s);
+  return BWD ? spread_bwd<T, false, false>(a, s) : spread_fwd<T, false, false>(a, s);
+}
+template <bool BWD>
+cudaError_t norm_pass(const NormArgs& a, cudaStream_t s) {
+  if (a.scope == 0)
+    return a.dtype == 0 ? by_lanes<bf16, BWD>(a, s) : by_lanes<float, BWD>(a, s);
+  return a.dtype == 0 ? spread_pass<bf16, BWD>(a, s) : spread_pass<float, BWD>(a, s);
+}
+
+}  // namespace
+
+size_t norm_workspace(int B, int T, int NH, int d, int scope, int, bool backward) {
+  const size_t D = (size_t)NH * d;
+  if (scope == 0)
+    return backward ? (size_t)token_blocks((long long)B * T, NH, d, kBwdWaves) * 2 * D * 4 : 0;
+  const Spread p = spread_for(B, T, NH, d);
+  if (!backward) return (size_t)p.ctas(B, NH) * 3 * 4;
+  return ((size_t)p.ctas(B, NH) * 2 + (size_t)B * p.slabs * 2 * D) * 4;
+}
+
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) { return norm_pass<false>(a, s); }
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s) { return norm_pass<true>(a, s); }
+
+}  // namespace mlstm

@@ -8,6 +8,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "block.h"
 #include "internal.h"
 #include "mlstm.h"
 
@@ -302,6 +303,8 @@ int run_plan(const Step* steps, int n, const Problem& p, const Args& a, cudaStre
 }  // namespace
 
 namespace mlstm {
+
+int cuda_result(cudaError_t e, const char* where) { return cuda_status(e, where); }
 
 unsigned int next_epoch() {
   static std::atomic<unsigned int> counter{0};
