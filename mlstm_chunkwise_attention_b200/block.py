@@ -13,8 +13,7 @@ their gradients and the scan's states are float32.  Work is enqueued on the curr
 tensors' device, or on ``stream``: outputs and workspaces are then allocated for that stream.
 """
 
-import contextlib
-import ctypes
+import struct
 
 from .binding import (
     BF16, FP32, STATUS_OK, STATUS_UNSUPPORTED, MLSTMError, Rows, ScanGrads, ScanProblem, load)
@@ -41,16 +40,18 @@ def _dtype_code(t):
 
 def _activation(name, t, shape, like):
     """An activation of `like`'s dtype and device, last dimension contiguous, of this shape."""
+    if (t.shape == shape and t.dtype == like.dtype and t.get_device() == like.get_device() and t.is_cuda
+            and (t.stride(-1) == 1 or shape[-1] <= 1)):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
     if t.dtype != like.dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
+    raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
 def _fp32(name, t, shape, like):
@@ -58,16 +59,18 @@ def _fp32(name, t, shape, like):
     import torch
     if t is None:
         return
+    if (t.shape == shape and t.dtype == torch.float32 and t.get_device() == like.get_device()
+            and t.is_cuda and t.is_contiguous()):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} has dtype {t.dtype}, expected float32")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _contiguous(name, t, shape, like):
@@ -95,35 +98,31 @@ def _rows(t):
 
 
 def _head_rows(t, layout, d):
-    """A tensor by heads: [B, NH, T, d] ("heads"), [B, T, NH, d] or [B, T, NH d] ("last"), or one
-    token, [B, NH, d] / [B, NH d]."""
+    """A tensor by heads: [B, NH, T, d] ("heads") or [B, T, NH d] ("last")."""
     if t is None:
         return Rows(None, 0, 0, 0)
-    if layout == "heads":
-        return Rows(t.data_ptr(), t.stride(0), t.stride(2) if t.dim() == 4 else 0, t.stride(1))
-    head = t.stride(2) if t.dim() == 4 else d
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1), head)
+    sb, s1, s2 = t.stride()[:3]
+    return Rows(t.data_ptr(), sb, s2, s1) if layout == "heads" else Rows(t.data_ptr(), sb, s1, d)
 
 
-@contextlib.contextmanager
-def _launch(stream, like, *tensors):
-    """The stream handle to launch on, with `like`'s device current.  With an explicit stream,
-    allocations inside belong to it, and the inputs are kept from reuse until its work is done."""
+def _on(stream, like, tensors, launch):
+    """launch(stream handle), with `like`'s device current.  With an explicit stream, what launch
+    allocates belongs to that stream, and the inputs are kept from reuse until its work is done."""
     import torch
-    with contextlib.ExitStack() as stack:
-        if like.device.index != torch.cuda.current_device():
-            stack.enter_context(torch.cuda.device(like.device))
+    device = like.get_device()
+    if stream is None and device == torch.cuda.current_device():
+        # the handle of torch.cuda.current_stream() without building a Stream (3 us of a 15 us call)
+        return launch(torch._C._cuda_getCurrentRawStream(device))
+    if stream is not None and stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, tensors on {like.device}")
+    with torch.cuda.device(device):
         if stream is None:
-            s = torch.cuda.current_stream()
-        else:
-            if stream.device != like.device:
-                raise ValueError(f"stream is on {stream.device}, tensors on {like.device}")
-            s = stream
-            stack.enter_context(torch.cuda.stream(s))
+            return launch(torch._C._cuda_getCurrentRawStream(device))
+        with torch.cuda.stream(stream):
             for t in (like, *tensors):
                 if t is not None:
-                    t.record_stream(s)
-        yield ctypes.c_void_p(s.cuda_stream)
+                    t.record_stream(stream)
+            return launch(stream.cuda_stream)
 
 
 def _check(status, where):
@@ -131,9 +130,9 @@ def _check(status, where):
         raise MLSTMError(status, where)
 
 
-def _bytes(n, device):
+def _bytes(n, like):
     import torch
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    return like.new_empty(max(n, 16), dtype=torch.uint8)
 
 
 # --------------------------------------------------------------------------
@@ -172,18 +171,19 @@ def causal_conv_forward(x, weight, bias=None, *, act=ACT_SILU, state_in=None, wa
     ``heads`` head-major, [B, heads, T, D / heads].  state_out: the last W - 1 inputs, for a later
     call or ``causal_conv_step`` (None unless want_state).
     """
-    import torch
     _dims("x", x, 3)
     B, T, D, W, dt = _conv_args(x, weight, bias, state_in, act, x.shape[1])
     NH, d = _heads_of(D, heads)
-    with _launch(stream, x, weight, bias, state_in) as s:
-        y = torch.empty((B, T, D) if heads is None else (B, NH, T, d), dtype=x.dtype, device=x.device)
-        state_out = (torch.empty((B, W - 1, D), dtype=x.dtype, device=x.device) if want_state
-                     else None)
+
+    def launch(s):
+        y = x.new_empty((B, T, D) if heads is None else (B, NH, T, d))
+        state_out = x.new_empty((B, W - 1, D)) if want_state else None
         _check(load().mlstm_conv_fwd(_rows(x), weight.data_ptr(), _ptr(bias), _ptr(state_in),
                                      _head_rows(y, "last" if heads is None else "heads", d),
                                      _ptr(state_out), B, T, NH, d, W, act, dt, s), "mlstm_conv_fwd")
-    return y, state_out
+        return y, state_out
+
+    return _on(stream, x, (weight, bias, state_in), launch)
 
 
 def causal_conv_backward(x, weight, bias, dy, *, act=ACT_SILU, state_in=None, dstate_out=None,
@@ -191,53 +191,58 @@ def causal_conv_backward(x, weight, bias, dy, *, act=ACT_SILU, state_in=None, ds
     """Gradients of sum(dy y) + sum(dstate_out state_out): dict of dx [B, T, D], dweight, dbias
     (None without a bias) and dstate_in (None unless want_dstate).  dy is laid out like the
     forward's y: [B, T, D], or head-major [B, NH, T, d]."""
-    import torch
     _dims("x", x, 3)
     B, T, D, W, dt = _conv_args(x, weight, bias, state_in, act, x.shape[1])
-    NH = 1
+    NH, d, layout = 1, D, "last"
     if dy.dim() == 4:
-        NH = dy.shape[1]
-        NH, d = _heads_of(D, NH)
-        _activation("dy", dy, (B, NH, T, d), x)
-    else:
-        d = D
-        _activation("dy", dy, (B, T, D), x)
+        NH, d = _heads_of(D, dy.shape[1])
+        layout = "heads"
+    _activation("dy", dy, (B, NH, T, d) if layout == "heads" else (B, T, D), x)
     _contiguous("dstate_out", dstate_out, (B, W - 1, D), x)
-    with _launch(stream, x, weight, bias, state_in, dy, dstate_out) as s:
-        out = {"dx": torch.empty((B, T, D), dtype=x.dtype, device=x.device),
-               "dweight": torch.empty_like(weight),
-               "dbias": torch.empty_like(bias) if bias is not None else None,
-               "dstate_in": (torch.empty((B, W - 1, D), dtype=x.dtype, device=x.device)
-                             if want_dstate else None)}
-        ws = _bytes(load().mlstm_conv_bwd_workspace_size(B, T, NH, d, W, dt), x.device)
+
+    def launch(s):
+        out = {"dx": x.new_empty((B, T, D)), "dweight": weight.new_empty((D, W)),
+               "dbias": bias.new_empty((D,)) if bias is not None else None,
+               "dstate_in": x.new_empty((B, W - 1, D)) if want_dstate else None}
+        ws = _bytes(load().mlstm_conv_bwd_workspace_size(B, T, NH, d, W, dt), x)
         _check(load().mlstm_conv_bwd(_rows(x), weight.data_ptr(), _ptr(bias), _ptr(state_in),
-                                     _head_rows(dy, "heads" if dy.dim() == 4 else "last", d),
-                                     _ptr(dstate_out), _rows(out["dx"]), out["dweight"].data_ptr(),
-                                     _ptr(out["dbias"]), _ptr(out["dstate_in"]), ws.data_ptr(),
-                                     ws.numel(), B, T, NH, d, W, act, dt, s), "mlstm_conv_bwd")
-    return out
+                                     _head_rows(dy, layout, d), _ptr(dstate_out), _rows(out["dx"]),
+                                     out["dweight"].data_ptr(), _ptr(out["dbias"]),
+                                     _ptr(out["dstate_in"]), ws.data_ptr(), ws.numel(), B, T, NH, d, W,
+                                     act, dt, s), "mlstm_conv_bwd")
+        return out
+
+    return _on(stream, x, (weight, bias, state_in, dy, dstate_out), launch)
 
 
 def causal_conv_step(x, weight, bias, state, *, act=ACT_SILU, heads=None, stream=None):
     """One token: x [B, D]; returns y [B, D] (with ``heads``: [B, heads, D / heads]) and updates
     ``state`` [B, W - 1, D] in place."""
-    import torch
     _dims("x", x, 2)
     if state is None:
         raise ValueError("state is required")
     B, _, D, W, dt = _conv_args(x, weight, bias, state, act, 1)
     NH, d = _heads_of(D, heads)
-    with _launch(stream, x, weight, bias, state) as s:
-        y = torch.empty((B, D) if heads is None else (B, NH, d), dtype=x.dtype, device=x.device)
-        _check(load().mlstm_conv_step(_rows(x), weight.data_ptr(), _ptr(bias), state.data_ptr(),
-                                      Rows(y.data_ptr(), D, 0, d), state.data_ptr(), B, NH, d, W, act,
-                                      dt, s), "mlstm_conv_step")
-    return y
+
+    def launch(s):
+        y = x.new_empty((B, D) if heads is None else (B, NH, d))
+        at = state.data_ptr()
+        _check(load().mlstm_conv_step(_rows(x), weight.data_ptr(), _ptr(bias), at,
+                                      Rows(y.data_ptr(), D, 0, d), at, B, NH, d, W, act, dt, s),
+               "mlstm_conv_step")
+        return y
+
+    return _on(stream, x, (weight, bias, state), launch)
 
 
 # --------------------------------------------------------------------------
 # selective state space scan
 # --------------------------------------------------------------------------
+
+#: mlstm_scan_t: five mlstm_rows_t, four pointers, seven ints (packed at once: a field at a time
+#: costs five times as long)
+_SCAN_PROBLEM = struct.Struct("@20q4q7i4x")
+
 
 def _scan_problem(x, dt, A, Bm, Cm, skip, z, dt_bias, softplus, state):
     """mlstm_scan_t of a call on [B, T, D] tensors (or [B, D]: one token)."""
@@ -263,19 +268,16 @@ def _scan_problem(x, dt, A, Bm, Cm, skip, z, dt_bias, softplus, state):
     if G <= 0 or D % G:
         raise ValueError(f"{G} groups do not divide {D} channels")
     _fp32("state", state, (x.shape[0], D, N), x)
-    p = ScanProblem()
-    p.x, p.dt, p.z = _rows(x), _rows(dt), _rows(z)
-    p.b, p.c = _group_rows(Bm, x.dim(), G), _group_rows(Cm, x.dim(), G)
-    p.a, p.skip, p.dt_bias, p.state_in = A.data_ptr(), _ptr(skip), _ptr(dt_bias), _ptr(state)
-    p.B, p.T, p.D, p.G, p.N = x.shape[0], x.shape[1] if x.dim() == 3 else 1, D, G, N
-    p.softplus, p.dtype = int(bool(softplus)), _dtype_code(x)
-    return p
-
-
-def _group_rows(t, xdim, G):
-    """B or C: [B, T, N], [B, T, G, N], or one token of either."""
-    head = t.stride(-2) if t.dim() == xdim + 1 else 0
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1) if xdim == 3 else 0, head)
+    token = x.dim() == 3
+    st = x.stride(1) if token else 0
+    bst, cst = (Bm.stride(1), Cm.stride(1)) if token else (0, 0)
+    bsh, csh = (Bm.stride(-2), Cm.stride(-2)) if Bm.dim() == x.dim() + 1 else (0, 0)
+    zp, zsb, zst = (0, 0, 0) if z is None else (z.data_ptr(), z.stride(0), z.stride(1) if token else 0)
+    return ScanProblem.from_buffer_copy(_SCAN_PROBLEM.pack(
+        x.data_ptr(), x.stride(0), st, 0, dt.data_ptr(), dt.stride(0), dt.stride(1) if token else 0, 0,
+        zp, zsb, zst, 0, Bm.data_ptr(), Bm.stride(0), bst, bsh, Cm.data_ptr(), Cm.stride(0), cst, csh,
+        A.data_ptr(), _ptr(skip) or 0, _ptr(dt_bias) or 0, _ptr(state) or 0,
+        x.shape[0], x.shape[1] if token else 1, D, G, N, 1 if softplus else 0, _dtype_code(x)))
 
 
 def selective_scan_forward(x, dt, A, B, C, *, skip=None, z=None, dt_bias=None, softplus=True,
@@ -291,15 +293,16 @@ def selective_scan_forward(x, dt, A, B, C, *, skip=None, z=None, dt_bias=None, s
     import torch
     _dims("x", x, 3)
     p = _scan_problem(x, dt, A, B, C, skip, z, dt_bias, softplus, state_in)
-    with _launch(stream, x, dt, A, B, C, skip, z, dt_bias, state_in) as s:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        saved = None
-        if keep_saved:
-            saved = _bytes(load().mlstm_scan_saved_size(p.B, p.T, p.D, p.G, p.N, p.dtype), x.device)
-        state_out = (torch.empty((p.B, p.D, p.N), dtype=torch.float32, device=x.device)
-                     if want_state else None)
+
+    def launch(s):
+        y = x.new_empty(x.shape)
+        saved = (_bytes(load().mlstm_scan_saved_size(p.B, p.T, p.D, p.G, p.N, p.dtype), x)
+                 if keep_saved else None)
+        state_out = x.new_empty((p.B, p.D, p.N), dtype=torch.float32) if want_state else None
         _check(load().mlstm_scan_fwd(p, _rows(y), _ptr(saved), _ptr(state_out), s), "mlstm_scan_fwd")
-    return y, saved, state_out
+        return y, saved, state_out
+
+    return _on(stream, x, (dt, A, B, C, skip, z, dt_bias, state_in), launch)
 
 
 def selective_scan_backward(x, dt, A, B, C, dy, saved, *, skip=None, z=None, dt_bias=None,
@@ -307,7 +310,6 @@ def selective_scan_backward(x, dt, A, B, C, dy, saved, *, skip=None, z=None, dt_
                             stream=None):
     """Gradients of sum(dy y) + sum(dstate_out state_out): dict of dx, ddt, dA, dB, dC, dskip,
     ddt_bias, dz and dstate_in (None where the input was not given, or not want_dstate)."""
-    import torch
     _dims("x", x, 3)
     p = _scan_problem(x, dt, A, B, C, skip, z, dt_bias, softplus, state_in)
     _activation("dy", dy, x.shape, x)
@@ -315,38 +317,43 @@ def selective_scan_backward(x, dt, A, B, C, dy, saved, *, skip=None, z=None, dt_
     need = load().mlstm_scan_saved_size(p.B, p.T, p.D, p.G, p.N, p.dtype)
     if saved is None or saved.device != x.device or saved.numel() * saved.element_size() < need:
         raise ValueError(f"saved must hold the {need} bytes of the forward of the same inputs")
-    with _launch(stream, x, dt, A, B, C, skip, z, dt_bias, state_in, dy, saved, dstate_out) as s:
-        new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+    def launch(s):
+        new = lambda t: None if t is None else t.new_empty(t.shape)
         out = {"dx": new(x), "ddt": new(x), "dA": new(A), "dB": new(B), "dC": new(C),
-               "dskip": new(skip) if skip is not None else None,
-               "ddt_bias": new(dt_bias) if dt_bias is not None else None,
-               "dz": new(x) if z is not None else None,
-               "dstate_in": (torch.empty((p.B, p.D, p.N), dtype=torch.float32, device=x.device)
-                             if want_dstate else None)}
-        g = ScanGrads()
-        g.dx, g.ddt, g.dz = _rows(out["dx"]), _rows(out["ddt"]), _rows(out["dz"])
-        g.db, g.dc = _group_rows(out["dB"], 3, p.G), _group_rows(out["dC"], 3, p.G)
-        g.da, g.dskip, g.ddt_bias = _ptr(out["dA"]), _ptr(out["dskip"]), _ptr(out["ddt_bias"])
-        g.dstate_in = _ptr(out["dstate_in"])
-        ws = _bytes(load().mlstm_scan_bwd_workspace_size(p.B, p.T, p.D, p.G, p.N, p.dtype), x.device)
+               "dskip": new(skip), "ddt_bias": new(dt_bias), "dz": new(z),
+               "dstate_in": A.new_empty((p.B, p.D, p.N)) if want_dstate else None}
+        g = ScanGrads(_rows(out["dx"]), _rows(out["ddt"]), _rows(out["dz"]), _group_rows(out["dB"]),
+                      _group_rows(out["dC"]), _ptr(out["dA"]), _ptr(out["dskip"]),
+                      _ptr(out["ddt_bias"]), _ptr(out["dstate_in"]))
+        ws = _bytes(load().mlstm_scan_bwd_workspace_size(p.B, p.T, p.D, p.G, p.N, p.dtype), x)
         _check(load().mlstm_scan_bwd(p, _rows(dy), saved.data_ptr(), _ptr(dstate_out), g, ws.data_ptr(),
                                      ws.numel(), s), "mlstm_scan_bwd")
-    return out
+        return out
+
+    return _on(stream, x, (dt, A, B, C, skip, z, dt_bias, state_in, dy, saved, dstate_out), launch)
+
+
+def _group_rows(t):
+    """The gradient of B or C: [B, T, N] or [B, T, G, N]."""
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2) if t.dim() == 4 else 0)
 
 
 def selective_scan_step(x, dt, A, B, C, state, *, skip=None, z=None, dt_bias=None, softplus=True,
                         stream=None):
     """One token: x, dt, z [B, D]; B, C [B, N] or [B, G, N]; returns y [B, D] and updates ``state``
     [B, D, N] in place."""
-    import torch
     _dims("x", x, 2)
     if state is None:
         raise ValueError("state is required")
     p = _scan_problem(x, dt, A, B, C, skip, z, dt_bias, softplus, state)
-    with _launch(stream, x, dt, A, B, C, skip, z, dt_bias, state) as s:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+    def launch(s):
+        y = x.new_empty(x.shape)
         _check(load().mlstm_scan_step(p, _rows(y), state.data_ptr(), s), "mlstm_scan_step")
-    return y
+        return y
+
+    return _on(stream, x, (dt, A, B, C, skip, z, dt_bias, state), launch)
 
 
 # --------------------------------------------------------------------------
@@ -395,40 +402,43 @@ def group_norm_forward(x, weight=None, bias=None, *, gate=None, act=ACT_NONE, sc
     """
     import torch
     layout, B, T, NH, d, dt = _norm_args(x, weight, bias, gate, act, scope, groups)
-    with _launch(stream, x, weight, bias, gate) as s:
-        y = torch.empty((B, T, NH * d), dtype=x.dtype, device=x.device)
-        stats = (torch.empty(_stats_shape(B, T, NH, scope), dtype=torch.float32, device=x.device)
-                 if keep_stats else None)
+
+    def launch(s):
+        y = x.new_empty((B, T, NH * d))
+        stats = (x.new_empty(_stats_shape(B, T, NH, scope), dtype=torch.float32) if keep_stats
+                 else None)
         need = load().mlstm_group_norm_workspace_size(B, T, NH, d, scope, dt, 0)
-        ws = _bytes(need, x.device) if need else None
+        ws = _bytes(need, x) if need else None
         _check(load().mlstm_group_norm_fwd(_head_rows(x, layout, d), _ptr(weight), _ptr(bias),
                                            _head_rows(gate, "last", d), _head_rows(y, "last", d),
                                            _ptr(stats), _ptr(ws), need, B, T, NH, d, scope, act, eps,
                                            dt, s), "mlstm_group_norm_fwd")
-    return y, stats
+        return y, stats
+
+    return _on(stream, x, (weight, bias, gate), launch)
 
 
 def group_norm_backward(x, weight, bias, dy, stats, *, gate=None, act=ACT_NONE, scope=SCOPE_TOKEN,
                         groups=None, stream=None):
     """Gradients of sum(dy y): dict of dx (laid out like x), dweight, dbias and dgate (None where
     the input was not given)."""
-    import torch
     layout, B, T, NH, d, dt = _norm_args(x, weight, bias, gate, act, scope, groups)
     _activation("dy", dy, (B, T, NH * d), x)
     if stats is None:
         raise ValueError("stats of the forward are required")
     _fp32("stats", stats, _stats_shape(B, T, NH, scope), x)
-    with _launch(stream, x, weight, bias, gate, dy, stats) as s:
-        new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)
-        out = {"dx": new(x), "dweight": new(weight) if weight is not None else None,
-               "dbias": new(bias) if bias is not None else None,
-               "dgate": new(gate) if gate is not None else None}
+
+    def launch(s):
+        new = lambda t: None if t is None else t.new_empty(t.shape)
+        out = {"dx": new(x), "dweight": new(weight), "dbias": new(bias), "dgate": new(gate)}
         need = load().mlstm_group_norm_workspace_size(B, T, NH, d, scope, dt, 1)
-        ws = _bytes(need, x.device) if need else None
+        ws = _bytes(need, x) if need else None
         _check(load().mlstm_group_norm_bwd(_head_rows(x, layout, d), _ptr(weight), _ptr(bias),
                                            _head_rows(gate, "last", d), _head_rows(dy, "last", d),
                                            stats.data_ptr(), _head_rows(out["dx"], layout, d),
                                            _head_rows(out["dgate"], "last", d), _ptr(out["dweight"]),
                                            _ptr(out["dbias"]), _ptr(ws), need, B, T, NH, d, scope, act,
                                            dt, s), "mlstm_group_norm_bwd")
-    return out
+        return out
+
+    return _on(stream, x, (weight, bias, gate, dy, stats), launch)

@@ -152,7 +152,7 @@ int mlstm_conv_fwd(const mlstm_rows_t* x, const float* weight, const float* bias
   a.w = weight; a.bias = bias; a.state_in = state_in; a.state_out = state_out;
   a.B = B; a.T = T; a.NH = NH; a.d = d; a.W = W; a.act = act; a.dtype = dtype;
   a.wide = d % 8 == 0 && aligned(a.x, dtype) && aligned(a.y, dtype) && !off16(state_in) &&
-           !off16(state_out);
+           !off16(state_out) && !off16(weight);
   if ((st = pending_error("before mlstm_conv_fwd")) != MLSTM_OK) return st;
   return cuda_result(mlstm::launch_conv_fwd(a, (cudaStream_t)stream), "conv_fwd");
 }
@@ -194,7 +194,7 @@ int mlstm_conv_bwd(const mlstm_rows_t* x, const float* weight, const float* bias
   a.dstate_in = dstate_in; a.dw = dweight; a.dbias = dbias; a.partial = (float*)workspace;
   a.B = B; a.T = T; a.NH = NH; a.d = d; a.W = W; a.act = act; a.dtype = dtype;
   a.wide = d % 8 == 0 && aligned(a.x, dtype) && aligned(a.y, dtype) && aligned(a.dx, dtype) &&
-           !off16(state_in) && !off16(dstate_out) && !off16(dstate_in);
+           !off16(state_in) && !off16(dstate_out) && !off16(dstate_in) && !off16(weight);
   if ((st = pending_error("before mlstm_conv_bwd")) != MLSTM_OK) return st;
   return cuda_result(mlstm::launch_conv_bwd(a, (cudaStream_t)stream), "conv_bwd");
 }
@@ -218,7 +218,7 @@ int mlstm_conv_step(const mlstm_rows_t* x, const float* weight, const float* bia
   a.w = weight; a.bias = bias; a.state_in = state_in; a.state_out = state_out;
   a.B = B; a.T = 1; a.NH = NH; a.d = d; a.W = W; a.act = act; a.dtype = dtype;
   a.wide = d % 8 == 0 && aligned(a.x, dtype) && aligned(a.y, dtype) && !off16(state_in) &&
-           !off16(state_out);
+           !off16(state_out) && !off16(weight);
   if ((st = pending_error("before mlstm_conv_step")) != MLSTM_OK) return st;
   return cuda_result(mlstm::launch_conv_step(a, (cudaStream_t)stream), "conv_step");
 }

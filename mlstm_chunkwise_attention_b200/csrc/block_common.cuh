@@ -65,6 +65,111 @@ __device__ __forceinline__ void store8(float* p, const float* v, int n) {
   }
 }
 
+// Four or eight consecutive channels as they lie in memory: loads into these stay in flight while
+// earlier ones are worked on (converting at once would wait for each).
+template <typename T, int C> struct Raw;
+template <> struct Raw<bf16, 4> { uint2 u; };
+template <> struct Raw<bf16, 8> { uint4 u; };
+template <> struct Raw<float, 4> { float4 u; };
+template <> struct Raw<float, 8> { float4 u, v; };
+
+// WIDE as in load8; else the first n elements, the rest zero.
+template <bool WIDE, int C>
+__device__ __forceinline__ void load_raw(const bf16* p, Raw<bf16, C>& r, int n) {
+  if (WIDE) {
+    r.u = *reinterpret_cast<const decltype(r.u)*>(p);
+  } else {
+    uint32_t w[C / 2];
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i)
+      w[i] = (2 * i < n ? (uint32_t)q[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)q[2 * i + 1] << 16 : 0u);
+    r.u = *reinterpret_cast<decltype(r.u)*>(w);
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void load_raw(const float* p, Raw<float, 4>& r, int n) {
+  if (WIDE)
+    r.u = *reinterpret_cast<const float4*>(p);
+  else
+    r.u = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+}
+template <bool WIDE>
+__device__ __forceinline__ void load_raw(const float* p, Raw<float, 8>& r, int n) {
+  Raw<float, 4> a, b;
+  load_raw<WIDE>(p, a, n);
+  load_raw<WIDE>(p + 4, b, n - 4);
+  r.u = a.u;
+  r.v = b.u;
+}
+template <typename T, int C>
+__device__ __forceinline__ void zero_raw(Raw<T, C>& r) { r = Raw<T, C>{}; }
+// As pairs of neighbouring channels.
+template <int C>
+__device__ __forceinline__ void expand(const Raw<bf16, C>& r, float2* v) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < C / 2; ++i)
+    v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <int C>
+__device__ __forceinline__ void expand(const Raw<float, C>& r, float2* v) {
+  const float2* w = reinterpret_cast<const float2*>(&r);
+#pragma unroll
+  for (int i = 0; i < C / 2; ++i) v[i] = w[i];
+}
+template <bool WIDE, int C>
+__device__ __forceinline__ void store_pairs(bf16* p, const float2* v, int n) {
+  if (WIDE) {
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    Raw<bf16, C> r;
+    r.u = *reinterpret_cast<decltype(r.u)*>(w);
+    *reinterpret_cast<decltype(r.u)*>(p) = r.u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (i < n) p[i] = from_f32<bf16>(i & 1 ? v[i / 2].y : v[i / 2].x);
+  }
+}
+template <bool WIDE, int C>
+__device__ __forceinline__ void store_pairs(float* p, const float2* v, int n) {
+  if (WIDE) {
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (i < n) p[i] = i & 1 ? v[i / 2].y : v[i / 2].x;
+  }
+}
+
+// Packed fp32 arithmetic: two lanes of fp32 in one instruction, each rounded as fmaf / + / * round.
+__device__ __forceinline__ unsigned long long as_u64(float2 a) {
+  return *reinterpret_cast<unsigned long long*>(&a);
+}
+__device__ __forceinline__ float2 as_f2(unsigned long long a) { return *reinterpret_cast<float2*>(&a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+
 // 1 / (1 + exp(-v)); 0 and 1 at the far ends, NaN for NaN.
 __device__ __forceinline__ float sigmoidf(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 

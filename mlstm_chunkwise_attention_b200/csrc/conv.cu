@@ -6,7 +6,7 @@
 //
 //   dx_t = sum_j w_j dp_{t + W - 1 - j}   dw_j = sum_t dp_t x_{t - W + 1 + j}   dbias = sum_t dp_t
 //
-// Bound by HBM: about W multiply-adds per element moved.  A thread owns a few
+// Bound by HBM: about W multiply-adds per element moved.  A thread owns four
 // channels and walks a run of tokens with the last W - 1 inputs in registers,
 // so each input is loaded once per run plus W - 1 tokens of the run before it.
 // Inputs and outputs are addressed by strides: the convolved half of a wider
@@ -17,82 +17,117 @@ namespace mlstm {
 
 namespace {
 
-// Channels c0 .. c0 + 7 of token t, where t < 0 is the carried state (or zero).
+// A thread's channels: two packed pairs.  Four channels keep a thread's registers low enough for
+// half the SM's warps (eight took 128 registers, 22 % of the warps and 2.2 TB/s).
+constexpr int kC = 4, kPairs = kC / 2;
+
+// Channels c0 .. c0 + 3 of token t, where t < 0 is the carried state (or zero).
 template <typename T, int W, bool WIDE>
-__device__ __forceinline__ void load_input(const ConvArgs& a, const T* x, const T* st, int t, int c0,
-                                           int n, float* v) {
-  if (t >= 0) {
-    load8<WIDE>(x + (long long)t * a.x.st, v, n);
-  } else if (st != nullptr) {
-    load8<WIDE>(st + (long long)(t + W - 1) * a.D() + c0, v, n);
+__device__ __forceinline__ void load_input(const ConvArgs& a, const T* x, const T* st, int t, int n,
+                                           float2* v) {
+  Raw<T, kC> r;
+  zero_raw(r);
+  if (t >= 0)
+    load_raw<WIDE>(x + t * a.x.st, r, n);
+  else if (st != nullptr)
+    load_raw<WIDE>(st + (long long)(t + W - 1) * a.D(), r, n);
+  expand(r, v);
+}
+
+// The taps of a thread's channels, [W][pairs], and its biases.
+template <int W, bool WIDE>
+__device__ __forceinline__ void load_taps(const ConvArgs& a, int c0, int n, float2 (*w)[kPairs],
+                                          float2* bias) {
+  float f[kC * W];
+  if (WIDE) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      reinterpret_cast<float4*>(f)[i] = reinterpret_cast<const float4*>(a.w + (long long)c0 * W)[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    for (int i = 0; i < kC * W; ++i) f[i] = i < n * W ? a.w[(long long)c0 * W + i] : 0.f;
+  }
+#pragma unroll
+  for (int p = 0; p < kPairs; ++p) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][p] = make_float2(f[2 * p * W + j], f[(2 * p + 1) * W + j]);
+    bias[p] = make_float2(a.bias != nullptr && 2 * p < n ? a.bias[c0 + 2 * p] : 0.f,
+                          a.bias != nullptr && 2 * p + 1 < n ? a.bias[c0 + 2 * p + 1] : 0.f);
   }
 }
 
-// Writes channels c0 .. c0 + n - 1 of a row whose channels lie in heads of d.
+// Writes channels c0 .. c0 + n - 1 of a row whose channels lie in heads of d; `off` is c0's place.
 template <typename T, bool WIDE>
-__device__ __forceinline__ void store_heads(T* row, long long sh, int d, int c0, int n, const float* v) {
-  if (WIDE) {  // d is a multiple of 8, so the eight channels share a head
-    store8<true>(row + (c0 / d) * sh + c0 % d, v, n);
+__device__ __forceinline__ void store_heads(T* row, long long off, long long sh, int d, int c0, int n,
+                                            const float2* v) {
+  if (WIDE) {  // d is a multiple of 8, so the channels share a head
+    store_pairs<true, kC>(row + off, v, n);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) row[((c0 + i) / d) * sh + (c0 + i) % d] = from_f32<T>(v[i]);
+    for (int i = 0; i < kC; ++i)
+      if (i < n)
+        row[((c0 + i) / d) * sh + (c0 + i) % d] = from_f32<T>(i & 1 ? v[i / 2].y : v[i / 2].x);
   }
 }
+
+template <int W, int ACT>
+__device__ __forceinline__ void conv_token(const float2 (*w)[kPairs], const float2* bias,
+                                           float2 (*win)[kPairs], const float2* x, float2* o) {
+#pragma unroll
+  for (int p = 0; p < kPairs; ++p) {
+    float2 s = bias[p];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) s = fma2(w[j][p], win[j][p], s);
+    s = fma2(w[W - 1][p], x[p], s);
+    o[p] = make_float2(act_value<ACT>(s.x), act_value<ACT>(s.y));
+#pragma unroll
+    for (int j = 0; j + 2 < W; ++j) win[j][p] = win[j + 1][p];
+    win[W - 2][p] = x[p];
+  }
+}
+
+constexpr int kAhead = 8;  // tokens whose loads a thread has in flight
 
 template <typename T, int W, int ACT, bool WIDE>
 __global__ void __launch_bounds__(128) conv_fwd_kernel(ConvArgs a, int run, int runs, int vecs) {
   const long long item = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= (long long)vecs * runs * a.B) return;
-  const int c0 = (int)(item % vecs) * 8;
+  const int c0 = (int)(item % vecs) * kC;
   const long long br = item / vecs;
   const int t0 = (int)(br % runs) * run, b = (int)(br / runs);
-  const int D = a.D(), n = min(8, D - c0);
+  const int D = a.D(), n = min(kC, D - c0);
   const T* x = (const T*)a.x.p + (long long)b * a.x.sb + c0;
-  const T* st = a.state_in ? (const T*)a.state_in + (long long)b * (W - 1) * D : nullptr;
+  const T* st = a.state_in ? (const T*)a.state_in + (long long)b * (W - 1) * D + c0 : nullptr;
   T* y = (T*)a.y.p + (long long)b * a.y.sb;
-  float w[W][8], bias[8], win[W - 1][8];
+  const long long off = (c0 / a.d) * a.y.sh + c0 % a.d;
+  float2 w[W][kPairs], bias[kPairs], win[W - 1][kPairs];
+  load_taps<W, WIDE>(a, c0, n, w, bias);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bias[i] = a.bias != nullptr && i < n ? a.bias[c0 + i] : 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = i < n ? a.w[(long long)(c0 + i) * W + j] : 0.f;
-  }
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) load_input<T, W, WIDE>(a, x, st, t0 - (W - 1) + j, c0, n, win[j]);
+  for (int j = 0; j < W - 1; ++j) load_input<T, W, WIDE>(a, x, st, t0 - (W - 1) + j, n, win[j]);
   const int t1 = min(t0 + run, a.T);
-  constexpr int U = 4;  // tokens in flight
-  for (int tb = t0; tb < t1; tb += U) {
-    float v[U][8];
+  int t = t0;
+  for (; t + kAhead <= t1; t += kAhead) {
+    Raw<T, kC> r[kAhead];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (tb + u < t1) load8<WIDE>(x + (long long)(tb + u) * a.x.st, v[u], n);
+    for (int u = 0; u < kAhead; ++u) load_raw<WIDE>(x + (t + u) * a.x.st, r[u], n);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (tb + u < t1) {
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float p = bias[i];
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) p = fmaf(w[j][i], win[j][i], p);
-          p = fmaf(w[W - 1][i], v[u][i], p);
-          o[i] = act_value<ACT>(p);
-#pragma unroll
-          for (int j = 0; j + 2 < W; ++j) win[j][i] = win[j + 1][i];
-          win[W - 2][i] = v[u][i];
-        }
-        store_heads<T, WIDE>(y + (long long)(tb + u) * a.y.st, a.y.sh, a.d, c0, n, o);
-      }
+    for (int u = 0; u < kAhead; ++u) {
+      float2 v[kPairs], o[kPairs];
+      expand(r[u], v);
+      conv_token<W, ACT>(w, bias, win, v, o);
+      store_heads<T, WIDE>(y + (t + u) * a.y.st, off, a.y.sh, a.d, c0, n, o);
     }
+  }
+  for (; t < t1; ++t) {
+    float2 v[kPairs], o[kPairs];
+    load_input<T, W, WIDE>(a, x, st, t, n, v);
+    conv_token<W, ACT>(w, bias, win, v, o);
+    store_heads<T, WIDE>(y + t * a.y.st, off, a.y.sh, a.d, c0, n, o);
   }
   if (a.state_out != nullptr && t1 == a.T) {  // the window is the last W - 1 inputs
     T* so = (T*)a.state_out + (long long)b * (W - 1) * D + c0;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) store8<WIDE>(so + (long long)j * D, win[j], n);
+    for (int j = 0; j < W - 1; ++j) store_pairs<WIDE, kC>(so + (long long)j * D, win[j], n);
   }
 }
 
@@ -102,76 +137,64 @@ template <typename T, int W, int ACT, bool WIDE>
 __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, int vecs) {
   const long long item = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= (long long)vecs * a.B) return;
-  const int c0 = (int)(item % vecs) * 8, b = (int)(item / vecs);
-  const int D = a.D(), n = min(8, D - c0);
+  const int c0 = (int)(item % vecs) * kC, b = (int)(item / vecs);
+  const int D = a.D(), n = min(kC, D - c0);
   const T* st = (const T*)a.state_in + (long long)b * (W - 1) * D + c0;
   T* so = (T*)a.state_out + (long long)b * (W - 1) * D + c0;
-  float v[W][8], o[8];
+  float2 w[W][kPairs], bias[kPairs], win[W - 1][kPairs], v[kPairs], o[kPairs];
+  load_taps<W, WIDE>(a, c0, n, w, bias);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) load8<WIDE>(st + (long long)j * D, v[j], n);
-  load8<WIDE>((const T*)a.x.p + (long long)b * a.x.sb + c0, v[W - 1], n);
+  for (int j = 0; j < W - 1; ++j) load_input<T, W, WIDE>(a, nullptr, st, j - (W - 1), n, win[j]);
+  load_input<T, W, WIDE>(a, (const T*)a.x.p + (long long)b * a.x.sb + c0, st, 0, n, v);
+  conv_token<W, ACT>(w, bias, win, v, o);
+  store_heads<T, WIDE>((T*)a.y.p + (long long)b * a.y.sb, (c0 / a.d) * a.y.sh + c0 % a.d, a.y.sh, a.d, c0,
+                       n, o);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float p = a.bias != nullptr && i < n ? a.bias[c0 + i] : 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) p = fmaf(i < n ? a.w[(long long)(c0 + i) * W + j] : 0.f, v[j][i], p);
-    o[i] = act_value<ACT>(p);
-  }
-  store_heads<T, WIDE>((T*)a.y.p + (long long)b * a.y.sb, a.y.sh, a.d, c0, n, o);
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) store8<WIDE>(so + (long long)j * D, v[j + 1], n);
+  for (int j = 0; j < W - 1; ++j) store_pairs<WIDE, kC>(so + (long long)j * D, win[j], n);
 }
 
 constexpr int kBwdRun = 64;    // tokens of one thread's run
 constexpr int kBwdLanes = 32;  // channel vectors of a CTA
 constexpr int kBwdRuns = 4;    // runs of a CTA, joined in shared memory
-constexpr int kBwdC = 4;       // channels of a thread: W windows of x and dp stay in registers
+constexpr int kBwdAhead = 4;   // tokens whose x and dy a thread has in flight
 
-template <bool WIDE>
-__device__ __forceinline__ void load4(const bf16* p, float* v, int n) {
-  if (WIDE) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
-  } else {
+// One thread's walk through its run: windows of W inputs and W values of dp, sums for the taps.
+template <typename T, int W, int ACT, bool WIDE>
+struct BwdWalk {
+  float2 w[W][kPairs], bias[kPairs], win[W][kPairs], dp[W][kPairs], dw[W][kPairs], db[kPairs];
+
+  // Takes token t in (x and dy; zero past the end of the sequence), `own`: its sums are this run's.
+  __device__ __forceinline__ void take(const float2* x, const float2* g, bool own) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
-  }
-}
-template <bool WIDE>
-__device__ __forceinline__ void load4(const float* p, float* v, int n) {
-  if (WIDE) {
-    const float4 u = *reinterpret_cast<const float4*>(p);
-    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-  } else {
+    for (int p = 0; p < kPairs; ++p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < n ? p[i] : 0.f;
-  }
-}
-template <bool WIDE>
-__device__ __forceinline__ void store4(bf16* p, const float* v, int n) {
-  if (WIDE) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    uint2 u;
-    u.x = *reinterpret_cast<const uint32_t*>(&a);
-    u.y = *reinterpret_cast<const uint32_t*>(&b);
-    *reinterpret_cast<uint2*>(p) = u;
-  } else {
+      for (int j = 0; j + 1 < W; ++j) {
+        win[j][p] = win[j + 1][p];
+        dp[j][p] = dp[j + 1][p];
+      }
+      win[W - 1][p] = x[p];
+      float2 s = bias[p], val, slope;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = from_f32<bf16>(v[i]);
-  }
-}
-template <bool WIDE>
-__device__ __forceinline__ void store4(float* p, const float* v, int n) {
-  if (WIDE) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
+      for (int j = 0; j < W; ++j) s = fma2(w[j][p], win[j][p], s);
+      act_slope<ACT>(s.x, &val.x, &slope.x);
+      act_slope<ACT>(s.y, &val.y, &slope.y);
+      dp[W - 1][p] = mul2(g[p], slope);
+      if (own) {
+        db[p] = add2(db[p], dp[W - 1][p]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = v[i];
+        for (int j = 0; j < W; ++j) dw[j][p] = fma2(dp[W - 1][p], win[j][p], dw[j][p]);
+      }
+    }
   }
-}
+  __device__ __forceinline__ void dx(float2* o) const {
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+      o[p] = mul2(w[0][p], dp[W - 1][p]);
+#pragma unroll
+      for (int j = 1; j < W; ++j) o[p] = fma2(w[j][p], dp[W - 1 - j][p], o[p]);
+    }
+  }
+};
 
 // A thread walks tokens t0 .. t0 + run + W - 2 of its channels: it recomputes pre at each,
 // forms dp, and W - 1 tokens later emits dx, whose last term is then known.  The first run
@@ -179,138 +202,119 @@ __device__ __forceinline__ void store4(float* p, const float* v, int n) {
 // tokens are taken for the run's own tokens only and joined over the CTA's runs, one row
 // of partials per CTA.
 template <typename T, int W, int ACT, bool WIDE>
-__global__ void __launch_bounds__(kBwdLanes * kBwdRuns) conv_bwd_kernel(ConvArgs a, int run, int runs,
-                                                                       int vecs, int cblocks) {
-  __shared__ float red[kBwdRuns][W + 1][kBwdC][kBwdLanes];
+__global__ void __launch_bounds__(kBwdLanes * kBwdRuns, 4) conv_bwd_kernel(ConvArgs a, int run, int runs,
+                                                                          int vecs, int cblocks) {
+  __shared__ float red[kBwdRuns][W + 1][kC][kBwdLanes];
   const int lane = threadIdx.x, rr = threadIdx.y;
   const int vec = (int)(blockIdx.x % cblocks) * kBwdLanes + lane;
   const long long row = blockIdx.x / cblocks;          // partial row of this CTA
   const long long br = row * kBwdRuns + rr;            // run of all batches
   const int D = a.D();
-  float dw[W][kBwdC], db[kBwdC];
+  BwdWalk<T, W, ACT, WIDE> k;
 #pragma unroll
-  for (int i = 0; i < kBwdC; ++i) {
-    db[i] = 0.f;
+  for (int p = 0; p < kPairs; ++p) {
+    k.db[p] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+    for (int j = 0; j < W; ++j) k.dw[j][p] = k.dp[j][p] = make_float2(0.f, 0.f);
   }
   if (vec < vecs && br < (long long)runs * a.B) {
-    const int c0 = vec * kBwdC, n = min(kBwdC, D - c0);
+    const int c0 = vec * kC, n = min(kC, D - c0);
     const int t0 = (int)(br % runs) * run, b = (int)(br / runs);
     const int t1 = min(t0 + run, a.T);
     const T* x = (const T*)a.x.p + (long long)b * a.x.sb + c0;
     const T* st = a.state_in ? (const T*)a.state_in + (long long)b * (W - 1) * D + c0 : nullptr;
     const T* dy = (const T*)a.y.p + (long long)b * a.y.sb;
-    long long off[kBwdC];  // of each channel in a row of dy
-#pragma unroll
-    for (int i = 0; i < kBwdC; ++i) off[i] = i < n ? ((c0 + i) / a.d) * a.y.sh + (c0 + i) % a.d : 0;
+    const long long off = (c0 / a.d) * a.y.sh + c0 % a.d;
     T* dx = (T*)a.dx.p + (long long)b * a.dx.sb + c0;
-    float w[W][kBwdC], bias[kBwdC], win[W][kBwdC], dp[W][kBwdC];
+    load_taps<W, WIDE>(a, c0, n, k.w, k.bias);
+    auto load_dy = [&](int t, Raw<T, kC>& r) {
+      if (WIDE) {
+        load_raw<true>(dy + t * a.y.st + off, r, n);
+      } else {
+        float2 v[kPairs];
 #pragma unroll
-    for (int i = 0; i < kBwdC; ++i) {
-      bias[i] = a.bias != nullptr && i < n ? a.bias[c0 + i] : 0.f;
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        w[j][i] = i < n ? a.w[(long long)(c0 + i) * W + j] : 0.f;
-        dp[j][i] = 0.f;
+        for (int p = 0; p < kPairs; ++p) {
+          const int c = c0 + 2 * p;
+          v[p].x = 2 * p < n ? to_f32(dy[t * a.y.st + (c / a.d) * a.y.sh + c % a.d]) : 0.f;
+          v[p].y = 2 * p + 1 < n ? to_f32(dy[t * a.y.st + ((c + 1) / a.d) * a.y.sh + (c + 1) % a.d]) : 0.f;
+        }
+        store_pairs<true, kC>(reinterpret_cast<T*>(&r), v, kC);  // exact: the values come from T
       }
-    }
+    };
     // win[j] = x_{tau - (W - 1) + j}; one step before tau = t0 it holds tokens t0 - W .. t0 - 1,
     // of which the first is shifted out unread
 #pragma unroll
-    for (int j = 1; j < W; ++j) {
-      const int t = t0 - W + j;
-      if (t >= 0)
-        load4<WIDE>(x + (long long)t * a.x.st, win[j], n);
-      else if (st != nullptr)
-        load4<WIDE>(st + (long long)(t + W - 1) * D, win[j], n);
-      else
-#pragma unroll
-        for (int i = 0; i < kBwdC; ++i) win[j][i] = 0.f;
-    }
+    for (int j = 1; j < W; ++j) load_input<T, W, WIDE>(a, x, st, t0 - W + j, n, k.win[j]);
     const int emit0 = t0 == 0 ? -(W - 1) : t0;  // first token whose gradient this run writes
     const int end = t1 + W - 1;                 // dx of t1 - 1 is complete at tau = t1 + W - 2
-    constexpr int U = 4;
-    for (int tb = t0; tb < end; tb += U) {
-      float xv[U][kBwdC], gv[U][kBwdC];
+    auto emit = [&](int e) {                    // the token whose gradient is complete
+      if (e < emit0) return;
+      float2 o[kPairs];
+      k.dx(o);
+      const int r = e - a.T + W - 1;  // row of the final state that is token e
+      if (a.dstate_out != nullptr && r >= 0) {
+        Raw<T, kC> q;
+        float2 g[kPairs];
+        load_raw<WIDE>((const T*)a.dstate_out + ((long long)b * (W - 1) + r) * D + c0, q, n);
+        expand(q, g);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u;
-        if (t < end && t < a.T) {
-          load4<WIDE>(x + (long long)t * a.x.st, xv[u], n);
-          if (WIDE) {
-            load4<true>(dy + (long long)t * a.y.st + off[0], gv[u], n);
-          } else {
+        for (int p = 0; p < kPairs; ++p) o[p] = add2(o[p], g[p]);
+      }
+      if (e >= 0)
+        store_pairs<WIDE, kC>(dx + e * a.dx.st, o, n);
+      else if (a.dstate_in != nullptr)
+        store_pairs<WIDE, kC>((T*)a.dstate_in + ((long long)b * (W - 1) + e + W - 1) * D + c0, o, n);
+    };
+    int t = t0;
+    for (; t + kBwdAhead <= t1; t += kBwdAhead) {
+      Raw<T, kC> rx[kBwdAhead], rg[kBwdAhead];
 #pragma unroll
-            for (int i = 0; i < kBwdC; ++i)
-              gv[u][i] = i < n ? to_f32(dy[(long long)t * a.y.st + off[i]]) : 0.f;
-          }
-        }
+      for (int u = 0; u < kBwdAhead; ++u) {
+        load_raw<WIDE>(x + (t + u) * a.x.st, rx[u], n);
+        load_dy(t + u, rg[u]);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tb + u;
-        if (t < end) {
-          const bool in = t < a.T;
-#pragma unroll
-          for (int i = 0; i < kBwdC; ++i) {
-#pragma unroll
-            for (int j = 0; j + 1 < W; ++j) {
-              win[j][i] = win[j + 1][i];
-              dp[j][i] = dp[j + 1][i];
-            }
-            win[W - 1][i] = in ? xv[u][i] : 0.f;
-            float p = bias[i], val, slope;
-#pragma unroll
-            for (int j = 0; j < W; ++j) p = fmaf(w[j][i], win[j][i], p);
-            act_slope<ACT>(p, &val, &slope);
-            dp[W - 1][i] = in ? gv[u][i] * slope : 0.f;
-            if (t < t1) {
-              db[i] += dp[W - 1][i];
-#pragma unroll
-              for (int j = 0; j < W; ++j) dw[j][i] = fmaf(dp[W - 1][i], win[j][i], dw[j][i]);
-            }
-          }
-          const int e = t - (W - 1);  // the token whose gradient is complete
-          if (e >= emit0 && e < t1) {
-            float o[kBwdC];
-#pragma unroll
-            for (int i = 0; i < kBwdC; ++i) {
-              o[i] = 0.f;
-#pragma unroll
-              for (int j = 0; j < W; ++j) o[i] = fmaf(w[j][i], dp[W - 1 - j][i], o[i]);
-            }
-            const int r = e - a.T + W - 1;  // row of the final state that is token e
-            if (a.dstate_out != nullptr && r >= 0) {
-              float g[kBwdC];
-              load4<WIDE>((const T*)a.dstate_out + ((long long)b * (W - 1) + r) * D + c0, g, n);
-#pragma unroll
-              for (int i = 0; i < kBwdC; ++i) o[i] += g[i];
-            }
-            if (e >= 0)
-              store4<WIDE>(dx + (long long)e * a.dx.st, o, n);
-            else if (a.dstate_in != nullptr)
-              store4<WIDE>((T*)a.dstate_in + ((long long)b * (W - 1) + e + W - 1) * D + c0, o, n);
-          }
-        }
+      for (int u = 0; u < kBwdAhead; ++u) {
+        float2 v[kPairs], g[kPairs];
+        expand(rx[u], v);
+        expand(rg[u], g);
+        k.take(v, g, true);
+        emit(t + u - (W - 1));
       }
+    }
+    for (; t < end; ++t) {
+      float2 v[kPairs], g[kPairs];
+      Raw<T, kC> rx, rg;
+      zero_raw(rx);
+      zero_raw(rg);
+      if (t < a.T) {
+        load_raw<WIDE>(x + t * a.x.st, rx, n);
+        load_dy(t, rg);
+      }
+      expand(rx, v);
+      expand(rg, g);
+      k.take(v, g, t < t1);
+      if (t >= a.T)  // nothing comes from behind the end, whatever the recomputed slope is
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) k.dp[W - 1][p] = make_float2(0.f, 0.f);
+      emit(t - (W - 1));
     }
   }
 #pragma unroll
-  for (int i = 0; i < kBwdC; ++i) {
-    red[rr][W][i][lane] = db[i];
+  for (int i = 0; i < kC; ++i) {
+    red[rr][W][i][lane] = i & 1 ? k.db[i / 2].y : k.db[i / 2].x;
 #pragma unroll
-    for (int j = 0; j < W; ++j) red[rr][j][i][lane] = dw[j][i];
+    for (int j = 0; j < W; ++j) red[rr][j][i][lane] = i & 1 ? k.dw[j][i / 2].y : k.dw[j][i / 2].x;
   }
   __syncthreads();
   // [W + 1][channels] sums of this CTA, channels contiguous
-  const int tid = rr * kBwdLanes + lane, cbase = (int)(blockIdx.x % cblocks) * kBwdLanes * kBwdC;
-  for (int e = tid; e < (W + 1) * kBwdLanes * kBwdC; e += kBwdLanes * kBwdRuns) {
-    const int k = e / (kBwdLanes * kBwdC), c = e % (kBwdLanes * kBwdC);
+  const int tid = rr * kBwdLanes + lane, cbase = (int)(blockIdx.x % cblocks) * kBwdLanes * kC;
+  for (int e = tid; e < (W + 1) * kBwdLanes * kC; e += kBwdLanes * kBwdRuns) {
+    const int q = e / (kBwdLanes * kC), c = e % (kBwdLanes * kC);
     float s = 0.f;
 #pragma unroll
-    for (int q = 0; q < kBwdRuns; ++q) s += red[q][k][c % kBwdC][c / kBwdC];
-    if (cbase + c < D) a.partial[(row * (W + 1) + k) * D + cbase + c] = s;
+    for (int i = 0; i < kBwdRuns; ++i) s += red[i][q][c % kC][c / kC];
+    if (cbase + c < D) a.partial[(row * (W + 1) + q) * D + cbase + c] = s;
   }
 }
 
@@ -345,10 +349,10 @@ int bwd_runs(int T) { return (T + kBwdRun - 1) / kBwdRun; }
 
 template <typename T, int W, int ACT, bool WIDE>
 cudaError_t fwd(const ConvArgs& a, cudaStream_t s) {
-  const int vecs = (a.D() + 7) / 8;
-  // Runs of 32 tokens (3 of 35 loads are the halo), shorter while that leaves under two
+  const int vecs = (a.D() + kC - 1) / kC;
+  // Runs of 64 tokens (3 of 67 loads are the halo), shorter while that leaves under two
   // thousand warps: few rows then spread over the GPU.
-  int run = 32;
+  int run = 64;
   while (run > 4 && (long long)vecs * a.B * ((a.T + run - 1) / run) < 65536) run /= 2;
   const int runs = (a.T + run - 1) / run;
   const long long items = (long long)vecs * runs * a.B;
@@ -358,7 +362,7 @@ cudaError_t fwd(const ConvArgs& a, cudaStream_t s) {
 
 template <typename T, int W, int ACT, bool WIDE>
 cudaError_t step(const ConvArgs& a, cudaStream_t s) {
-  const int vecs = (a.D() + 7) / 8;
+  const int vecs = (a.D() + kC - 1) / kC;
   const long long items = (long long)vecs * a.B;
   conv_step_kernel<T, W, ACT, WIDE><<<(unsigned)((items + 127) / 128), 128, 0, s>>>(a, vecs);
   return cudaGetLastError();
@@ -366,7 +370,7 @@ cudaError_t step(const ConvArgs& a, cudaStream_t s) {
 
 template <typename T, int W, int ACT, bool WIDE>
 cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
-  const int D = a.D(), vecs = (D + kBwdC - 1) / kBwdC, cblocks = (vecs + kBwdLanes - 1) / kBwdLanes;
+  const int D = a.D(), vecs = (D + kC - 1) / kC, cblocks = (vecs + kBwdLanes - 1) / kBwdLanes;
   const int rows = conv_bwd_rows(a.B, a.T, D);
   conv_bwd_kernel<T, W, ACT, WIDE>
       <<<(unsigned)((long long)rows * cblocks), dim3(kBwdLanes, kBwdRuns), 0, s>>>(

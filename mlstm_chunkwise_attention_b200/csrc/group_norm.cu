@@ -62,11 +62,43 @@ __device__ __forceinline__ void load_affine(const NormArgs& a, int c, int n, flo
 // together write neighbouring parts of the same tokens.
 // ---------------------------------------------------------------------------
 
+// Walks rows r, r + step, .. of [B, T] without a division per row.
+struct RowWalk {
+  int b, t;
+  __device__ __forceinline__ RowWalk(int r, int T) : b(r / T), t(r % T) {}
+  __device__ __forceinline__ void advance(int step, int T) {
+    t += step;
+    if (t >= T) {
+      b += t / T;
+      t %= T;
+    }
+  }
+  __device__ __forceinline__ long long at(const Rows& r, int head) const {
+    return b * r.sb + t * r.st + head * r.sh;
+  }
+};
+
+// What a lane holds of one row, still as it lies in memory.
+template <typename T, int K, int TENSORS>
+struct RowLoads {
+  Raw<T, 8> r[TENSORS][K];
+  template <bool WIDE>
+  __device__ __forceinline__ void load(int i, const T* row, const int* c, const int* n) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      zero_raw(r[i][k]);
+      if (n[k] > 0) load_raw<WIDE>(row + c[k], r[i][k], n[k]);
+    }
+  }
+};
+
+// Each row's loads are issued before the row before it is worked on, so a lane always has one
+// row in flight: without that the kernels waited on memory at 3.7 TB/s.
 template <typename T, int LANES, int K, bool GATED, bool WIDE>
 __global__ void __launch_bounds__(kThreads) norm_token_fwd_kernel(NormArgs a, int blocks) {
   constexpr int ROWS = kThreads / LANES;
   const int head = blockIdx.x % a.NH, lane = threadIdx.x % LANES;
-  const int tokens = a.B * a.T, d = a.d;
+  const int tokens = a.B * a.T, d = a.d, step = blocks * ROWS;
   int c[K], n[K];
   float w[K][8], bias[K][8];
 #pragma unroll
@@ -76,134 +108,150 @@ __global__ void __launch_bounds__(kThreads) norm_token_fwd_kernel(NormArgs a, in
     load_affine<WIDE>(a, head * d + c[k], n[k], w[k], bias[k]);
   }
   const float inv_d = 1.f / d;
-  // whole warps stay in the loop together: rows past the end repeat the last one unstored
-  for (int r0 = (blockIdx.x / a.NH) * ROWS; r0 < tokens; r0 += blocks * ROWS) {
-    const int r = r0 + threadIdx.x / LANES;
+  int r = (blockIdx.x / a.NH) * ROWS + threadIdx.x / LANES;
+  RowWalk cur(r, a.T);
+  RowLoads<T, K, 1 + GATED> next = {};
+  auto fetch = [&](const RowWalk& q) {
+    next.template load<WIDE>(0, (const T*)a.x.p + q.at(a.x, head), c, n);
+    if (GATED) next.template load<WIDE>(GATED, (const T*)a.gate.p + q.at(a.gate, head), c, n);
+  };
+  if (r < tokens) fetch(cur);
+  // whole warps stay in the loop together; rows past the end compute on what they hold, unstored
+  for (int r0 = (blockIdx.x / a.NH) * ROWS; r0 < tokens; r0 += step) {
     const bool live = r < tokens;
-    const int tok = live ? r : tokens - 1, b = tok / a.T, t = tok % a.T;
-    const T* x = (const T*)a.x.p + b * a.x.sb + t * a.x.st + head * a.x.sh;
-    float v[K][8], g[K][8], s = 0.f;
+    const RowLoads<T, K, 1 + GATED> now = next;
+    const RowWalk at = cur;
+    r += step;
+    cur.advance(step, a.T);
+    if (r < tokens) fetch(cur);
+    float2 v[K][4], s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (n[k] > 0) {
-        load8<WIDE>(x + c[k], v[k], n[k]);
-        if (GATED)
-          load8<WIDE>((const T*)a.gate.p + b * a.gate.sb + t * a.gate.st + head * a.gate.sh + c[k], g[k],
-                      n[k]);
-      } else {
+      expand(now.r[0][k], v[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[k][i];
+      for (int i = 0; i < 4; ++i) s = add2(s, v[k][i]);
     }
-    const float mean = lanes_sum<LANES>(s) * inv_d;
-    s = 0.f;
+    const float mean = lanes_sum<LANES>(s.x + s.y) * inv_d;
+    const float2 neg = make_float2(-mean, -mean);
+    s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[k][i] -= mean;
-        if (WIDE ? n[k] > 0 : i < n[k]) s = fmaf(v[k][i], v[k][i], s);
+      for (int i = 0; i < 4; ++i) {
+        v[k][i] = add2(v[k][i], neg);
+        // channels that do not exist do not count
+        if (WIDE ? n[k] > 0 : 2 * i + 1 < n[k])
+          s = fma2(v[k][i], v[k][i], s);
+        else if (2 * i < n[k])
+          s.x = fmaf(v[k][i].x, v[k][i].x, s.x);
       }
-    const float rstd = rsqrtf(fmaf(lanes_sum<LANES>(s), inv_d, a.eps));
+    const float rstd = rsqrtf(fmaf(lanes_sum<LANES>(s.x + s.y), inv_d, a.eps));
     if (!live) continue;
-    T* y = (T*)a.y.p + b * a.y.sb + t * a.y.st + head * a.y.sh;
+    T* y = (T*)a.y.p + at.at(a.y, head);
+    const float2 rs = make_float2(rstd, rstd);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (n[k] > 0) {
-        float o[8];
+        float2 g[4];
+        if (GATED) expand(now.r[GATED][k], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = fmaf(v[k][i] * rstd, w[k][i], bias[k][i]);
+        for (int i = 0; i < 4; ++i) {
+          float2 o = fma2(mul2(v[k][i], rs), make_float2(w[k][2 * i], w[k][2 * i + 1]),
+                          make_float2(bias[k][2 * i], bias[k][2 * i + 1]));
           if (GATED)
-            o[i] *= act_run(a.act, g[k][i]);
+            v[k][i] = mul2(o, make_float2(act_run(a.act, g[i].x), act_run(a.act, g[i].y)));
           else
-            o[i] = act_run(a.act, o[i]);
+            v[k][i] = make_float2(act_run(a.act, o.x), act_run(a.act, o.y));
         }
-        store8<WIDE>(y + c[k], o, n[k]);
+        store_pairs<WIDE, 8>(y + c[k], v[k], n[k]);
       }
     }
     if (a.stats != nullptr && lane == 0)
-      reinterpret_cast<float2*>(a.stats)[(long long)tok * a.NH + head] = make_float2(mean, rstd);
+      reinterpret_cast<float2*>(a.stats)[((long long)at.b * a.T + at.t) * a.NH + head] =
+          make_float2(mean, rstd);
   }
 }
 
 // ws: rows of partial sums [blocks, 2, NH d] (dw, then dbias).
 template <typename T, int LANES, int K, bool GATED, bool WIDE>
-__global__ void __launch_bounds__(kThreads) norm_token_bwd_kernel(NormArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_token_bwd_kernel(NormArgs a, int blocks) {
   constexpr int ROWS = kThreads / LANES, CH = LANES * K * 8;
   __shared__ float red[kThreads / 32][2][CH];
   const int head = blockIdx.x % a.NH, block = blockIdx.x / a.NH, lane = threadIdx.x % LANES;
-  const int tokens = a.B * a.T, d = a.d;
+  const int tokens = a.B * a.T, d = a.d, step = blocks * ROWS;
   int c[K], n[K];
-  float w[K][8], bias[K][8], dw[K][8], db[K][8];
+  float w[K][8], bias[K][8];
+  float2 dw[K][4], db[K][4];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     c[k] = (k * LANES + lane) * 8;
     n[k] = max(0, min(8, d - c[k]));
     load_affine<WIDE>(a, head * d + c[k], n[k], w[k], bias[k]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.f;
+    for (int i = 0; i < 4; ++i) dw[k][i] = db[k][i] = make_float2(0.f, 0.f);
   }
   const float inv_d = 1.f / d;
-  for (int r0 = block * ROWS; r0 < tokens; r0 += blocks * ROWS) {
-    const int r = r0 + threadIdx.x / LANES;
+  int r = block * ROWS + threadIdx.x / LANES;
+  RowWalk cur(r, a.T);
+  RowLoads<T, K, 2 + GATED> next = {};
+  float2 next_ms = make_float2(0.f, 0.f);
+  auto fetch = [&](const RowWalk& q) {
+    next_ms = reinterpret_cast<const float2*>(a.stats)[((long long)q.b * a.T + q.t) * a.NH + head];
+    next.template load<WIDE>(0, (const T*)a.x.p + q.at(a.x, head), c, n);
+    next.template load<WIDE>(1, (const T*)a.y.p + q.at(a.y, head), c, n);
+    if (GATED) next.template load<WIDE>(1 + GATED, (const T*)a.gate.p + q.at(a.gate, head), c, n);
+  };
+  if (r < tokens) fetch(cur);
+  for (int r0 = block * ROWS; r0 < tokens; r0 += step) {
     const bool live = r < tokens;
-    const int tok = live ? r : tokens - 1, b = tok / a.T, t = tok % a.T;
-    const float2 ms = reinterpret_cast<const float2*>(a.stats)[(long long)tok * a.NH + head];
-    const T* x = (const T*)a.x.p + b * a.x.sb + t * a.x.st + head * a.x.sh;
-    const T* dy = (const T*)a.y.p + b * a.y.sb + t * a.y.st + head * a.y.sh;
-    const T* gp = GATED ? (const T*)a.gate.p + b * a.gate.sb + t * a.gate.st + head * a.gate.sh : nullptr;
-    float v[K][8], q[K][8], g[K][8], s1 = 0.f, s2 = 0.f;
+    const RowLoads<T, K, 2 + GATED> now = next;
+    const float2 ms = next_ms;
+    const RowWalk at = cur;
+    r += step;
+    cur.advance(step, a.T);
+    if (r < tokens) fetch(cur);
+    float2 v[K][4], q[K][4], s1 = make_float2(0.f, 0.f), s2 = s1;
+    const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (n[k] > 0) {
-        load8<WIDE>(x + c[k], v[k], n[k]);
-        load8<WIDE>(dy + c[k], q[k], n[k]);
-        if (GATED) load8<WIDE>(gp + c[k], g[k], n[k]);
-      }
-    }
+      float2 g[4], dg[4];
+      expand(now.r[0][k], v[k]);
+      expand(now.r[1][k], q[k]);
+      if (GATED) expand(now.r[1 + GATED][k], g);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float dg[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (WIDE ? n[k] > 0 : i < n[k]) {
-          const float xh = (v[k][i] - ms.x) * ms.y, nn = fmaf(xh, w[k][i], bias[k][i]);
-          float val, slope, dn;
-          if (GATED) {
-            slope_run(a.act, g[k][i], &val, &slope);
-            dg[i] = q[k][i] * nn * slope;
-            dn = q[k][i] * val;
-          } else {
-            slope_run(a.act, nn, &val, &slope);
-            dn = q[k][i] * slope;
-          }
-          if (live) {
-            dw[k][i] = fmaf(dn, xh, dw[k][i]);
-            db[k][i] += dn;
-          }
-          const float dxh = dn * w[k][i];
-          s1 += dxh;
-          s2 = fmaf(dxh, xh, s2);
-          v[k][i] = xh;
-          q[k][i] = dxh;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float2 wi = make_float2(w[k][2 * i], w[k][2 * i + 1]);
+        const float2 xh = mul2(add2(v[k][i], neg), rs);
+        const float2 nn = fma2(xh, wi, make_float2(bias[k][2 * i], bias[k][2 * i + 1]));
+        const float2 of = GATED ? g[i] : nn;
+        float2 val, slope;
+        slope_run(a.act, of.x, &val.x, &slope.x);
+        slope_run(a.act, of.y, &val.y, &slope.y);
+        float2 dn = mul2(q[k][i], GATED ? val : slope);
+        if (GATED) dg[i] = mul2(mul2(q[k][i], nn), slope);
+        if (!live || 2 * i >= n[k]) dn.x = 0.f;  // nothing from rows or channels that do not exist
+        if (!live || 2 * i + 1 >= n[k]) dn.y = 0.f;
+        dw[k][i] = fma2(dn, xh, dw[k][i]);
+        db[k][i] = add2(db[k][i], dn);
+        const float2 dxh = mul2(dn, wi);
+        s1 = add2(s1, dxh);
+        s2 = fma2(dxh, xh, s2);
+        v[k][i] = xh;
+        q[k][i] = dxh;
       }
       if (GATED && live && n[k] > 0)
-        store8<WIDE>((T*)a.dgate.p + b * a.dgate.sb + t * a.dgate.st + head * a.dgate.sh + c[k], dg, n[k]);
+        store_pairs<WIDE, 8>((T*)a.dgate.p + at.at(a.dgate, head) + c[k], dg, n[k]);
     }
-    const float m1 = lanes_sum<LANES>(s1) * inv_d, m2 = lanes_sum<LANES>(s2) * inv_d;
+    const float m1 = lanes_sum<LANES>(s1.x + s1.y) * inv_d, m2 = lanes_sum<LANES>(s2.x + s2.y) * inv_d;
     if (!live) continue;
-    T* dx = (T*)a.dx.p + b * a.dx.sb + t * a.dx.st + head * a.dx.sh;
+    T* dx = (T*)a.dx.p + at.at(a.dx, head);
+    const float2 n1 = make_float2(-m1, -m1), n2 = make_float2(-m2, -m2);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (n[k] > 0) {
-        float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = ms.y * (q[k][i] - m1 - v[k][i] * m2);
-        store8<WIDE>(dx + c[k], o, n[k]);
+        for (int i = 0; i < 4; ++i) q[k][i] = mul2(rs, fma2(v[k][i], n2, add2(q[k][i], n1)));
+        store_pairs<WIDE, 8>(dx + c[k], q[k], n[k]);
       }
     }
   }
@@ -213,14 +261,15 @@ __global__ void __launch_bounds__(kThreads) norm_token_bwd_kernel(NormArgs a, in
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      float sw = i & 1 ? dw[k][i / 2].y : dw[k][i / 2].x, sb = i & 1 ? db[k][i / 2].y : db[k][i / 2].x;
 #pragma unroll
       for (int o = LANES; o < 32; o <<= 1) {
-        dw[k][i] += __shfl_xor_sync(0xffffffffu, dw[k][i], o);
-        db[k][i] += __shfl_xor_sync(0xffffffffu, db[k][i], o);
+        sw += __shfl_xor_sync(0xffffffffu, sw, o);
+        sb += __shfl_xor_sync(0xffffffffu, sb, o);
       }
       if ((threadIdx.x & 31) < LANES) {
-        red[threadIdx.x / 32][0][c[k] + i] = dw[k][i];
-        red[threadIdx.x / 32][1][c[k] + i] = db[k][i];
+        red[threadIdx.x / 32][0][c[k] + i] = sw;
+        red[threadIdx.x / 32][1][c[k] + i] = sb;
       }
     }
   __syncthreads();
