@@ -95,7 +95,8 @@ int mlstm_conv_step(const mlstm_rows_t* x, const float* weight, const float* bia
  * x, dt, z, y [B, T, D] (head strides ignored); b, c [B, T, G, N] (head: the
  * stride between groups); a [D, N]; skip, dt_bias [D] or NULL (zeros); z.data
  * NULL: no gate.  state_in, state_out [B, D, N] fp32 contiguous, the state
- * before the first and after the last token; NULL: zeros / not wanted.
+ * before the first and after the last token; NULL: zeros / not wanted.  States,
+ * saved and workspaces are 16-byte aligned.
  * ------------------------------------------------------------------------- */
 typedef struct {
   mlstm_rows_t x, dt, z, b, c;
@@ -108,10 +109,15 @@ typedef struct {
  * states entering every eighth token, fp32 (0 on an argument error). */
 size_t mlstm_scan_saved_size(int B, int T, int D, int G, int N, int dtype);
 
+/* Bytes of workspace mlstm_scan_fwd needs; may be 0, and then the workspace
+ * may be NULL (0 on an argument error too).  Few long sequences are cut into
+ * segments that are scanned at once, whose states lie there. */
+size_t mlstm_scan_fwd_workspace_size(int B, int T, int D, int G, int N, int dtype);
+
 /* Forward.  saved NULL: no backward will follow.  state_out must not overlap
  * state_in.  T = 0 copies state_in (or zeros) to state_out. */
 int mlstm_scan_fwd(const mlstm_scan_t* p, const mlstm_rows_t* y, void* saved, float* state_out,
-                   void* stream);
+                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace mlstm_scan_bwd needs (0 on an argument error). */
 size_t mlstm_scan_bwd_workspace_size(int B, int T, int D, int G, int N, int dtype);

@@ -98,7 +98,8 @@ EXPORTS = {
                        [_I] * 7 + [_P]),
     "mlstm_conv_step": (_I, [_ROWS, _P, _P, _P, _ROWS, _P] + [_I] * 6 + [_P]),
     "mlstm_scan_saved_size": (ctypes.c_size_t, [_I] * 6),
-    "mlstm_scan_fwd": (_I, [ctypes.POINTER(ScanProblem), _ROWS, _P, _P, _P]),
+    "mlstm_scan_fwd_workspace_size": (ctypes.c_size_t, [_I] * 6),
+    "mlstm_scan_fwd": (_I, [ctypes.POINTER(ScanProblem), _ROWS, _P, _P, _P, ctypes.c_size_t, _P]),
     "mlstm_scan_bwd_workspace_size": (ctypes.c_size_t, [_I] * 6),
     "mlstm_scan_bwd": (_I, [ctypes.POINTER(ScanProblem), _ROWS, _P, _P, ctypes.POINTER(ScanGrads), _P,
                             ctypes.c_size_t, _P]),

@@ -299,7 +299,10 @@ def selective_scan_forward(x, dt, A, B, C, *, skip=None, z=None, dt_bias=None, s
         saved = (_bytes(load().mlstm_scan_saved_size(p.B, p.T, p.D, p.G, p.N, p.dtype), x)
                  if keep_saved else None)
         state_out = x.new_empty((p.B, p.D, p.N), dtype=torch.float32) if want_state else None
-        _check(load().mlstm_scan_fwd(p, _rows(y), _ptr(saved), _ptr(state_out), s), "mlstm_scan_fwd")
+        need = load().mlstm_scan_fwd_workspace_size(p.B, p.T, p.D, p.G, p.N, p.dtype)
+        ws = _bytes(need, x) if need else None
+        _check(load().mlstm_scan_fwd(p, _rows(y), _ptr(saved), _ptr(state_out), _ptr(ws), need, s),
+               "mlstm_scan_fwd")
         return y, saved, state_out
 
     return _on(stream, x, (dt, A, B, C, skip, z, dt_bias, state_in), launch)

@@ -57,12 +57,21 @@ struct ScanArgs {
   float *dA, *dskip, *ddt_bias, *dstate_in;
   const float* dstate_out;
   float *part_bc, *part_a, *part_d;
+  // the sequence's segments (one: the whole of it)
+  float *seg_state, *seg_sum;   // [segs, B, D, scan_pad(N)], [segs, B, D]
+  int seg_len, segs;
   int B, T, D, G, N, softplus, dtype;
   bool wide, wide_bc;           // 16-byte accesses of the [B, T, D] tensors / of B and C
 };
 constexpr int kScanEvery = 8;  // tokens between two saved states
 // States per channel as the kernels hold them: four to a lane, 2, 4, 8 or 16 lanes to a channel.
 inline int scan_pad(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
+// How the sequence is cut: into segments of `len` tokens (a multiple of the kernels' tiles) that
+// are scanned at once, where whole sequences are too few to fill the GPU.
+struct ScanSegments {
+  int len, count;
+};
+ScanSegments scan_segments(int B, int T, int D, int N);
 struct ScanBwdSizes {
   int tiles;                    // channel tiles of one group
   size_t part_bc, part_a, part_d;  // floats
@@ -70,6 +79,7 @@ struct ScanBwdSizes {
 ScanBwdSizes scan_bwd_sizes(int B, int T, int D, int G, int N);
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
+cudaError_t launch_scan_reverse_segments(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t s);
 
 // ---- group norm --------------------------------------------------------------

@@ -85,16 +85,30 @@ int fill(void* dst, const void* src, size_t bytes, void* stream, const char* whe
 }
 
 struct ScanWorkspace {
-  size_t bc, a, d, total;
+  size_t seg_state, seg_sum, bc, a, d, total;
 };
-ScanWorkspace scan_workspace(int B, int T, int D, int G, int N) {
-  const mlstm::ScanBwdSizes z = mlstm::scan_bwd_sizes(B, T, D, G, N);
-  ScanWorkspace w;
-  w.bc = 0;
-  w.a = align256(z.part_bc * 4);
-  w.d = align256(w.a + z.part_a * 4);
-  w.total = align256(w.d + z.part_d * 4);
+// The forward's workspace holds the segments alone (nothing for a whole sequence).
+ScanWorkspace scan_workspace(int B, int T, int D, int G, int N, bool backward) {
+  ScanWorkspace w = {};
+  const mlstm::ScanSegments g = mlstm::scan_segments(B, T, D, N);
+  const size_t rows = g.count > 1 ? (size_t)g.count * B * D : 0;
+  w.seg_sum = align256(rows * mlstm::scan_pad(N) * 4);
+  w.bc = align256(w.seg_sum + rows * 4);
+  w.total = w.bc;
+  if (backward) {
+    const mlstm::ScanBwdSizes z = mlstm::scan_bwd_sizes(B, T, D, G, N);
+    w.a = align256(w.bc + z.part_bc * 4);
+    w.d = align256(w.a + z.part_a * 4);
+    w.total = align256(w.d + z.part_d * 4);
+  }
   return w;
+}
+void use_segments(mlstm::ScanArgs* a, char* ws, const ScanWorkspace& w) {
+  const mlstm::ScanSegments g = mlstm::scan_segments(a->B, a->T, a->D, a->N);
+  a->seg_len = g.len;
+  a->segs = g.count;
+  a->seg_state = (float*)(ws + w.seg_state);
+  a->seg_sum = (float*)(ws + w.seg_sum);
 }
 
 // The inputs of a scan call; T is that of the call (1 for a step).
@@ -233,8 +247,13 @@ size_t mlstm_scan_saved_size(int B, int T, int D, int G, int N, int dtype) {
   return (size_t)B * NC * D * mlstm::scan_pad(N) * 4;
 }
 
+size_t mlstm_scan_fwd_workspace_size(int B, int T, int D, int G, int N, int dtype) {
+  if (check_scan(B, T, D, G, N, dtype) != MLSTM_OK) return 0;
+  return scan_workspace(B, T, D, G, N, false).total;
+}
+
 int mlstm_scan_fwd(const mlstm_scan_t* p, const mlstm_rows_t* y, void* saved, float* state_out,
-                   void* stream) {
+                   void* workspace, size_t workspace_bytes, void* stream) {
   if (p == nullptr) return MLSTM_ERR_INVALID;
   int st = check_scan(p->B, p->T, p->D, p->G, p->N, p->dtype);
   if (st != MLSTM_OK) return st;
@@ -248,6 +267,10 @@ int mlstm_scan_fwd(const mlstm_scan_t* p, const mlstm_rows_t* y, void* saved, fl
   a.y = rows_of(y, p->B, p->T, 1);
   if (bad_rows(a.y, p->dtype)) return MLSTM_ERR_INVALID;
   a.wide = a.wide && aligned(a.y, p->dtype);
+  const ScanWorkspace w = scan_workspace(p->B, p->T, p->D, p->G, p->N, false);
+  if (off16(workspace)) return MLSTM_ERR_INVALID;
+  if (w.total > 0 && (workspace == nullptr || workspace_bytes < w.total)) return MLSTM_ERR_WORKSPACE;
+  use_segments(&a, (char*)workspace, w);
   a.state_out = state_out;
   a.saved = (float*)saved;
   if ((st = pending_error("before mlstm_scan_fwd")) != MLSTM_OK) return st;
@@ -273,7 +296,7 @@ int mlstm_scan_step(const mlstm_scan_t* p, const mlstm_rows_t* y, float* state_o
 
 size_t mlstm_scan_bwd_workspace_size(int B, int T, int D, int G, int N, int dtype) {
   if (check_scan(B, T, D, G, N, dtype) != MLSTM_OK) return 0;
-  return scan_workspace(B, T, D, G, N).total;
+  return scan_workspace(B, T, D, G, N, true).total;
 }
 
 int mlstm_scan_bwd(const mlstm_scan_t* p, const mlstm_rows_t* dy, const void* saved,
@@ -309,7 +332,7 @@ int mlstm_scan_bwd(const mlstm_scan_t* p, const mlstm_rows_t* dy, const void* sa
       bad_rows(a.dc, dt) || (gate && bad_rows(a.dz, dt)) || saved == nullptr || off16(saved) ||
       off16(workspace))
     return MLSTM_ERR_INVALID;
-  const ScanWorkspace w = scan_workspace(B, T, D, p->G, p->N);
+  const ScanWorkspace w = scan_workspace(B, T, D, p->G, p->N, true);
   if (workspace == nullptr || workspace_bytes < w.total) return MLSTM_ERR_WORKSPACE;
   a.wide = a.wide && aligned(a.y, dt) && aligned(a.dx, dt) && aligned(a.ddt, dt) &&
            (!gate || aligned(a.dz, dt));
@@ -318,6 +341,7 @@ int mlstm_scan_bwd(const mlstm_scan_t* p, const mlstm_rows_t* dy, const void* sa
   a.dA = grads->da; a.dskip = grads->dskip; a.ddt_bias = grads->ddt_bias;
   a.dstate_in = grads->dstate_in;
   char* ws = (char*)workspace;
+  use_segments(&a, ws, w);
   a.part_bc = (float*)(ws + w.bc);
   a.part_a = (float*)(ws + w.a);
   a.part_d = (float*)(ws + w.d);

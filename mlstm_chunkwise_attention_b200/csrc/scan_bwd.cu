@@ -19,154 +19,220 @@ namespace mlstm {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = 16;
+static_assert(kTile == 2 * kScanEvery, "two saved states to a tile");
 
-template <int LPC>
+template <typename T, int LPC>
 struct Cfg {
   static constexpr int NP = 4 * LPC;
   static constexpr int CL = 32 / LPC;         // channel lanes of a warp
   static constexpr int CT = kWarps * CL * 2;  // channels of a CTA
-  static constexpr int VECS = CT / 8;
-  static constexpr int ITEMS = (kTile * VECS + kThreads - 1) / kThreads;
-  // shared memory, in floats: delta, delta x, dy [tile][CT]; sums over states [3][tile][CT];
-  // B and C [tile][2 NP]; dB and dC of each warp [warps][tile][2 NP]; dskip and ddt_bias
-  // shares of each thread's channels [16][threads]
-  static constexpr int DT = 0, DTX = DT + kTile * CT, DY = DTX + kTile * CT, SUM = DY + kTile * CT,
-                       BC = SUM + 3 * kTile * CT, RED = BC + kTile * 2 * NP,
-                       ACC = RED + kWarps * kTile * 2 * NP, TOTAL = ACC + 16 * kThreads;
+  static constexpr int VECS = CT / 8, UNITS = kTile * VECS;
+  static constexpr int ITEMS = (UNITS + kThreads - 1) / kThreads;  // units of a thread
+  // shared memory, in floats: (delta, delta x) and dy of the tile; sums over states of g B, u A and
+  // C s; B and C [tile][2 NP]; dB and dC of each warp [warps][tile][2 NP]; dskip and ddt_bias
+  // shares of each thread's channels [16][threads]; dt_bias and skip; two saved states ahead
+  // [2][2][threads] of four floats; and two tiles of x, dt, dy, z as they lie in memory
+  static constexpr int DX = 0, DY = DX + UNITS * kPairUnit * 2, SUM = DY + UNITS * kFloatUnit,
+                       BC = SUM + 3 * UNITS * kFloatUnit, RED = BC + kTile * 2 * NP,
+                       ACC = RED + kWarps * kTile * 2 * NP, BIAS = ACC + 16 * kThreads, SKIP = BIAS + CT,
+                       SAVED = SKIP + CT, RAW = SAVED + 16 * kThreads,
+                       TOTAL = RAW + 2 * 4 * UNITS * 8 * (int)sizeof(T) / 4;
 };
 
 template <typename T, int LPC, bool GATE, bool WIDE>
 __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tiles) {
-  using C = Cfg<LPC>;
-  constexpr int NP = C::NP, CL = C::CL, CT = C::CT, VECS = C::VECS;
+  using C = Cfg<T, LPC>;
+  constexpr int NP = C::NP, CL = C::CL, CT = C::CT, VECS = C::VECS, UNITS = C::UNITS;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, nl = lane % LPC, cr = lane / LPC;
   const int cl = (warp * CL + cr) * 2;  // the lane's two channels within the tile
-  const int b = blockIdx.x / (tiles * a.G), ti = blockIdx.x % (tiles * a.G);
+  const int per_seg = a.B * a.G * tiles, seg = blockIdx.x / per_seg, bi = blockIdx.x % per_seg;
+  const int b = bi / (tiles * a.G), ti = bi % (tiles * a.G);
   const ChannelTile q = channel_tile(a, ti, tiles, CT);
   const int NC = (a.T + kScanEvery - 1) / kScanEvery;
-  float A2[2][4], G[2][4], dA[2][4];
+  const int first = seg * a.seg_len, last = min(first + a.seg_len, a.T);
+  float2 A2[2][2], G[2][2], dA[2][2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
+  for (int e = 0; e < 2; ++e) {
+    float av[4], gv[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int n = nl * 4 + k;
       const bool on = cl + e < q.n && n < a.N;
-      A2[e][k] = on ? a.A[(long long)(q.c0 + cl + e) * a.N + n] * kLog2e : 0.f;
-      G[e][k] = on && a.dstate_out != nullptr
-                    ? a.dstate_out[((long long)b * a.D + q.c0 + cl + e) * a.N + n]
-                    : 0.f;
-      dA[e][k] = 0.f;
+      av[k] = on ? a.A[(long long)(q.c0 + cl + e) * a.N + n] * kLog2e : 0.f;
+      gv[k] = on && a.dstate_out != nullptr
+                  ? a.dstate_out[((long long)b * a.D + q.c0 + cl + e) * a.N + n]
+                  : 0.f;
     }
 #pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      A2[e][p] = make_float2(av[2 * p], av[2 * p + 1]);
+      G[e][p] = make_float2(gv[2 * p], gv[2 * p + 1]);
+      dA[e][p] = make_float2(0.f, 0.f);
+    }
+    if (cl + e < q.n) enter_segment<NP, true>(a, b, q.c0 + cl + e, nl, seg, A2[e], G[e]);
+  }
+#pragma unroll
   for (int i = 0; i < 16; ++i) sm[C::ACC + i * kThreads + tid] = 0.f;
-  const T* xp = (const T*)a.x.p + b * a.x.sb + q.c0;
-  const T* dp = (const T*)a.dt.p + b * a.dt.sb + q.c0;
-  const T* zp = GATE ? (const T*)a.z.p + b * a.z.sb + q.c0 : nullptr;
-  const T* gp = (const T*)a.y.p + b * a.y.sb + q.c0;
-
-  for (int t0 = (a.T - 1) / kTile * kTile; t0 >= 0; t0 -= kTile) {
+  for (int i = tid; i < CT; i += kThreads) {
+    sm[C::BIAS + i] = a.dt_bias != nullptr && i < q.n ? a.dt_bias[q.c0 + i] : 0.f;
+    sm[C::SKIP + i] = a.skip != nullptr && i < q.n ? a.skip[q.c0 + i] : 0.f;
+  }
+  const T* in[4] = {(const T*)a.x.p + b * a.x.sb + q.c0, (const T*)a.dt.p + b * a.dt.sb + q.c0,
+                    (const T*)a.y.p + b * a.y.sb + q.c0,
+                    GATE ? (const T*)a.z.p + b * a.z.sb + q.c0 : nullptr};
+  const long long stride[4] = {a.x.st, a.dt.st, a.y.st, a.z.st};
+  auto raw = [&](int stage, int tensor, int item) {
+    return reinterpret_cast<Raw<T, 8>*>(sm + C::RAW) + (stage * 4 + tensor) * UNITS + item;
+  };
+  // A thread fetches and reads only its own units, so no barrier is needed for them.
+  auto fetch = [&](int t0, int stage) {
 #pragma unroll
     for (int m = 0; m < C::ITEMS; ++m) {
-      const int item = tid + m * kThreads, t = item / VECS, cv = (item % VECS) * 8;
-      if (item < kTile * VECS) {
-        const int n = min(8, q.n - cv);
-        const bool in = t0 + t < a.T && n > 0;
-        float x[8], d[8], g[8], z[8];
-        if (in) {
-          load8<WIDE>(xp + (t0 + t) * a.x.st + cv, x, n);
-          load8<WIDE>(dp + (t0 + t) * a.dt.st + cv, d, n);
-          load8<WIDE>(gp + (t0 + t) * a.y.st + cv, g, n);
-          if (GATE) load8<WIDE>(zp + (t0 + t) * a.z.st + cv, z, n);
-        }
+      const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
+      if (item < UNITS) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float delta = 0.f, dx = 0.f, dy = 0.f;
-          if (in && i < n) {
-            delta = d[i] + (a.dt_bias != nullptr ? a.dt_bias[q.c0 + cv + i] : 0.f);
-            if (a.softplus) delta = softplusf(delta);
-            dx = delta * x[i];
-            dy = GATE ? g[i] * act_value<kActSilu>(z[i]) : g[i];
+        for (int k = 0; k < 3 + GATE; ++k) {
+          Raw<T, 8>* to = raw(stage, k, item);
+          const T* from = in[k] + t * stride[k] + cv;
+          if (t < last && n > 0) {
+            if (WIDE) {
+#pragma unroll
+              for (int h = 0; h < (int)sizeof(Raw<T, 8>) / 16; ++h)
+                copy16_async((char*)to + 16 * h, (const char*)from + 16 * h);
+            } else {
+              Raw<T, 8> r;
+              load_raw<false>(from, r, n);
+              *to = r;
+            }
+          } else {
+            zero_raw(*to);
           }
-          sm[C::DT + t * CT + cv + i] = delta;
-          sm[C::DTX + t * CT + cv + i] = dx;
-          sm[C::DY + t * CT + cv + i] = dy;
         }
       }
     }
-    stage_bc<T, NP, kTile>(a, b, q.g, t0, sm + C::BC, tid, kThreads);
+  };
+  // The lane's states entering the eight tokens from t on; each thread reads its own slots.
+  auto fetch_saved = [&](int t, int stage) {
+    if (t < first) return;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (cl + e < q.n && t < last)
+        copy16_async(sm + C::SAVED + ((stage * 2 + e) * kThreads + tid) * 4,
+                     a.saved + (((long long)b * NC + t / kScanEvery) * a.D + q.c0 + cl + e) * NP + nl * 4);
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // channels that do not exist keep a state of zero
+    *reinterpret_cast<float4*>(sm + C::SAVED + (i * kThreads + tid) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int top = (last - 1 - first) / kTile * kTile + first;
+  fetch(top, 0);
+  fetch_saved(top + kTile - kScanEvery, 0);  // the first eight tokens taken lie in stage 0
+  copies_commit();
+  int stage = 0;
+  __syncthreads();
+  for (int t0 = top; t0 >= first; t0 -= kTile, stage ^= 1) {
+    stage_bc<T, NP, kTile>(a, b, q.g, t0, last, sm + C::BC, tid, kThreads);
+    copies_wait<0>();
+#pragma unroll
+    for (int m = 0; m < C::ITEMS; ++m) {
+      const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
+      if (item < UNITS) {
+        stage_delta<T>(a, *raw(stage, 0, item), *raw(stage, 1, item), sm + C::BIAS + cv, t < last, n,
+                       reinterpret_cast<float2*>(sm + C::DX) + item * kPairUnit);
+        float2 g[4], z[4];
+        expand(*raw(stage, 2, item), g);
+        if (GATE) {
+          expand(*raw(stage, 3, item), z);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            g[i] = mul2(g[i], make_float2(act_value<kActSilu>(z[i].x), act_value<kActSilu>(z[i].y)));
+        }
+        store_unit(sm + C::DY + item * kFloatUnit, g);
+      }
+    }
+    if (t0 - kTile >= first) fetch(t0 - kTile, stage ^ 1);
+    copies_commit();
     __syncthreads();
 #pragma unroll 1
     for (int sub = kTile - kScanEvery; sub >= 0; sub -= kScanEvery) {
-      if (t0 + sub >= a.T) continue;
-      float h0[2][4], s[kScanEvery][2][4], ev[kScanEvery][2][4];
+      const int half = sub / kScanEvery;  // the upper eight tokens' states lie in stage 0, the lower's in 1
+      fetch_saved(t0 + sub - kScanEvery, half);
+      copies_commit();
+      if (half == 0) copies_wait<1>();  // the upper's were waited for with the tile
+      if (t0 + sub >= last) continue;
+      float2 h0[2][2], s[kScanEvery][2][2], ev[kScanEvery][2][2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (cl + e < q.n)
-          v = *reinterpret_cast<const float4*>(
-              a.saved + (((long long)b * NC + (t0 + sub) / kScanEvery) * a.D + q.c0 + cl + e) * NP + nl * 4);
-        h0[e][0] = v.x; h0[e][1] = v.y; h0[e][2] = v.z; h0[e][3] = v.w;
+        const float4 v =
+            *reinterpret_cast<const float4*>(sm + C::SAVED + (((half ^ 1) * 2 + e) * kThreads + tid) * 4);
+        h0[e][0] = make_float2(v.x, v.y);
+        h0[e][1] = make_float2(v.z, v.w);
       }
 #pragma unroll
       for (int i = 0; i < kScanEvery; ++i) {
-        const int t = sub + i;
-        const float2 dt = *reinterpret_cast<const float2*>(sm + C::DT + t * CT + cl);
-        const float2 dtx = *reinterpret_cast<const float2*>(sm + C::DTX + t * CT + cl);
+        const int t = sub + i, unit = t * VECS + cl / 8;
+        const float4 d = *reinterpret_cast<const float4*>(sm + C::DX + unit * kPairUnit * 2 + (cl % 8) * 2);
         const float4 Bq = *reinterpret_cast<const float4*>(sm + C::BC + t * 2 * NP + nl * 4);
-        const float Bv[4] = {Bq.x, Bq.y, Bq.z, Bq.w};
-        const float dtv[2] = {dt.x, dt.y}, dxv[2] = {dtx.x, dtx.y};
+        const float2 Bv[2] = {make_float2(Bq.x, Bq.y), make_float2(Bq.z, Bq.w)};
+        const float2 dd[2] = {make_float2(d.x, d.x), make_float2(d.z, d.z)};
+        const float2 dx[2] = {make_float2(d.y, d.y), make_float2(d.w, d.w)};
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            ev[i][e][k] = exp2_fast(dtv[e] * A2[e][k]);
-            s[i][e][k] = fmaf(ev[i][e][k], i == 0 ? h0[e][k] : s[i - 1][e][k], dxv[e] * Bv[k]);
+          for (int p = 0; p < 2; ++p) {
+            ev[i][e][p] = exp2_pair(mul2(dd[e], A2[e][p]));
+            s[i][e][p] = fma2(ev[i][e][p], i == 0 ? h0[e][p] : s[i - 1][e][p], mul2(dx[e], Bv[p]));
           }
         if (GATE) {  // the ungated output, for dz
           const float4 Cq = *reinterpret_cast<const float4*>(sm + C::BC + t * 2 * NP + NP + nl * 4);
           float y[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            y[e] = fmaf(s[i][e][0], Cq.x, fmaf(s[i][e][1], Cq.y, fmaf(s[i][e][2], Cq.z, s[i][e][3] * Cq.w)));
+          for (int e = 0; e < 2; ++e) {
+            const float2 v = fma2(s[i][e][1], make_float2(Cq.z, Cq.w), mul2(s[i][e][0], make_float2(Cq.x, Cq.y)));
+            y[e] = v.x + v.y;
+          }
           scatter_sum<2, LPC, 1>(y, nl);
-          if (nl % (LPC / 2) == 0) sm[C::SUM + (2 * kTile + t) * CT + cl + nl / (LPC / 2)] = y[0];
+          if (nl % (LPC / 2) == 0)
+            sm[C::SUM + (2 * UNITS + unit) * kFloatUnit + cl % 8 + nl / (LPC / 2)] = y[0];
         }
       }
 #pragma unroll
       for (int i = kScanEvery - 1; i >= 0; --i) {
-        const int t = sub + i;
-        const float2 dt = *reinterpret_cast<const float2*>(sm + C::DT + t * CT + cl);
-        const float2 dtx = *reinterpret_cast<const float2*>(sm + C::DTX + t * CT + cl);
-        const float2 dy = *reinterpret_cast<const float2*>(sm + C::DY + t * CT + cl);
+        const int t = sub + i, unit = t * VECS + cl / 8;
+        const float4 d = *reinterpret_cast<const float4*>(sm + C::DX + unit * kPairUnit * 2 + (cl % 8) * 2);
+        const float2 y2 = *reinterpret_cast<const float2*>(sm + C::DY + unit * kFloatUnit + cl % 8);
         const float4 Bq = *reinterpret_cast<const float4*>(sm + C::BC + t * 2 * NP + nl * 4);
         const float4 Cq = *reinterpret_cast<const float4*>(sm + C::BC + t * 2 * NP + NP + nl * 4);
-        const float Bv[4] = {Bq.x, Bq.y, Bq.z, Bq.w}, Cv[4] = {Cq.x, Cq.y, Cq.z, Cq.w};
-        const float dtv[2] = {dt.x, dt.y}, dxv[2] = {dtx.x, dtx.y}, dyv[2] = {dy.x, dy.y};
-        float bc[8], st[4] = {0.f, 0.f, 0.f, 0.f};  // dB, dC; sums of g B and of u A per channel
-#pragma unroll
-        for (int k = 0; k < 8; ++k) bc[k] = 0.f;
+        const float2 Bv[2] = {make_float2(Bq.x, Bq.y), make_float2(Bq.z, Bq.w)};
+        const float2 Cv[2] = {make_float2(Cq.x, Cq.y), make_float2(Cq.z, Cq.w)};
+        const float2 dd[2] = {make_float2(d.x, d.x), make_float2(d.z, d.z)};
+        const float2 dx[2] = {make_float2(d.y, d.y), make_float2(d.w, d.w)};
+        const float2 dy[2] = {make_float2(y2.x, y2.x), make_float2(y2.y, y2.y)};
+        float2 db[2], dc[2], gb[2], ua[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float g = fmaf(dyv[e], Cv[k], G[e][k]);
-            bc[k] = fmaf(dxv[e], g, bc[k]);
-            bc[4 + k] = fmaf(dyv[e], s[i][e][k], bc[4 + k]);
-            st[e] = fmaf(g, Bv[k], st[e]);
-            G[e][k] = ev[i][e][k] * g;
-            const float u = G[e][k] * (i == 0 ? h0[e][k] : s[i - 1][e][k]);
-            st[2 + e] = fmaf(u, A2[e][k], st[2 + e]);
-            dA[e][k] = fmaf(u, dtv[e], dA[e][k]);
+          for (int p = 0; p < 2; ++p) {
+            const float2 g = fma2(dy[e], Cv[p], G[e][p]);
+            db[p] = e == 0 ? mul2(dx[e], g) : fma2(dx[e], g, db[p]);
+            dc[p] = e == 0 ? mul2(dy[e], s[i][e][p]) : fma2(dy[e], s[i][e][p], dc[p]);
+            gb[e] = p == 0 ? mul2(g, Bv[p]) : fma2(g, Bv[p], gb[e]);
+            G[e][p] = mul2(ev[i][e][p], g);
+            const float2 u = mul2(G[e][p], i == 0 ? h0[e][p] : s[i - 1][e][p]);
+            ua[e] = p == 0 ? mul2(u, A2[e][p]) : fma2(u, A2[e][p], ua[e]);
+            dA[e][p] = fma2(u, dd[e], dA[e][p]);
           }
+        float st[4] = {gb[0].x + gb[0].y, gb[1].x + gb[1].y, ua[0].x + ua[0].y, ua[1].x + ua[1].y};
         scatter_sum<4, LPC, 1>(st, nl);
+        float* sum = sm + C::SUM + unit * kFloatUnit + cl % 8;
         if constexpr (LPC == 2) {  // lane 0: both channels' g B; lane 1: their u A
-          sm[C::SUM + (nl * kTile + t) * CT + cl] = st[0];
-          sm[C::SUM + (nl * kTile + t) * CT + cl + 1] = st[1];
+          sum[nl * UNITS * kFloatUnit] = st[0];
+          sum[nl * UNITS * kFloatUnit + 1] = st[1];
         } else if (nl % (LPC / 4) == 0) {
           const int v = nl / (LPC / 4);
-          sm[C::SUM + ((v >> 1) * kTile + t) * CT + cl + (v & 1)] = st[0];
+          sum[(v >> 1) * UNITS * kFloatUnit + (v & 1)] = st[0];
         }
+        float bc[8] = {db[0].x, db[0].y, db[1].x, db[1].y, dc[0].x, dc[0].y, dc[1].x, dc[1].y};
         scatter_sum<8, CL, LPC>(bc, cr);
         float* red = sm + C::RED + (warp * kTile + t) * 2 * NP + nl * 4;
         if constexpr (CL >= 8) {
@@ -187,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
     // the CTA's share of dB and dC
     for (int e = tid; e < kTile * 2 * NP; e += kThreads) {
       const int t = e / (2 * NP), r = e % (2 * NP);
-      if (t0 + t < a.T) {
+      if (t0 + t < last) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += sm[C::RED + (w * kTile + t) * 2 * NP + r];
@@ -196,64 +262,75 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
     }
 #pragma unroll
     for (int m = 0; m < C::ITEMS; ++m) {
-      const int item = tid + m * kThreads, t = item / VECS, cv = (item % VECS) * 8;
-      const int n = min(8, q.n - cv);
-      if (item < kTile * VECS && t0 + t < a.T && n > 0) {
-        float x[8], d[8], g[8], z[8], o[8];
-        load8<WIDE>(xp + (t0 + t) * a.x.st + cv, x, n);
-        load8<WIDE>(dp + (t0 + t) * a.dt.st + cv, d, n);
+      const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
+      if (item < UNITS && t < last && n > 0) {
+        float2 x[4], d[4], v[4], sgb[4], dy[4], o[4];
+        expand(*raw(stage, 0, item), x);
+        load_unit(sm + C::SUM + item * kFloatUnit, sgb);
+        load_unit(sm + C::DY + item * kFloatUnit, dy);
         if (GATE) {
-          load8<WIDE>(gp + (t0 + t) * a.y.st + cv, g, n);
-          load8<WIDE>(zp + (t0 + t) * a.z.st + cv, z, n);
-        }
+          float2 g[4], z[4], y[4];
+          expand(*raw(stage, 2, item), g);
+          expand(*raw(stage, 3, item), z);
+          load_unit(sm + C::SUM + (2 * UNITS + item) * kFloatUnit, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i < n) {
-            const int at = t * CT + cv + i, ch = q.c0 + cv + i;
-            const float sgb = sm[C::SUM + at], sua = sm[C::SUM + kTile * CT + at] * kLn2;
-            const float dy = sm[C::DY + at], delta = sm[C::DT + at];
-            const float skip = a.skip != nullptr ? a.skip[ch] : 0.f;
-            if (GATE) {
-              const float y = fmaf(skip, x[i], sm[C::SUM + 2 * kTile * CT + at]);
-              float val, slope;
-              act_slope<kActSilu>(z[i], &val, &slope);
-              z[i] = g[i] * y * slope;
-            }
-            float dd = fmaf(x[i], sgb, sua);
-            if (a.softplus) dd *= sigmoidf(d[i] + (a.dt_bias != nullptr ? a.dt_bias[ch] : 0.f));
-            sm[C::ACC + i * kThreads + tid] += dy * x[i];
-            sm[C::ACC + (8 + i) * kThreads + tid] += dd;
-            o[i] = fmaf(delta, sgb, skip * dy);
-            d[i] = dd;
+          for (int i = 0; i < 4; ++i) {
+            float2 val, slope;
+            act_slope<kActSilu>(z[i].x, &val.x, &slope.x);
+            act_slope<kActSilu>(z[i].y, &val.y, &slope.y);
+            o[i] = mul2(mul2(g[i], fma2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), x[i], y[i])),
+                        slope);
           }
+          store_pairs<WIDE, 8>((T*)a.dz.p + b * a.dz.sb + t * a.dz.st + q.c0 + cv, o, n);
         }
-        store8<WIDE>((T*)a.dx.p + b * a.dx.sb + (t0 + t) * a.dx.st + q.c0 + cv, o, n);
-        store8<WIDE>((T*)a.ddt.p + b * a.ddt.sb + (t0 + t) * a.ddt.st + q.c0 + cv, d, n);
-        if (GATE) store8<WIDE>((T*)a.dz.p + b * a.dz.sb + (t0 + t) * a.dz.st + q.c0 + cv, z, n);
+        expand(*raw(stage, 1, item), d);
+        load_unit(sm + C::SUM + (UNITS + item) * kFloatUnit, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 pair = reinterpret_cast<const float4*>(sm + C::DX + item * kPairUnit * 2)[i];
+          v[i] = fma2(v[i], make_float2(kLn2, kLn2), mul2(x[i], sgb[i]));
+          if (a.softplus) {
+            const float2 rw = add2(d[i], *reinterpret_cast<const float2*>(sm + C::BIAS + cv + 2 * i));
+            v[i] = mul2(v[i], make_float2(sigmoidf(rw.x), sigmoidf(rw.y)));
+          }
+          o[i] = fma2(make_float2(pair.x, pair.z), sgb[i],
+                      mul2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), dy[i]));
+          const float2 dk = mul2(dy[i], x[i]);
+          float* acc = sm + C::ACC + 2 * i * kThreads + tid;
+          acc[0] += dk.x;
+          acc[kThreads] += dk.y;
+          acc[8 * kThreads] += v[i].x;
+          acc[9 * kThreads] += v[i].y;
+        }
+        store_pairs<WIDE, 8>((T*)a.dx.p + b * a.dx.sb + t * a.dx.st + q.c0 + cv, o, n);
+        store_pairs<WIDE, 8>((T*)a.ddt.p + b * a.ddt.sb + t * a.ddt.st + q.c0 + cv, v, n);
       }
     }
     __syncthreads();
   }
+  const int row = seg * a.B + b;  // of the partial sums
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
+  for (int e = 0; e < 2; ++e) {
+    const float da[4] = {dA[e][0].x, dA[e][0].y, dA[e][1].x, dA[e][1].y};
+    const float gs[4] = {G[e][0].x, G[e][0].y, G[e][1].x, G[e][1].y};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int n = nl * 4 + k;
       if (cl + e < q.n && n < a.N) {
-        const long long at = ((long long)b * a.D + q.c0 + cl + e) * a.N + n;
-        a.part_a[at] = dA[e][k];
-        if (a.dstate_in != nullptr) a.dstate_in[at] = G[e][k];
+        const long long at = (long long)(q.c0 + cl + e) * a.N + n, all = (long long)a.D * a.N;
+        a.part_a[row * all + at] = da[k];
+        if (seg == 0 && a.dstate_in != nullptr) a.dstate_in[b * all + at] = gs[k];
       }
     }
+  }
   // threads with the same channels: tid % VECS (a thread keeps its vector through all items)
   static_assert(kThreads % VECS == 0, "a thread's channels are the same in every item");
-  __syncthreads();
   for (int e = tid; e < 2 * CT; e += kThreads) {
     const int which = e / CT, c = e % CT;
     if (c < q.n) {
       float v = 0.f;
       for (int w = c / 8; w < kThreads; w += VECS) v += sm[C::ACC + (which * 8 + c % 8) * kThreads + w];
-      a.part_d[((long long)b * 2 + which) * a.D + q.c0 + c] = v;
+      a.part_d[((long long)row * 2 + which) * a.D + q.c0 + c] = v;
     }
   }
 }
@@ -277,45 +354,46 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(ScanArgs a, int tiles, int
   ((T*)o.p)[b * o.sb + t * o.st + g * o.sh + n] = from_f32<T>(v);
 }
 
-// dA: the sum of the batches' shares.
+// dA: the sum of the batches' and segments' shares.
 __global__ void __launch_bounds__(256) scan_da_kernel(const float* __restrict__ part, float* __restrict__ dA,
-                                                      int B, long long count) {
+                                                      int rows, long long count) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= count) return;
   float v = 0.f;
 #pragma unroll 8
-  for (int b = 0; b < B; ++b) v += part[b * count + i];
+  for (int r = 0; r < rows; ++r) v += part[r * count + i];
   dA[i] = v;
 }
 
 template <typename T, int LPC, bool GATE, bool WIDE>
 cudaError_t bwd_kernel(const ScanArgs& a, int tiles, cudaStream_t s) {
-  constexpr int bytes = Cfg<LPC>::TOTAL * sizeof(float);
+  constexpr int bytes = Cfg<T, LPC>::TOTAL * sizeof(float);
   const cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<T, LPC, GATE, WIDE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   scan_bwd_kernel<T, LPC, GATE, WIDE>
-      <<<(unsigned)((long long)a.B * a.G * tiles), kThreads, bytes, s>>>(a, tiles);
+      <<<(unsigned)((long long)a.B * a.G * tiles * a.segs), kThreads, bytes, s>>>(a, tiles);
   return cudaGetLastError();
 }
 
 template <typename T, int LPC>
 cudaError_t bwd(const ScanArgs& a, cudaStream_t s) {
-  const int tiles = (a.D / a.G + Cfg<LPC>::CT - 1) / Cfg<LPC>::CT;
+  const int tiles = (a.D / a.G + Cfg<T, LPC>::CT - 1) / Cfg<T, LPC>::CT;
   cudaError_t e;
+  if (a.segs > 1 && (e = launch_scan_reverse_segments(a, s)) != cudaSuccess) return e;
   if (a.z.p != nullptr)
     e = a.wide ? bwd_kernel<T, LPC, true, true>(a, tiles, s) : bwd_kernel<T, LPC, true, false>(a, tiles, s);
   else
     e = a.wide ? bwd_kernel<T, LPC, false, true>(a, tiles, s) : bwd_kernel<T, LPC, false, false>(a, tiles, s);
   if (e != cudaSuccess) return e;
-  const long long total = (long long)a.B * a.T * a.G * 2 * Cfg<LPC>::NP;
-  scan_bc_kernel<T><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, tiles, Cfg<LPC>::NP);
+  const long long total = (long long)a.B * a.T * a.G * 2 * Cfg<T, LPC>::NP;
+  scan_bc_kernel<T><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, tiles, Cfg<T, LPC>::NP);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long count = (long long)a.D * a.N;
-  scan_da_kernel<<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a.part_a, a.dA, a.B, count);
+  scan_da_kernel<<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a.part_a, a.dA, a.B * a.segs, count);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.dskip == nullptr && a.ddt_bias == nullptr) return cudaSuccess;
-  return launch_param_sums(a.part_d, a.B, a.D, 1, a.dskip, a.ddt_bias, s);
+  return launch_param_sums(a.part_d, a.B * a.segs, a.D, 1, a.dskip, a.ddt_bias, s);
 }
 
 template <typename T>
@@ -335,8 +413,9 @@ ScanBwdSizes scan_bwd_sizes(int B, int T, int D, int G, int N) {
   ScanBwdSizes z;
   z.tiles = (D / G + CT - 1) / CT;
   z.part_bc = (size_t)z.tiles * B * T * G * 2 * NP;
-  z.part_a = (size_t)B * D * N;
-  z.part_d = (size_t)B * 2 * D;
+  const int segs = scan_segments(B, T, D, N).count;
+  z.part_a = (size_t)segs * B * D * N;
+  z.part_d = (size_t)segs * B * 2 * D;
   return z;
 }
 

@@ -20,8 +20,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// log(1 + exp(v)) without overflow.
-__device__ __forceinline__ float softplusf(float v) { return fmaxf(v, 0.f) + log1pf(__expf(-fabsf(v))); }
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|), with log(1 + e) = 2 artanh(s), s = e / (2 + e)
+// in [0, 1/3]: Gregory's series to s^13 leaves 2e-8 of the value, and small e keep their digits.
+// A quarter of log1pf's instructions, for every element of the sequence.
+__device__ __forceinline__ float softplusf(float v) {
+  const float e = exp2_fast(-fabsf(v) * kLog2e);
+  const float s = __fdividef(e, 2.f + e), z = s * s;
+  float p = fmaf(z, 1.f / 13.f, 1.f / 11.f);
+  p = fmaf(z, p, 1.f / 9.f);
+  p = fmaf(z, p, 1.f / 7.f);
+  p = fmaf(z, p, 1.f / 5.f);
+  p = fmaf(z, p, 1.f / 3.f);
+  p = fmaf(z, p, 1.f);
+  return fmaf(2.f * s, p, fmaxf(v, 0.f));
+}
+
+// A unit is eight channels of one token in shared memory, written by one thread with 16-byte
+// stores and read by a warp along the channels.  Padding a unit of pairs to 80 bytes and one of
+// floats to 48 spreads eight threads' 16-byte accesses over all 32 banks.
+constexpr int kPairUnit = 10;   // float2 of a unit of pairs
+constexpr int kFloatUnit = 12;  // floats of a unit of floats
 
 // Sums V values over L lanes that are STRIDE apart (rank: the lane's index among them) and
 // spreads the results: with V >= L lane r ends with the sums of values r V / L .. in v[0 ..];
@@ -45,10 +63,79 @@ __device__ __forceinline__ void scatter_sum(float (&v)[M], int rank) {
   }
 }
 
-// B and C of tokens t0 .. t0 + TT - 1 as fp32 rows [TT][2 NP]; zero past the end and in the padding.
+__device__ __forceinline__ float2 exp2_pair(float2 v) {
+  return make_float2(exp2_fast(v.x), exp2_fast(v.y));
+}
+
+__device__ __forceinline__ void load_unit(const float* u, float2* v) {
+  const float4 a = reinterpret_cast<const float4*>(u)[0], b = reinterpret_cast<const float4*>(u)[1];
+  v[0] = make_float2(a.x, a.y); v[1] = make_float2(a.z, a.w);
+  v[2] = make_float2(b.x, b.y); v[3] = make_float2(b.z, b.w);
+}
+__device__ __forceinline__ void store_unit(float* u, const float2* v) {
+  reinterpret_cast<float4*>(u)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  reinterpret_cast<float4*>(u)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+
+// delta of eight channels from dt as it lies in memory; zero where there is no token or channel,
+// so that such a token leaves every state as it is.
+template <typename T>
+__device__ __forceinline__ void delta_of(const ScanArgs& a, const Raw<T, 8>& dt, const float* bias, bool in,
+                                         int n, float2* delta) {
+  expand(dt, delta);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    delta[i] = add2(delta[i], *reinterpret_cast<const float2*>(bias + 2 * i));
+    if (a.softplus) delta[i] = make_float2(softplusf(delta[i].x), softplusf(delta[i].y));
+    if (!in || 2 * i >= n) delta[i].x = 0.f;
+    if (!in || 2 * i + 1 >= n) delta[i].y = 0.f;
+  }
+}
+// A unit of pairs (delta, w).
+template <typename T>
+__device__ __forceinline__ void stage_pair(const ScanArgs& a, const float2* w, const Raw<T, 8>& dt,
+                                           const float* bias, bool in, int n, float2* unit) {
+  float2 d[4];
+  delta_of<T>(a, dt, bias, in, n, d);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<float4*>(unit)[i] = make_float4(d[i].x, w[i].x, d[i].y, w[i].y);
+}
+// A unit of pairs (delta, delta x).  Absent elements of x were loaded as zero.
+template <typename T>
+__device__ __forceinline__ void stage_delta(const ScanArgs& a, const Raw<T, 8>& x, const Raw<T, 8>& dt,
+                                            const float* bias, bool in, int n, float2* unit) {
+  float2 d[4], v[4];
+  expand(x, v);
+  delta_of<T>(a, dt, bias, in, n, d);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<float4*>(unit)[i] = make_float4(d[i].x, d[i].x * v[i].x, d[i].y, d[i].y * v[i].y);
+}
+
+// The state (or, REVERSE, the state's gradient) that enters segment `seg`, from what enters the
+// first (last) one in h and the segments between.
+template <int NP, bool REVERSE>
+__device__ __forceinline__ void enter_segment(const ScanArgs& a, int b, int c, int nl, int seg,
+                                              const float2* A2, float2* h) {
+  for (int i = REVERSE ? a.segs - 1 : 0; REVERSE ? i > seg : i < seg; i += REVERSE ? -1 : 1) {
+    const long long row = ((long long)i * a.B + b) * a.D + c;
+    const float4 s = *reinterpret_cast<const float4*>(a.seg_state + row * NP + nl * 4);
+    const float2 sum = make_float2(a.seg_sum[row], a.seg_sum[row]);
+    const float2 e0 = exp2_pair(mul2(sum, A2[0])), e1 = exp2_pair(mul2(sum, A2[1]));
+    // a state of zero stays zero, however far a growing mode (A > 0) would have grown
+    h[0].x = (h[0].x == 0.f ? 0.f : e0.x * h[0].x) + s.x;
+    h[0].y = (h[0].y == 0.f ? 0.f : e0.y * h[0].y) + s.y;
+    h[1].x = (h[1].x == 0.f ? 0.f : e1.x * h[1].x) + s.z;
+    h[1].y = (h[1].y == 0.f ? 0.f : e1.y * h[1].y) + s.w;
+  }
+}
+
+// B and C of tokens t0 .. t0 + TT - 1 as fp32 rows [TT][2 NP]; zero from token `last` on and in the
+// padding.
 template <typename T, int NP, int TT>
-__device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0, float* out, int tid,
-                                         int threads) {
+__device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0, int last, float* out,
+                                         int tid, int threads) {
   const T* bp = (const T*)a.b.p + b * a.b.sb + g * a.b.sh;
   const T* cp = (const T*)a.c.p + b * a.c.sb + g * a.c.sh;
   if (a.wide_bc && a.N == NP) {  // whole vectors of eight
@@ -56,7 +143,7 @@ __device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0
       const int t = e / (NP / 4), r = e % (NP / 4), n = (r % (NP / 8)) * 8;
       const bool is_c = r >= NP / 8;
       float v[8];
-      if (t0 + t < a.T)
+      if (t0 + t < last)
         load8<true>(is_c ? cp + (t0 + t) * a.c.st + n : bp + (t0 + t) * a.b.st + n, v, 8);
       else
 #pragma unroll
@@ -67,11 +154,23 @@ __device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0
     for (int e = tid; e < TT * 2 * NP; e += threads) {
       const int t = e / (2 * NP), r = e % (2 * NP), n = r % NP;
       float v = 0.f;
-      if (t0 + t < a.T && n < a.N)
+      if (t0 + t < last && n < a.N)
         v = r >= NP ? to_f32(cp[(t0 + t) * a.c.st + n]) : to_f32(bp[(t0 + t) * a.b.st + n]);
       out[e] = v;
     }
   }
+}
+
+// A 16-byte copy into shared memory that completes in the background.
+__device__ __forceinline__ void copy16_async(void* smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)),
+               "l"(gmem)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {  // all but the newest LEFT groups are done
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
 // Channels of a CTA: tiles do not cross groups.

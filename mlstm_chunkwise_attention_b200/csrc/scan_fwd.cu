@@ -8,6 +8,10 @@
 // lane), then gated and stored with 16-byte stores.
 //
 // Bound by the exponentials: one ex2 per state, channel and token.
+//
+// With few rows the sequence is cut into segments that are scanned at once.  A first pass finds
+// each segment's state from zero and its sum of delta; segment j then starts from
+// sum_i exp(A sum of delta over i + 1 .. j - 1) state_i, which each CTA adds up for itself.
 #include "scan_common.cuh"
 
 namespace mlstm {
@@ -16,103 +20,247 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = 32;
 
+template <int LPC>
+struct Shape {
+  static constexpr int NP = 4 * LPC, CT = kWarps * 32 / LPC, VECS = CT / 8;
+  static constexpr int ITEMS = (kTile * VECS + kThreads - 1) / kThreads;  // units of a thread
+};
+
+// What a thread loads of one tile: its units of x and dt.
+template <typename T, int ITEMS>
+struct TileLoads {
+  Raw<T, 8> x[ITEMS], dt[ITEMS];
+};
+
 template <typename T, int LPC, bool GATE, bool WIDE>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanArgs a, int tiles) {
-  constexpr int NP = 4 * LPC, CT = kWarps * 32 / LPC, VECS = CT / 8;
-  constexpr int ITEMS = (kTile * VECS + kThreads - 1) / kThreads;
-  __shared__ __align__(16) float2 sd[kTile][CT];   // delta, delta x
-  __shared__ __align__(16) float sy[kTile][CT];
+__global__ void __launch_bounds__(kThreads, LPC == 4 ? 7 : 1) scan_fwd_kernel(ScanArgs a, int tiles) {
+  using S = Shape<LPC>;
+  constexpr int NP = S::NP, CT = S::CT, VECS = S::VECS, ITEMS = S::ITEMS;
+  __shared__ __align__(16) float2 sd[kTile * VECS * kPairUnit];  // delta, delta x
+  __shared__ __align__(16) float sy[kTile * VECS * kFloatUnit];
   __shared__ __align__(16) float sbc[kTile][2 * NP];
+  __shared__ __align__(16) float sbias[CT], sskip[CT];
   const int tid = threadIdx.x, lane = tid & 31, nl = lane % LPC;
   const int cl = (tid / 32) * (32 / LPC) + lane / LPC;  // channel within the tile
-  const int b = blockIdx.x / (tiles * a.G);
-  const ChannelTile q = channel_tile(a, blockIdx.x % (tiles * a.G), tiles, CT);
+  const int per_seg = a.B * a.G * tiles, seg = blockIdx.x / per_seg, bi = blockIdx.x % per_seg;
+  const int b = bi / (tiles * a.G);
+  const ChannelTile q = channel_tile(a, bi % (tiles * a.G), tiles, CT);
   const bool live = cl < q.n;
   const int c = q.c0 + cl, NC = (a.T + kScanEvery - 1) / kScanEvery;
-  float A2[4], h[4];
+  const int first = seg * a.seg_len, last = min(first + a.seg_len, a.T);
+  float2 A2[2], h[2];
+  {
+    float av[4], hv[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int n = nl * 4 + k;
-    const bool on = live && n < a.N;
-    A2[k] = on ? a.A[(long long)c * a.N + n] * kLog2e : 0.f;
-    h[k] = on && a.state_in != nullptr ? a.state_in[((long long)b * a.D + c) * a.N + n] : 0.f;
+    for (int k = 0; k < 4; ++k) {
+      const int n = nl * 4 + k;
+      const bool on = live && n < a.N;
+      av[k] = on ? a.A[(long long)c * a.N + n] * kLog2e : 0.f;
+      hv[k] = on && a.state_in != nullptr ? a.state_in[((long long)b * a.D + c) * a.N + n] : 0.f;
+    }
+    A2[0] = make_float2(av[0], av[1]); A2[1] = make_float2(av[2], av[3]);
+    h[0] = make_float2(hv[0], hv[1]); h[1] = make_float2(hv[2], hv[3]);
+  }
+  if (live) enter_segment<NP, false>(a, b, c, nl, seg, A2, h);
+  for (int i = tid; i < CT; i += kThreads) {
+    sbias[i] = a.dt_bias != nullptr && i < q.n ? a.dt_bias[q.c0 + i] : 0.f;
+    sskip[i] = a.skip != nullptr && i < q.n ? a.skip[q.c0 + i] : 0.f;
   }
   const T* xp = (const T*)a.x.p + b * a.x.sb + q.c0;
   const T* dp = (const T*)a.dt.p + b * a.dt.sb + q.c0;
   const T* zp = GATE ? (const T*)a.z.p + b * a.z.sb + q.c0 : nullptr;
   T* yp = (T*)a.y.p + b * a.y.sb + q.c0;
-
-  for (int t0 = 0; t0 < a.T; t0 += kTile) {
-    float xv[ITEMS][8];
+  TileLoads<T, ITEMS> next;
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int m = 0; m < ITEMS; ++m) {
+      const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
+      zero_raw(next.x[m]);
+      zero_raw(next.dt[m]);
+      if (item < kTile * VECS && t < last && n > 0) {
+        load_raw<WIDE>(xp + t * a.x.st + cv, next.x[m], n);
+        load_raw<WIDE>(dp + t * a.dt.st + cv, next.dt[m], n);
+      }
+    }
+  };
+  fetch(first);
+  __syncthreads();
+  for (int t0 = first; t0 < last; t0 += kTile) {
+    const TileLoads<T, ITEMS> now = next;
+    Raw<T, 8> zr[ITEMS];
 #pragma unroll
     for (int m = 0; m < ITEMS; ++m) {
       const int item = tid + m * kThreads, t = item / VECS, cv = (item % VECS) * 8;
-      if (item < kTile * VECS) {
-        const int n = min(8, q.n - cv);
-        float dv[8];
-        const bool in = t0 + t < a.T && n > 0;
-        if (in) {
-          load8<WIDE>(xp + (t0 + t) * a.x.st + cv, xv[m], n);
-          load8<WIDE>(dp + (t0 + t) * a.dt.st + cv, dv, n);
-        }
+      if (item < kTile * VECS)
+        stage_delta<T>(a, now.x[m], now.dt[m], sbias + cv, t0 + t < last, q.n - cv, sd + item * kPairUnit);
+    }
+    stage_bc<T, NP, kTile>(a, b, q.g, t0, last, &sbc[0][0], tid, kThreads);
+    if (t0 + kTile < last) fetch(t0 + kTile);
+    if (GATE) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float delta = 0.f, dx = 0.f;
-          if (in && i < n) {
-            delta = dv[i] + (a.dt_bias != nullptr ? a.dt_bias[q.c0 + cv + i] : 0.f);
-            if (a.softplus) delta = softplusf(delta);
-            dx = delta * xv[m][i];
-          }
-          sd[t][cv + i] = make_float2(delta, dx);
-        }
+      for (int m = 0; m < ITEMS; ++m) {
+        const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
+        zero_raw(zr[m]);
+        if (item < kTile * VECS && t < last && n > 0) load_raw<WIDE>(zp + t * a.z.st + cv, zr[m], n);
       }
     }
-    stage_bc<T, NP, kTile>(a, b, q.g, t0, &sbc[0][0], tid, kThreads);
     __syncthreads();
     for (int t = 0; t < kTile; t += LPC) {
       float acc[LPC];
 #pragma unroll
       for (int u = 0; u < LPC; ++u) {
-        if (a.saved != nullptr && ((t + u) % kScanEvery) == 0 && t0 + t + u < a.T && live)
+        if (a.saved != nullptr && ((t + u) % kScanEvery) == 0 && t0 + t + u < last && live)
           *reinterpret_cast<float4*>(a.saved +
                                      (((long long)b * NC + (t0 + t + u) / kScanEvery) * a.D + c) * NP +
-                                     nl * 4) = make_float4(h[0], h[1], h[2], h[3]);
-        const float2 d = sd[t + u][cl];
+                                     nl * 4) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+        const float2 d = sd[((t + u) * VECS + cl / 8) * kPairUnit + cl % 8];
         const float4 Bv = *reinterpret_cast<const float4*>(&sbc[t + u][nl * 4]);
         const float4 Cv = *reinterpret_cast<const float4*>(&sbc[t + u][NP + nl * 4]);
-        h[0] = fmaf(exp2_fast(d.x * A2[0]), h[0], d.y * Bv.x);
-        h[1] = fmaf(exp2_fast(d.x * A2[1]), h[1], d.y * Bv.y);
-        h[2] = fmaf(exp2_fast(d.x * A2[2]), h[2], d.y * Bv.z);
-        h[3] = fmaf(exp2_fast(d.x * A2[3]), h[3], d.y * Bv.w);
-        acc[u] = fmaf(h[0], Cv.x, fmaf(h[1], Cv.y, fmaf(h[2], Cv.z, h[3] * Cv.w)));
+        const float2 dd = make_float2(d.x, d.x), ww = make_float2(d.y, d.y);
+        h[0] = fma2(exp2_pair(mul2(dd, A2[0])), h[0], mul2(ww, make_float2(Bv.x, Bv.y)));
+        h[1] = fma2(exp2_pair(mul2(dd, A2[1])), h[1], mul2(ww, make_float2(Bv.z, Bv.w)));
+        const float2 y = fma2(h[1], make_float2(Cv.z, Cv.w), mul2(h[0], make_float2(Cv.x, Cv.y)));
+        acc[u] = y.x + y.y;
       }
       scatter_sum<LPC, LPC, 1>(acc, nl);
-      sy[t + nl][cl] = acc[0];
+      sy[((t + nl) * VECS + cl / 8) * kFloatUnit + cl % 8] = acc[0];
     }
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < ITEMS; ++m) {
-      const int item = tid + m * kThreads, t = item / VECS, cv = (item % VECS) * 8;
-      const int n = min(8, q.n - cv);
-      if (item < kTile * VECS && t0 + t < a.T && n > 0) {
-        float z[8], o[8];
-        if (GATE) load8<WIDE>(zp + (t0 + t) * a.z.st + cv, z, n);
+      const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
+      if (item < kTile * VECS && t < last && n > 0) {
+        float2 x[4], o[4], z[4];
+        expand(now.x[m], x);
+        load_unit(sy + item * kFloatUnit, o);
+        if (GATE) expand(zr[m], z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = sy[t][cv + i];
-          if (a.skip != nullptr && i < n) o[i] = fmaf(a.skip[q.c0 + cv + i], xv[m][i], o[i]);
-          if (GATE) o[i] *= act_value<kActSilu>(z[i]);
+        for (int i = 0; i < 4; ++i) {
+          o[i] = fma2(*reinterpret_cast<const float2*>(sskip + cv + 2 * i), x[i], o[i]);
+          if (GATE)
+            o[i] = mul2(o[i], make_float2(act_value<kActSilu>(z[i].x), act_value<kActSilu>(z[i].y)));
         }
-        store8<WIDE>(yp + (t0 + t) * a.y.st + cv, o, n);
+        store_pairs<WIDE, 8>(yp + t * a.y.st + cv, o, n);
       }
     }
     // the next tile's sd and sbc were last read before the barrier above; its sy is written
     // after the next one
   }
-  if (a.state_out != nullptr && live)
+  if (a.state_out != nullptr && live && last == a.T) {
+    const float hv[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (nl * 4 + k < a.N) a.state_out[((long long)b * a.D + c) * a.N + nl * 4 + k] = h[k];
+      if (nl * 4 + k < a.N) a.state_out[((long long)b * a.D + c) * a.N + nl * 4 + k] = hv[k];
+  }
+}
+
+// A segment's own state: REVERSE false, the forward state from zero over all segments but the
+// last; true, the gradient that all segments but the first hand back, from zero and dy alone.  With
+// them the segment's sum of delta, whose exponential carries a state across it.
+template <typename T, int LPC, bool REVERSE, bool GATE, bool WIDE>
+__global__ void __launch_bounds__(kThreads, LPC == 4 ? 7 : 1) scan_segment_kernel(ScanArgs a, int tiles) {
+  using S = Shape<LPC>;
+  constexpr int NP = S::NP, CT = S::CT, VECS = S::VECS, ITEMS = S::ITEMS;
+  __shared__ __align__(16) float2 sd[kTile * VECS * kPairUnit];  // delta and delta x, or delta and dy
+  __shared__ __align__(16) float sv[kTile][NP];                  // B, or C
+  __shared__ __align__(16) float sbias[CT];
+  const int tid = threadIdx.x, lane = tid & 31, nl = lane % LPC;
+  const int cl = (tid / 32) * (32 / LPC) + lane / LPC;
+  const int per_seg = a.B * a.G * tiles, bi = blockIdx.x % per_seg;
+  const int seg = blockIdx.x / per_seg + (REVERSE ? 1 : 0);
+  const int b = bi / (tiles * a.G);
+  const ChannelTile q = channel_tile(a, bi % (tiles * a.G), tiles, CT);
+  const bool live = cl < q.n;
+  const int c = q.c0 + cl;
+  const int first = seg * a.seg_len, last = min(first + a.seg_len, a.T);
+  float av[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    av[k] = live && nl * 4 + k < a.N ? a.A[(long long)c * a.N + nl * 4 + k] * kLog2e : 0.f;
+  const float2 A2[2] = {make_float2(av[0], av[1]), make_float2(av[2], av[3])};
+  float2 h[2] = {};
+  float sum = 0.f;
+  for (int i = tid; i < CT; i += kThreads)
+    sbias[i] = a.dt_bias != nullptr && i < q.n ? a.dt_bias[q.c0 + i] : 0.f;
+  // the second factor: x, or dy (with its gate)
+  const Rows& wr = REVERSE ? a.y : a.x;
+  const T* xp = (const T*)wr.p + b * wr.sb + q.c0;
+  const T* dp = (const T*)a.dt.p + b * a.dt.sb + q.c0;
+  const T* zp = GATE ? (const T*)a.z.p + b * a.z.sb + q.c0 : nullptr;
+  const Rows& vr = REVERSE ? a.c : a.b;
+  const T* vp = (const T*)vr.p + b * vr.sb + q.g * vr.sh;
+  const int count = (last - first + kTile - 1) / kTile;
+  TileLoads<T, ITEMS> next;
+  auto fetch = [&](int t0) {
+#pragma unroll
+    for (int m = 0; m < ITEMS; ++m) {
+      const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
+      zero_raw(next.x[m]);
+      zero_raw(next.dt[m]);
+      if (item < kTile * VECS && t < last && n > 0) {
+        load_raw<WIDE>(xp + t * wr.st + cv, next.x[m], n);
+        load_raw<WIDE>(dp + t * a.dt.st + cv, next.dt[m], n);
+      }
+    }
+  };
+  auto origin = [&](int i) { return first + (REVERSE ? count - 1 - i : i) * kTile; };
+  fetch(origin(0));
+  __syncthreads();
+  for (int i = 0; i < count; ++i) {
+    const int t0 = origin(i);
+    const TileLoads<T, ITEMS> now = next;
+#pragma unroll
+    for (int m = 0; m < ITEMS; ++m) {
+      const int item = tid + m * kThreads, t = item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
+      if (item < kTile * VECS) {
+        if (!REVERSE) {
+          stage_delta<T>(a, now.x[m], now.dt[m], sbias + cv, t0 + t < last, n, sd + item * kPairUnit);
+        } else {
+          float2 g[4], z[4];
+          expand(now.x[m], g);
+          if (GATE) {
+            Raw<T, 8> zr;
+            zero_raw(zr);
+            if (t0 + t < last && n > 0) load_raw<WIDE>(zp + (t0 + t) * a.z.st + cv, zr, n);
+            expand(zr, z);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              g[k] = mul2(g[k], make_float2(act_value<kActSilu>(z[k].x), act_value<kActSilu>(z[k].y)));
+          }
+          stage_pair<T>(a, g, now.dt[m], sbias + cv, t0 + t < last, n, sd + item * kPairUnit);
+        }
+      }
+    }
+    for (int e = tid; e < kTile * NP; e += kThreads) {
+      const int t = t0 + e / NP, n = e % NP;
+      sv[e / NP][n] = t < last && n < a.N ? to_f32(vp[t * vr.st + n]) : 0.f;
+    }
+    if (i + 1 < count) fetch(origin(i + 1));
+    __syncthreads();
+#pragma unroll 4
+    for (int u = 0; u < kTile; ++u) {
+      const int t = REVERSE ? kTile - 1 - u : u;
+      const float2 d = sd[(t * VECS + cl / 8) * kPairUnit + cl % 8];
+      const float4 V = *reinterpret_cast<const float4*>(&sv[t][nl * 4]);
+      const float2 dd = make_float2(d.x, d.x), ww = make_float2(d.y, d.y);
+      const float2 e0 = exp2_pair(mul2(dd, A2[0])), e1 = exp2_pair(mul2(dd, A2[1]));
+      const float2 v0 = make_float2(V.x, V.y), v1 = make_float2(V.z, V.w);
+      if (REVERSE) {
+        h[0] = mul2(e0, fma2(ww, v0, h[0]));
+        h[1] = mul2(e1, fma2(ww, v1, h[1]));
+      } else {
+        h[0] = fma2(e0, h[0], mul2(ww, v0));
+        h[1] = fma2(e1, h[1], mul2(ww, v1));
+      }
+      sum += d.x;
+    }
+    __syncthreads();
+  }
+  if (live) {
+    const long long row = ((long long)seg * a.B + b) * a.D + c;
+    *reinterpret_cast<float4*>(a.seg_state + row * NP + nl * 4) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    if (nl == 0) a.seg_sum[row] = sum;
+  }
 }
 
 // One token: four states of one channel to a lane.  Bound by the states, read and written once.
@@ -165,11 +313,28 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
   }
 }
 
+template <typename T, int LPC, bool REVERSE>
+cudaError_t segments(const ScanArgs& a, cudaStream_t s) {
+  const int tiles = (a.D / a.G + Shape<LPC>::CT - 1) / Shape<LPC>::CT;
+  const unsigned grid = (unsigned)((long long)a.B * a.G * tiles * (a.segs - 1));
+  if (REVERSE && a.z.p != nullptr) {
+    if (a.wide) scan_segment_kernel<T, LPC, REVERSE, REVERSE, true><<<grid, kThreads, 0, s>>>(a, tiles);
+    else scan_segment_kernel<T, LPC, REVERSE, REVERSE, false><<<grid, kThreads, 0, s>>>(a, tiles);
+  } else {
+    if (a.wide) scan_segment_kernel<T, LPC, REVERSE, false, true><<<grid, kThreads, 0, s>>>(a, tiles);
+    else scan_segment_kernel<T, LPC, REVERSE, false, false><<<grid, kThreads, 0, s>>>(a, tiles);
+  }
+  return cudaGetLastError();
+}
+
 template <typename T, int LPC>
 cudaError_t fwd(const ScanArgs& a, cudaStream_t s) {
-  constexpr int CT = kWarps * 32 / LPC;
-  const int tiles = (a.D / a.G + CT - 1) / CT;
-  const unsigned grid = (unsigned)((long long)a.B * a.G * tiles);
+  if (a.segs > 1) {
+    const cudaError_t e = segments<T, LPC, false>(a, s);
+    if (e != cudaSuccess) return e;
+  }
+  const int tiles = (a.D / a.G + Shape<LPC>::CT - 1) / Shape<LPC>::CT;
+  const unsigned grid = (unsigned)((long long)a.B * a.G * tiles * a.segs);
   if (a.z.p != nullptr) {
     if (a.wide) scan_fwd_kernel<T, LPC, true, true><<<grid, kThreads, 0, s>>>(a, tiles);
     else scan_fwd_kernel<T, LPC, true, false><<<grid, kThreads, 0, s>>>(a, tiles);
@@ -187,23 +352,52 @@ cudaError_t step(const ScanArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T, bool STEP>
+enum Pass { kFwd, kStep, kReverseSegments };
+
+template <Pass P, typename T, int LPC>
+cudaError_t run_pass(const ScanArgs& a, cudaStream_t s) {
+  if constexpr (P == kFwd) return fwd<T, LPC>(a, s);
+  if constexpr (P == kStep) return step<T, LPC>(a, s);
+  return segments<T, LPC, true>(a, s);
+}
+template <Pass P, typename T>
 cudaError_t by_states(const ScanArgs& a, cudaStream_t s) {
   switch (scan_pad(a.N)) {
-    case 8: return STEP ? step<T, 2>(a, s) : fwd<T, 2>(a, s);
-    case 16: return STEP ? step<T, 4>(a, s) : fwd<T, 4>(a, s);
-    case 32: return STEP ? step<T, 8>(a, s) : fwd<T, 8>(a, s);
-    default: return STEP ? step<T, 16>(a, s) : fwd<T, 16>(a, s);
+    case 8: return run_pass<P, T, 2>(a, s);
+    case 16: return run_pass<P, T, 4>(a, s);
+    case 32: return run_pass<P, T, 8>(a, s);
+    default: return run_pass<P, T, 16>(a, s);
   }
+}
+template <Pass P>
+cudaError_t by_type(const ScanArgs& a, cudaStream_t s) {
+  return a.dtype == 0 ? by_states<P, bf16>(a, s) : by_states<P, float>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s) {
-  return a.dtype == 0 ? by_states<bf16, false>(a, s) : by_states<float, false>(a, s);
+ScanSegments scan_segments(int B, int T, int D, int N) {
+  // Warps of an undivided scan, and how many tokens a segment keeps at least.
+  const long long warps = ((long long)B * D * scan_pad(N) + 127) / 128;
+  constexpr int want = 148 * 20, least = 4 * kTile;
+  long long segs = warps > 0 ? (want + warps - 1) / warps : 1;
+  if (segs > T / least) segs = T / least;
+  ScanSegments z;
+  if (segs <= 1) {
+    z.len = T;
+    z.count = 1;
+    return z;
+  }
+  const long long tiles = (T + kTile - 1) / kTile;
+  z.len = (int)((tiles + segs - 1) / segs) * kTile;
+  z.count = (T + z.len - 1) / z.len;
+  return z;
 }
-cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s) {
-  return a.dtype == 0 ? by_states<bf16, true>(a, s) : by_states<float, true>(a, s);
+
+cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s) { return by_type<kFwd>(a, s); }
+cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s) { return by_type<kStep>(a, s); }
+cudaError_t launch_scan_reverse_segments(const ScanArgs& a, cudaStream_t s) {
+  return by_type<kReverseSegments>(a, s);
 }
 
 }  // namespace mlstm

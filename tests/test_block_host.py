@@ -160,7 +160,7 @@ def scan_problem(**kw):
 ])
 def test_scan_argument_errors(lib, kw, status):
     p = scan_problem(**kw)
-    assert lib.mlstm_scan_fwd(p, rows(), None, None, None) == status
+    assert lib.mlstm_scan_fwd(p, rows(), None, None, None, 0, None) == status
     grads = B.ScanGrads()
     grads.dx = grads.ddt = grads.dz = grads.db = grads.dc = rows()
     grads.da = FAKE
@@ -169,10 +169,10 @@ def test_scan_argument_errors(lib, kw, status):
 
 def test_scan_states_workspaces_and_step_errors(lib):
     p = scan_problem(state_in=FAKE)
-    assert lib.mlstm_scan_fwd(None, rows(), None, None, None) == 1
-    assert lib.mlstm_scan_fwd(p, rows(), None, FAKE + 1024, None) == 1     # overlapping states
-    assert lib.mlstm_scan_fwd(p, rows(), FAKE + 8, None, None) == 1        # misaligned saved
-    assert lib.mlstm_scan_fwd(p, rows(None), None, None, None) == 1
+    assert lib.mlstm_scan_fwd(None, rows(), None, None, None, 0, None) == 1
+    assert lib.mlstm_scan_fwd(p, rows(), None, FAKE + 1024, None, 0, None) == 1  # overlapping states
+    assert lib.mlstm_scan_fwd(p, rows(), FAKE + 8, None, None, 0, None) == 1  # misaligned saved
+    assert lib.mlstm_scan_fwd(p, rows(None), None, None, None, 0, None) == 1
     assert lib.mlstm_scan_step(p, rows(), None, None) == 1
     assert lib.mlstm_scan_step(p, rows(), FAKE + 512, None) == 1
     assert lib.mlstm_scan_step(scan_problem(), rows(), FAKE, None) == 1    # no state
@@ -186,6 +186,13 @@ def test_scan_states_workspaces_and_step_errors(lib):
     assert lib.mlstm_scan_bwd(scan_problem(z=rows()), *args[1:], need, None) == 1  # no dz
     grads.da = None
     assert lib.mlstm_scan_bwd(*args, need, None) == 1
+    # a long sequence of few channels is cut into segments, and needs room for their states
+    few = scan_problem(B=1, T=4096)
+    need = lib.mlstm_scan_fwd_workspace_size(1, 4096, 64, 1, 16, B.BF16)
+    assert need > 0 and lib.mlstm_scan_fwd(few, rows(), None, None, None, need, None) == 3
+    assert lib.mlstm_scan_fwd(few, rows(), None, None, FAKE, need - 1, None) == 3
+    assert lib.mlstm_scan_fwd(few, rows(), None, None, FAKE + 8, need, None) == 1
+    assert lib.mlstm_scan_fwd_workspace_size(2, 5, 64, 1, 16, B.BF16) == 0
     # two saved states of 64 channels, 16 states each, for 5 (one group of eight) and 9 tokens
     assert lib.mlstm_scan_saved_size(2, 5, 64, 1, 16, B.BF16) == 2 * 1 * 64 * 16 * 4
     assert lib.mlstm_scan_saved_size(2, 9, 64, 1, 12, B.BF16) == 2 * 2 * 64 * 16 * 4
@@ -227,7 +234,7 @@ def test_empty_problems_need_no_tensors(lib):
     assert conv_fwd(lib, x=none, y=none, w=None, Bn=0) == 0
     assert conv_fwd(lib, x=none, y=none, w=None, T=0) == 0
     p = scan_problem(B=0, x=none, dt=none, b=none, c=none, a=None)
-    assert lib.mlstm_scan_fwd(p, none, None, None, None) == 0
+    assert lib.mlstm_scan_fwd(p, none, None, None, None, 0, None) == 0
     assert lib.mlstm_scan_step(p, none, None, None) == 0
 
 

@@ -139,6 +139,8 @@ SCAN = [
     (2, 130, 136, 16, 1, True, True, True, True, False, BF, False),  # ragged channel tiles
     (1, 65, 48, 32, 2, True, True, False, True, True, F32, False),
     (1, 70, 20, 64, 1, False, True, True, False, True, F32, False),
+    (1, 1111, 24, 16, 1, True, True, True, True, True, F32, False),  # eight segments, the last ragged
+    (2, 530, 40, 6, 2, True, True, True, True, True, BF, False),     # four segments
     (2, 64, 64, 20, 64, True, True, True, True, True, F32, False),   # a group per channel
 ]
 
@@ -445,7 +447,7 @@ def test_outputs_stay_inside_their_rows():
     assert untouched(o) and torch.equal(o[:, :T, :D], want)
     o = room()
     p = block._scan_problem(x, x, A, Bm, Bm, None, None, None, True, None)
-    assert lib.mlstm_scan_fwd(p, rows(o), None, None, s) == 0
+    assert lib.mlstm_scan_fwd(p, rows(o), None, None, None, 0, s) == 0
     want, _, _ = block.selective_scan_forward(x, x, A, Bm, Bm)
     assert untouched(o) and torch.equal(o[:, :T, :D], want)
     o = room()
