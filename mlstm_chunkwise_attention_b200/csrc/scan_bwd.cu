@@ -19,6 +19,13 @@ namespace mlstm {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = 16;
+#ifndef KEEP
+#define KEEP 1
+#endif
+#ifndef CTAS
+#define CTAS 2
+#endif
+constexpr bool kKeepDecay = KEEP;
 static_assert(kTile == 2 * kScanEvery, "two saved states to a tile");
 
 template <typename T, int LPC>
@@ -28,24 +35,31 @@ struct Cfg {
   static constexpr int CT = kWarps * CL * 2;  // channels of a CTA
   static constexpr int VECS = CT / 8, UNITS = kTile * VECS;
   static constexpr int ITEMS = (UNITS + kThreads - 1) / kThreads;  // units of a thread
-  // shared memory, in floats: (delta, delta x) and dy of the tile; sums over states of g B, u A and
-  // C s; B and C [tile][2 NP]; dB and dC of each warp [warps][tile][2 NP]; dskip and ddt_bias
-  // shares of each thread's channels [16][threads]; dt_bias and skip; two saved states ahead
+  // A lane keeps its states in the order k ^ perm, perm from its channel rank, so that each step
+  // of the sum over channels sends one half of what it holds and keeps the other without choosing;
+  // B and C lie in one copy for each order.
+  static constexpr int ORDER = kTile * 2 * NP + 8;  // floats of a copy, with 8 to spread the banks
+  // shared memory, in floats: delta and delta x of the tile, dy of the tile; sums over states of g B,
+  // u A and C s; B and C; dB and dC of each warp [warps][tile][2 NP]; dskip and ddt_bias shares of
+  // each thread's channels [4][threads] of four; dt_bias and skip; two saved states ahead
   // [2][2][threads] of four floats; and two tiles of x, dt, dy, z as they lie in memory
-  static constexpr int DX = 0, DY = DX + UNITS * kPairUnit * 2, SUM = DY + UNITS * kFloatUnit,
-                       BC = SUM + 3 * UNITS * kFloatUnit, RED = BC + kTile * 2 * NP,
+  static constexpr int DX = 0, DY = DX + UNITS * kPairUnit, SUM = DY + UNITS * kFloatUnit,
+                       BC = SUM + 3 * UNITS * kFloatUnit, RED = BC + 4 * ORDER,
                        ACC = RED + kWarps * kTile * 2 * NP, BIAS = ACC + 16 * kThreads, SKIP = BIAS + CT,
                        SAVED = SKIP + CT, RAW = SAVED + 16 * kThreads,
                        TOTAL = RAW + 2 * 4 * UNITS * 8 * (int)sizeof(T) / 4;
 };
 
 template <typename T, int LPC, bool GATE, bool WIDE>
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, int tiles) {
   using C = Cfg<T, LPC>;
   constexpr int NP = C::NP, CL = C::CL, CT = C::CT, VECS = C::VECS, UNITS = C::UNITS;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, nl = lane % LPC, cr = lane / LPC;
   const int cl = (warp * CL + cr) * 2;  // the lane's two channels within the tile
+  const int swap = nl & 1;              // it takes them in this order: cl + swap, then the other
+  const int perm = (cr & 1) * 2 + (CL >= 4 ? (cr >> 1) & 1 : 0);  // and state k ^ perm as its k-th
+  const int ch[2] = {cl + swap, cl + 1 - swap};
   const int per_seg = a.B * a.G * tiles, seg = blockIdx.x / per_seg, bi = blockIdx.x % per_seg;
   const int b = bi / (tiles * a.G), ti = bi % (tiles * a.G);
   const ChannelTile q = channel_tile(a, ti, tiles, CT);
@@ -57,11 +71,11 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
     float av[4], gv[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int n = nl * 4 + k;
-      const bool on = cl + e < q.n && n < a.N;
-      av[k] = on ? a.A[(long long)(q.c0 + cl + e) * a.N + n] * kLog2e : 0.f;
+      const int n = nl * 4 + (k ^ perm);
+      const bool on = ch[e] < q.n && n < a.N;
+      av[k] = on ? a.A[(long long)(q.c0 + ch[e]) * a.N + n] * kLog2e : 0.f;
       gv[k] = on && a.dstate_out != nullptr
-                  ? a.dstate_out[((long long)b * a.D + q.c0 + cl + e) * a.N + n]
+                  ? a.dstate_out[((long long)b * a.D + q.c0 + ch[e]) * a.N + n]
                   : 0.f;
     }
 #pragma unroll
@@ -70,10 +84,11 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
       G[e][p] = make_float2(gv[2 * p], gv[2 * p + 1]);
       dA[e][p] = make_float2(0.f, 0.f);
     }
-    if (cl + e < q.n) enter_segment<NP, true>(a, b, q.c0 + cl + e, nl, seg, A2[e], G[e]);
+    if (ch[e] < q.n) enter_segment<NP, true>(a, b, q.c0 + ch[e], nl, seg, A2[e], G[e], perm);
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sm[C::ACC + i * kThreads + tid] = 0.f;
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<float4*>(sm + C::ACC)[i * kThreads + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = tid; i < CT; i += kThreads) {
     sm[C::BIAS + i] = a.dt_bias != nullptr && i < q.n ? a.dt_bias[q.c0 + i] : 0.f;
     sm[C::SKIP + i] = a.skip != nullptr && i < q.n ? a.skip[q.c0 + i] : 0.f;
@@ -117,9 +132,9 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
     if (t < first) return;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      if (cl + e < q.n && t < last)
+      if (ch[e] < q.n && t < last)
         copy16_async(sm + C::SAVED + ((stage * 2 + e) * kThreads + tid) * 4,
-                     a.saved + (((long long)b * NC + t / kScanEvery) * a.D + q.c0 + cl + e) * NP + nl * 4);
+                     a.saved + (((long long)b * NC + t / kScanEvery) * a.D + q.c0 + ch[e]) * NP + nl * 4);
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i)  // channels that do not exist keep a state of zero
@@ -131,14 +146,14 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
   int stage = 0;
   __syncthreads();
   for (int t0 = top; t0 >= first; t0 -= kTile, stage ^= 1) {
-    stage_bc<T, NP, kTile>(a, b, q.g, t0, last, sm + C::BC, tid, kThreads);
+    stage_bc<T, NP, kTile, 4, C::ORDER>(a, b, q.g, t0, last, sm + C::BC, tid, kThreads);
     copies_wait<0>();
 #pragma unroll
     for (int m = 0; m < C::ITEMS; ++m) {
       const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
       if (item < UNITS) {
         stage_delta<T>(a, *raw(stage, 0, item), *raw(stage, 1, item), sm + C::BIAS + cv, t < last, n,
-                       reinterpret_cast<float2*>(sm + C::DX) + item * kPairUnit);
+                       sm + C::DX + item * kPairUnit);
         float2 g[4], z[4];
         expand(*raw(stage, 2, item), g);
         if (GATE) {
@@ -160,91 +175,113 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
       copies_commit();
       if (half == 0) copies_wait<1>();  // the upper's were waited for with the tile
       if (t0 + sub >= last) continue;
-      float2 h0[2][2], s[kScanEvery][2][2], ev[kScanEvery][2][2];
+      float2 h0[2][2], s[kScanEvery][2][2], ev[kKeepDecay ? kScanEvery : 1][2][2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float4 v =
-            *reinterpret_cast<const float4*>(sm + C::SAVED + (((half ^ 1) * 2 + e) * kThreads + tid) * 4);
+        const float4 v = permuted(
+            *reinterpret_cast<const float4*>(sm + C::SAVED + (((half ^ 1) * 2 + e) * kThreads + tid) * 4), perm);
         h0[e][0] = make_float2(v.x, v.y);
         h0[e][1] = make_float2(v.z, v.w);
       }
+      const float* bcs = sm + C::BC + perm * C::ORDER + sub * 2 * NP + nl * 4;
+      const float* dxs[2] = {sm + C::DX + (sub * VECS + cl / 8) * kPairUnit + (ch[0] % 8) * 2,
+                             sm + C::DX + (sub * VECS + cl / 8) * kPairUnit + (ch[1] % 8) * 2};
+      const float* dys[2] = {sm + C::DY + (sub * VECS + cl / 8) * kFloatUnit + ch[0] % 8,
+                             sm + C::DY + (sub * VECS + cl / 8) * kFloatUnit + ch[1] % 8};
+      float* sums = sm + C::SUM + (sub * VECS + cl / 8) * kFloatUnit + ch[0] % 8;
 #pragma unroll
       for (int i = 0; i < kScanEvery; ++i) {
-        const int t = sub + i, unit = t * VECS + cl / 8;
-        const float4 d = *reinterpret_cast<const float4*>(sm + C::DX + unit * kPairUnit * 2 + (cl % 8) * 2);
-        const float4 Bq = *reinterpret_cast<const float4*>(sm + C::BC + t * 2 * NP + nl * 4);
+        const float4 Bq = *reinterpret_cast<const float4*>(bcs + i * 2 * NP);
         const float2 Bv[2] = {make_float2(Bq.x, Bq.y), make_float2(Bq.z, Bq.w)};
-        const float2 dd[2] = {make_float2(d.x, d.x), make_float2(d.z, d.z)};
-        const float2 dx[2] = {make_float2(d.y, d.y), make_float2(d.w, d.w)};
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e) {
+          const float2 d = *reinterpret_cast<const float2*>(dxs[e] + i * VECS * kPairUnit);
+          const float2 dd = make_float2(d.x, d.x), dx = make_float2(d.y, d.y);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            ev[i][e][p] = exp2_pair(mul2(dd[e], A2[e][p]));
-            s[i][e][p] = fma2(ev[i][e][p], i == 0 ? h0[e][p] : s[i - 1][e][p], mul2(dx[e], Bv[p]));
+            const float2 w = exp2_pair(mul2(dd, A2[e][p]));
+            if (kKeepDecay) ev[i][e][p] = w;
+            s[i][e][p] = fma2(w, i == 0 ? h0[e][p] : s[i - 1][e][p], mul2(dx, Bv[p]));
           }
+        }
         if (GATE) {  // the ungated output, for dz
-          const float4 Cq = *reinterpret_cast<const float4*>(sm + C::BC + t * 2 * NP + NP + nl * 4);
+          const float4 Cq = *reinterpret_cast<const float4*>(bcs + i * 2 * NP + NP);
           float y[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float2 v = fma2(s[i][e][1], make_float2(Cq.z, Cq.w), mul2(s[i][e][0], make_float2(Cq.x, Cq.y)));
             y[e] = v.x + v.y;
           }
-          scatter_sum<2, LPC, 1>(y, nl);
-          if (nl % (LPC / 2) == 0)
-            sm[C::SUM + (2 * UNITS + unit) * kFloatUnit + cl % 8 + nl / (LPC / 2)] = y[0];
+          // the neighbour's first channel is this lane's second
+          y[0] += __shfl_xor_sync(0xffffffffu, y[1], 1);
+#pragma unroll
+          for (int o = 2; o < LPC; o <<= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
+          if (nl < 2) sums[(2 * UNITS + i * VECS) * kFloatUnit] = y[0];
         }
       }
 #pragma unroll
       for (int i = kScanEvery - 1; i >= 0; --i) {
-        const int t = sub + i, unit = t * VECS + cl / 8;
-        const float4 d = *reinterpret_cast<const float4*>(sm + C::DX + unit * kPairUnit * 2 + (cl % 8) * 2);
-        const float2 y2 = *reinterpret_cast<const float2*>(sm + C::DY + unit * kFloatUnit + cl % 8);
-        const float4 Bq = *reinterpret_cast<const float4*>(sm + C::BC + t * 2 * NP + nl * 4);
-        const float4 Cq = *reinterpret_cast<const float4*>(sm + C::BC + t * 2 * NP + NP + nl * 4);
+        const float4 Bq = *reinterpret_cast<const float4*>(bcs + i * 2 * NP);
+        const float4 Cq = *reinterpret_cast<const float4*>(bcs + i * 2 * NP + NP);
         const float2 Bv[2] = {make_float2(Bq.x, Bq.y), make_float2(Bq.z, Bq.w)};
         const float2 Cv[2] = {make_float2(Cq.x, Cq.y), make_float2(Cq.z, Cq.w)};
-        const float2 dd[2] = {make_float2(d.x, d.x), make_float2(d.z, d.z)};
-        const float2 dx[2] = {make_float2(d.y, d.y), make_float2(d.w, d.w)};
-        const float2 dy[2] = {make_float2(y2.x, y2.x), make_float2(y2.y, y2.y)};
         float2 db[2], dc[2], gb[2], ua[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e) {
+          const float2 d = *reinterpret_cast<const float2*>(dxs[e] + i * VECS * kPairUnit);
+          const float2 dd = make_float2(d.x, d.x), dx = make_float2(d.y, d.y);
+          const float dy1 = dys[e][i * VECS * kFloatUnit];
+          const float2 dy = make_float2(dy1, dy1);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const float2 g = fma2(dy[e], Cv[p], G[e][p]);
-            db[p] = e == 0 ? mul2(dx[e], g) : fma2(dx[e], g, db[p]);
-            dc[p] = e == 0 ? mul2(dy[e], s[i][e][p]) : fma2(dy[e], s[i][e][p], dc[p]);
+            const float2 g = fma2(dy, Cv[p], G[e][p]);
+            db[p] = e == 0 ? mul2(dx, g) : fma2(dx, g, db[p]);
+            dc[p] = e == 0 ? mul2(dy, s[i][e][p]) : fma2(dy, s[i][e][p], dc[p]);
             gb[e] = p == 0 ? mul2(g, Bv[p]) : fma2(g, Bv[p], gb[e]);
-            G[e][p] = mul2(ev[i][e][p], g);
+            G[e][p] = mul2(kKeepDecay ? ev[i][e][p] : exp2_pair(mul2(dd, A2[e][p])), g);
             const float2 u = mul2(G[e][p], i == 0 ? h0[e][p] : s[i - 1][e][p]);
             ua[e] = p == 0 ? mul2(u, A2[e][p]) : fma2(u, A2[e][p], ua[e]);
-            dA[e][p] = fma2(u, dd[e], dA[e][p]);
+            dA[e][p] = fma2(u, dd, dA[e][p]);
           }
-        float st[4] = {gb[0].x + gb[0].y, gb[1].x + gb[1].y, ua[0].x + ua[0].y, ua[1].x + ua[1].y};
-        scatter_sum<4, LPC, 1>(st, nl);
-        float* sum = sm + C::SUM + unit * kFloatUnit + cl % 8;
-        if constexpr (LPC == 2) {  // lane 0: both channels' g B; lane 1: their u A
-          sum[nl * UNITS * kFloatUnit] = st[0];
-          sum[nl * UNITS * kFloatUnit + 1] = st[1];
-        } else if (nl % (LPC / 4) == 0) {
-          const int v = nl / (LPC / 4);
-          sum[(v >> 1) * UNITS * kFloatUnit + (v & 1)] = st[0];
         }
-        float bc[8] = {db[0].x, db[0].y, db[1].x, db[1].y, dc[0].x, dc[0].y, dc[1].x, dc[1].y};
-        scatter_sum<8, CL, LPC>(bc, cr);
-        float* red = sm + C::RED + (warp * kTile + t) * 2 * NP + nl * 4;
-        if constexpr (CL >= 8) {
-          if (cr % (CL / 8) == 0) {
-            const int v = cr / (CL / 8);
-            red[(v >> 2) * NP + (v & 3)] = bc[0];
-          }
-        } else {
+        // over the channel's lanes: the neighbour's first channel is this lane's second
+        float sg = gb[0].x + gb[0].y, su = ua[0].x + ua[0].y;
+        sg += __shfl_xor_sync(0xffffffffu, gb[1].x + gb[1].y, 1);
+        su += __shfl_xor_sync(0xffffffffu, ua[1].x + ua[1].y, 1);
+        if constexpr (LPC == 2) {
+          sums[i * VECS * kFloatUnit] = sg;
+          sums[(UNITS + i * VECS) * kFloatUnit] = su;
+        } else {  // lanes 0, 1 of a channel end with g B, lanes 2, 3 with u A
+          const bool up = nl & 2;
+          float v = (up ? su : sg) + __shfl_xor_sync(0xffffffffu, up ? sg : su, 2);
 #pragma unroll
-          for (int k = 0; k < 8 / CL; ++k) {
-            const int v = cr * (8 / CL) + k;
-            red[(v >> 2) * NP + (v & 3)] = bc[k];
+          for (int o = 4; o < LPC; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (nl < 4) sums[((nl >> 1) * UNITS + i * VECS) * kFloatUnit] = v;
+        }
+        // over the warp's channels: rank bit 0 halves the states by pairs, bit 1 the pair, bit 2
+        // chooses between dB and dC; what is sent is the partner's first half
+        float2 rb = db[0], rc = dc[0];
+        rb.x += __shfl_xor_sync(0xffffffffu, db[1].x, LPC);
+        rb.y += __shfl_xor_sync(0xffffffffu, db[1].y, LPC);
+        rc.x += __shfl_xor_sync(0xffffffffu, dc[1].x, LPC);
+        rc.y += __shfl_xor_sync(0xffffffffu, dc[1].y, LPC);
+        float* red = sm + C::RED + (warp * kTile + sub + i) * 2 * NP + nl * 4;
+        if constexpr (CL == 2) {
+          red[perm] = rb.x;
+          red[perm ^ 1] = rb.y;
+          red[NP + perm] = rc.x;
+          red[NP + (perm ^ 1)] = rc.y;
+        } else {
+          rb.x += __shfl_xor_sync(0xffffffffu, rb.y, 2 * LPC);
+          rc.x += __shfl_xor_sync(0xffffffffu, rc.y, 2 * LPC);
+          if constexpr (CL == 4) {
+            red[perm] = rb.x;
+            red[NP + perm] = rc.x;
+          } else {
+            const bool up = cr & 4;
+            float v = (up ? rc.x : rb.x) + __shfl_xor_sync(0xffffffffu, up ? rb.x : rc.x, 4 * LPC);
+            if constexpr (CL == 16) v += __shfl_xor_sync(0xffffffffu, v, 8 * LPC);
+            if (cr < 8) red[(up ? NP : 0) + perm] = v;
           }
         }
       }
@@ -287,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
         load_unit(sm + C::SUM + (UNITS + item) * kFloatUnit, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 pair = reinterpret_cast<const float4*>(sm + C::DX + item * kPairUnit * 2)[i];
+          const float4 pair = reinterpret_cast<const float4*>(sm + C::DX + item * kPairUnit)[i];
           v[i] = fma2(v[i], make_float2(kLn2, kLn2), mul2(x[i], sgb[i]));
           if (a.softplus) {
             const float2 rw = add2(d[i], *reinterpret_cast<const float2*>(sm + C::BIAS + cv + 2 * i));
@@ -295,12 +332,21 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
           }
           o[i] = fma2(make_float2(pair.x, pair.z), sgb[i],
                       mul2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), dy[i]));
-          const float2 dk = mul2(dy[i], x[i]);
-          float* acc = sm + C::ACC + 2 * i * kThreads + tid;
-          acc[0] += dk.x;
-          acc[kThreads] += dk.y;
-          acc[8 * kThreads] += v[i].x;
-          acc[9 * kThreads] += v[i].y;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float4* acc = reinterpret_cast<float4*>(sm + C::ACC) + i * kThreads + tid;
+          float4 k = acc[0], l = acc[2 * kThreads];
+          k.x = fmaf(dy[2 * i].x, x[2 * i].x, k.x);
+          k.y = fmaf(dy[2 * i].y, x[2 * i].y, k.y);
+          k.z = fmaf(dy[2 * i + 1].x, x[2 * i + 1].x, k.z);
+          k.w = fmaf(dy[2 * i + 1].y, x[2 * i + 1].y, k.w);
+          l.x += v[2 * i].x;
+          l.y += v[2 * i].y;
+          l.z += v[2 * i + 1].x;
+          l.w += v[2 * i + 1].y;
+          acc[0] = k;
+          acc[2 * kThreads] = l;
         }
         store_pairs<WIDE, 8>((T*)a.dx.p + b * a.dx.sb + t * a.dx.st + q.c0 + cv, o, n);
         store_pairs<WIDE, 8>((T*)a.ddt.p + b * a.ddt.sb + t * a.ddt.st + q.c0 + cv, v, n);
@@ -315,9 +361,9 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
     const float gs[4] = {G[e][0].x, G[e][0].y, G[e][1].x, G[e][1].y};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int n = nl * 4 + k;
-      if (cl + e < q.n && n < a.N) {
-        const long long at = (long long)(q.c0 + cl + e) * a.N + n, all = (long long)a.D * a.N;
+      const int n = nl * 4 + (k ^ perm);
+      if (ch[e] < q.n && n < a.N) {
+        const long long at = (long long)(q.c0 + ch[e]) * a.N + n, all = (long long)a.D * a.N;
         a.part_a[row * all + at] = da[k];
         if (seg == 0 && a.dstate_in != nullptr) a.dstate_in[b * all + at] = gs[k];
       }
@@ -329,7 +375,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanArgs a, int tile
     const int which = e / CT, c = e % CT;
     if (c < q.n) {
       float v = 0.f;
-      for (int w = c / 8; w < kThreads; w += VECS) v += sm[C::ACC + (which * 8 + c % 8) * kThreads + w];
+      for (int w = c / 8; w < kThreads; w += VECS) v += sm[C::ACC + ((which * 2 + c % 8 / 4) * kThreads + w) * 4 + c % 4];
       a.part_d[((long long)row * 2 + which) * a.D + q.c0 + c] = v;
     }
   }

@@ -20,25 +20,32 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|), with log(1 + e) = 2 artanh(s), s = e / (2 + e)
-// in [0, 1/3]: Gregory's series to s^13 leaves 2e-8 of the value, and small e keep their digits.
-// A quarter of log1pf's instructions, for every element of the sequence.
-__device__ __forceinline__ float softplusf(float v) {
-  const float e = exp2_fast(-fabsf(v) * kLog2e);
-  const float s = __fdividef(e, 2.f + e), z = s * s;
-  float p = fmaf(z, 1.f / 13.f, 1.f / 11.f);
-  p = fmaf(z, p, 1.f / 9.f);
-  p = fmaf(z, p, 1.f / 7.f);
-  p = fmaf(z, p, 1.f / 5.f);
-  p = fmaf(z, p, 1.f / 3.f);
-  p = fmaf(z, p, 1.f);
-  return fmaf(2.f * s, p, fmaxf(v, 0.f));
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1], of two values.  log(1 + e) / e is
+// a polynomial of degree 8, the best one in relative error on [0, 1] (found with Remez' exchange
+// algorithm in 50 digits): 1.4e-7 of the value with fp32 arithmetic, for small e as well.  Half
+// the instructions of log1pf, on the pipe that the exponentials leave free.
+__device__ __forceinline__ float2 softplus_pair(float2 v) {
+  const float2 e =
+      make_float2(exp2_fast(-fabsf(v.x) * kLog2e), exp2_fast(-fabsf(v.y) * kLog2e));
+  constexpr float c[9] = {9.999999699e-01f, -4.999949314e-01f, 3.331909679e-01f,
+                          -2.484298211e-01f, 1.910600644e-01f, -1.366324530e-01f,
+                          7.822594782e-02f, -2.950523728e-02f, 5.232694110e-03f};
+  float2 p = make_float2(c[8], c[8]);
+#pragma unroll
+  for (int i = 7; i >= 0; --i) p = fma2(e, p, make_float2(c[i], c[i]));
+  return fma2(e, p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
+__device__ __forceinline__ float softplusf(float v) { return softplus_pair(make_float2(v, v)).x; }
 
 // A unit is eight channels of one token in shared memory, written by one thread with 16-byte
-// stores and read by a warp along the channels.  Padding a unit of pairs to 80 bytes and one of
-// floats to 48 spreads eight threads' 16-byte accesses over all 32 banks.
-constexpr int kPairUnit = 10;   // float2 of a unit of pairs
+// stores and read by a warp along the channels.  The padding (16 bytes to a unit) spreads eight
+// threads' 16-byte accesses over all 32 banks.
+//
+// What bounds the inner loops is what shared memory hands to registers, 128 bytes a cycle and SM,
+// and a value that several lanes read counts once for each: a thread that holds four states of one
+// channel takes 10 bytes for each state and token, two channels 6.  So a thread holds two channels,
+// and nothing is stored twice to save a move.
+constexpr int kPairUnit = 20;   // floats of a unit of pairs (delta, w)
 constexpr int kFloatUnit = 12;  // floats of a unit of floats
 
 // Sums V values over L lanes that are STRIDE apart (rank: the lane's index among them) and
@@ -86,15 +93,15 @@ __device__ __forceinline__ void delta_of(const ScanArgs& a, const Raw<T, 8>& dt,
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     delta[i] = add2(delta[i], *reinterpret_cast<const float2*>(bias + 2 * i));
-    if (a.softplus) delta[i] = make_float2(softplusf(delta[i].x), softplusf(delta[i].y));
+    if (a.softplus) delta[i] = softplus_pair(delta[i]);
     if (!in || 2 * i >= n) delta[i].x = 0.f;
     if (!in || 2 * i + 1 >= n) delta[i].y = 0.f;
   }
 }
 // A unit of pairs (delta, w).
 template <typename T>
-__device__ __forceinline__ void stage_pair(const ScanArgs& a, const float2* w, const Raw<T, 8>& dt,
-                                           const float* bias, bool in, int n, float2* unit) {
+__device__ __forceinline__ void stage_pairs(const ScanArgs& a, const float2* w, const Raw<T, 8>& dt,
+                                            const float* bias, bool in, int n, float* unit) {
   float2 d[4];
   delta_of<T>(a, dt, bias, in, n, d);
 #pragma unroll
@@ -104,23 +111,32 @@ __device__ __forceinline__ void stage_pair(const ScanArgs& a, const float2* w, c
 // A unit of pairs (delta, delta x).  Absent elements of x were loaded as zero.
 template <typename T>
 __device__ __forceinline__ void stage_delta(const ScanArgs& a, const Raw<T, 8>& x, const Raw<T, 8>& dt,
-                                            const float* bias, bool in, int n, float2* unit) {
+                                            const float* bias, bool in, int n, float* unit) {
   float2 d[4], v[4];
   expand(x, v);
   delta_of<T>(a, dt, bias, in, n, d);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4*>(unit)[i] = make_float4(d[i].x, d[i].x * v[i].x, d[i].y, d[i].y * v[i].y);
+  for (int i = 0; i < 4; ++i) {
+    const float2 w = mul2(d[i], v[i]);
+    reinterpret_cast<float4*>(unit)[i] = make_float4(d[i].x, w.x, d[i].y, w.y);
+  }
+}
+
+// Element i becomes element i ^ perm.
+__device__ __forceinline__ float4 permuted(float4 v, int perm) {
+  if (perm & 2) v = make_float4(v.z, v.w, v.x, v.y);
+  if (perm & 1) v = make_float4(v.y, v.x, v.w, v.z);
+  return v;
 }
 
 // The state (or, REVERSE, the state's gradient) that enters segment `seg`, from what enters the
-// first (last) one in h and the segments between.
+// first (last) one in h and the segments between; A2 and h hold state i ^ perm at i.
 template <int NP, bool REVERSE>
 __device__ __forceinline__ void enter_segment(const ScanArgs& a, int b, int c, int nl, int seg,
-                                              const float2* A2, float2* h) {
+                                              const float2* A2, float2* h, int perm = 0) {
   for (int i = REVERSE ? a.segs - 1 : 0; REVERSE ? i > seg : i < seg; i += REVERSE ? -1 : 1) {
     const long long row = ((long long)i * a.B + b) * a.D + c;
-    const float4 s = *reinterpret_cast<const float4*>(a.seg_state + row * NP + nl * 4);
+    const float4 s = permuted(*reinterpret_cast<const float4*>(a.seg_state + row * NP + nl * 4), perm);
     const float2 sum = make_float2(a.seg_sum[row], a.seg_sum[row]);
     const float2 e0 = exp2_pair(mul2(sum, A2[0])), e1 = exp2_pair(mul2(sum, A2[1]));
     // a state of zero stays zero, however far a growing mode (A > 0) would have grown
@@ -132,8 +148,8 @@ __device__ __forceinline__ void enter_segment(const ScanArgs& a, int b, int c, i
 }
 
 // B and C of tokens t0 .. t0 + TT - 1 as fp32 rows [TT][2 NP]; zero from token `last` on and in the
-// padding.
-template <typename T, int NP, int TT>
+// padding.  COPIES > 1: copy p, STRIDE floats behind copy p - 1, holds element n ^ p at n.
+template <typename T, int NP, int TT, int COPIES = 1, int STRIDE = 0>
 __device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0, int last, float* out,
                                          int tid, int threads) {
   const T* bp = (const T*)a.b.p + b * a.b.sb + g * a.b.sh;
@@ -148,7 +164,13 @@ __device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0
       else
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
-      store8<true>(out + t * 2 * NP + (is_c ? NP : 0) + n, v, 8);
+#pragma unroll
+      for (int p = 0; p < COPIES; ++p) {
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = v[i ^ p];
+        store8<true>(out + p * STRIDE + t * 2 * NP + (is_c ? NP : 0) + n, w, 8);
+      }
     }
   } else {
     for (int e = tid; e < TT * 2 * NP; e += threads) {
@@ -156,7 +178,8 @@ __device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0
       float v = 0.f;
       if (t0 + t < last && n < a.N)
         v = r >= NP ? to_f32(cp[(t0 + t) * a.c.st + n]) : to_f32(bp[(t0 + t) * a.b.st + n]);
-      out[e] = v;
+#pragma unroll
+      for (int p = 0; p < COPIES; ++p) out[p * STRIDE + (e ^ p)] = v;
     }
   }
 }

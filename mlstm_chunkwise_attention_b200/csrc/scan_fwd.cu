@@ -1,11 +1,11 @@
 // Selective state space scan, forward and one-token step.
 //
 // The scan is serial in time, so parallelism comes from batches, channels and states: a
-// thread holds four states of one channel in registers and walks the sequence.  Tiles of 32
+// thread holds four states of two channels in registers and walks the sequence.  Tiles of 32
 // tokens go through shared memory: delta and delta x are computed once per (token,
 // channel) from 16-byte loads, B and C are shared by all channels, and y is summed over
-// the channel's lanes by a transposing reduction (LPC tokens at a time, one result per
-// lane), then gated and stored with 16-byte stores.
+// the channels' lanes by a transposing reduction (each lane ends with one token of one
+// channel), then gated and stored with 16-byte stores.
 //
 // Bound by the exponentials: one ex2 per state, channel and token.
 //
@@ -18,12 +18,28 @@ namespace mlstm {
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = 32;
+constexpr int kTile = 32;
+
+constexpr int kThreads = 64;
 
 template <int LPC>
 struct Shape {
-  static constexpr int NP = 4 * LPC, CT = kWarps * 32 / LPC, VECS = CT / 8;
+  static constexpr int NP = 4 * LPC, CT = 2 * kThreads / LPC, VECS = CT / 8;
   static constexpr int ITEMS = (kTile * VECS + kThreads - 1) / kThreads;  // units of a thread
+};
+
+// A thread's two channels, cl + swap first.  Neighbouring lanes take them in opposite orders, so that
+// in the sum over a channel's lanes each sends its second and keeps its first.
+template <int LPC>
+struct Lanes {
+  int nl, cl, ch[2];
+  __device__ __forceinline__ Lanes(int tid) {
+    const int lane = tid & 31;
+    nl = lane % LPC;
+    cl = ((tid / 32) * (32 / LPC) + lane / LPC) * 2;
+    ch[0] = cl + (nl & 1);
+    ch[1] = cl + 1 - (nl & 1);
+  }
 };
 
 // What a thread loads of one tile: its units of x and dt.
@@ -33,35 +49,40 @@ struct TileLoads {
 };
 
 template <typename T, int LPC, bool GATE, bool WIDE>
-__global__ void __launch_bounds__(kThreads, LPC == 4 ? 7 : 1) scan_fwd_kernel(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads, 7) scan_fwd_kernel(ScanArgs a, int tiles) {
   using S = Shape<LPC>;
   constexpr int NP = S::NP, CT = S::CT, VECS = S::VECS, ITEMS = S::ITEMS;
-  __shared__ __align__(16) float2 sd[kTile * VECS * kPairUnit];  // delta, delta x
+  __shared__ __align__(16) float sd[kTile * VECS * kPairUnit];  // delta, delta x
   __shared__ __align__(16) float sy[kTile * VECS * kFloatUnit];
   __shared__ __align__(16) float sbc[kTile][2 * NP];
   __shared__ __align__(16) float sbias[CT], sskip[CT];
-  const int tid = threadIdx.x, lane = tid & 31, nl = lane % LPC;
-  const int cl = (tid / 32) * (32 / LPC) + lane / LPC;  // channel within the tile
+  const int tid = threadIdx.x;
+  const Lanes<LPC> l(tid);
+  const int nl = l.nl;
   const int per_seg = a.B * a.G * tiles, seg = blockIdx.x / per_seg, bi = blockIdx.x % per_seg;
   const int b = bi / (tiles * a.G);
   const ChannelTile q = channel_tile(a, bi % (tiles * a.G), tiles, CT);
-  const bool live = cl < q.n;
-  const int c = q.c0 + cl, NC = (a.T + kScanEvery - 1) / kScanEvery;
+  const int NC = (a.T + kScanEvery - 1) / kScanEvery;
   const int first = seg * a.seg_len, last = min(first + a.seg_len, a.T);
-  float2 A2[2], h[2];
-  {
+  float2 A2[2][2], h[2][2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
     float av[4], hv[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int n = nl * 4 + k;
-      const bool on = live && n < a.N;
-      av[k] = on ? a.A[(long long)c * a.N + n] * kLog2e : 0.f;
-      hv[k] = on && a.state_in != nullptr ? a.state_in[((long long)b * a.D + c) * a.N + n] : 0.f;
+      const bool on = l.ch[e] < q.n && n < a.N;
+      const long long row = q.c0 + l.ch[e];
+      av[k] = on ? a.A[row * a.N + n] * kLog2e : 0.f;
+      hv[k] = on && a.state_in != nullptr ? a.state_in[((long long)b * a.D + row) * a.N + n] : 0.f;
     }
-    A2[0] = make_float2(av[0], av[1]); A2[1] = make_float2(av[2], av[3]);
-    h[0] = make_float2(hv[0], hv[1]); h[1] = make_float2(hv[2], hv[3]);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      A2[e][p] = make_float2(av[2 * p], av[2 * p + 1]);
+      h[e][p] = make_float2(hv[2 * p], hv[2 * p + 1]);
+    }
+    if (l.ch[e] < q.n) enter_segment<NP, false>(a, b, q.c0 + l.ch[e], nl, seg, A2[e], h[e]);
   }
-  if (live) enter_segment<NP, false>(a, b, c, nl, seg, A2, h);
   for (int i = tid; i < CT; i += kThreads) {
     sbias[i] = a.dt_bias != nullptr && i < q.n ? a.dt_bias[q.c0 + i] : 0.f;
     sskip[i] = a.skip != nullptr && i < q.n ? a.skip[q.c0 + i] : 0.f;
@@ -105,25 +126,45 @@ __global__ void __launch_bounds__(kThreads, LPC == 4 ? 7 : 1) scan_fwd_kernel(Sc
       }
     }
     __syncthreads();
-    for (int t = 0; t < kTile; t += LPC) {
-      float acc[LPC];
+    // eight tokens, between two saved states, at a time
+    constexpr int AT_ONCE = LPC / 2;  // tokens whose sums are taken together
+    const float* dsrc[2] = {sd + (l.cl / 8) * kPairUnit + (l.ch[0] % 8) * 2,
+                            sd + (l.cl / 8) * kPairUnit + (l.ch[1] % 8) * 2};
+    float* ydst = sy + ((nl >> 1) * VECS + l.cl / 8) * kFloatUnit + l.ch[0] % 8;
+#pragma unroll 1
+    for (int tg = 0; tg < kTile; tg += kScanEvery) {
+      if (a.saved != nullptr && t0 + tg < last) {
 #pragma unroll
-      for (int u = 0; u < LPC; ++u) {
-        if (a.saved != nullptr && ((t + u) % kScanEvery) == 0 && t0 + t + u < last && live)
-          *reinterpret_cast<float4*>(a.saved +
-                                     (((long long)b * NC + (t0 + t + u) / kScanEvery) * a.D + c) * NP +
-                                     nl * 4) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-        const float2 d = sd[((t + u) * VECS + cl / 8) * kPairUnit + cl % 8];
-        const float4 Bv = *reinterpret_cast<const float4*>(&sbc[t + u][nl * 4]);
-        const float4 Cv = *reinterpret_cast<const float4*>(&sbc[t + u][NP + nl * 4]);
-        const float2 dd = make_float2(d.x, d.x), ww = make_float2(d.y, d.y);
-        h[0] = fma2(exp2_pair(mul2(dd, A2[0])), h[0], mul2(ww, make_float2(Bv.x, Bv.y)));
-        h[1] = fma2(exp2_pair(mul2(dd, A2[1])), h[1], mul2(ww, make_float2(Bv.z, Bv.w)));
-        const float2 y = fma2(h[1], make_float2(Cv.z, Cv.w), mul2(h[0], make_float2(Cv.x, Cv.y)));
-        acc[u] = y.x + y.y;
+        for (int e = 0; e < 2; ++e)
+          if (l.ch[e] < q.n)
+            *reinterpret_cast<float4*>(
+                a.saved + (((long long)b * NC + (t0 + tg) / kScanEvery) * a.D + q.c0 + l.ch[e]) * NP +
+                nl * 4) = make_float4(h[e][0].x, h[e][0].y, h[e][1].x, h[e][1].y);
       }
-      scatter_sum<LPC, LPC, 1>(acc, nl);
-      sy[((t + nl) * VECS + cl / 8) * kFloatUnit + cl % 8] = acc[0];
+#pragma unroll
+      for (int ti = 0; ti < kScanEvery; ti += AT_ONCE) {
+        float acc[AT_ONCE];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          const int t = tg + ti + u;
+          const float4 Bv = *reinterpret_cast<const float4*>(&sbc[t][nl * 4]);
+          const float4 Cv = *reinterpret_cast<const float4*>(&sbc[t][NP + nl * 4]);
+          float y[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 d = *reinterpret_cast<const float2*>(dsrc[e] + t * VECS * kPairUnit);
+            const float2 dd = make_float2(d.x, d.x), ww = make_float2(d.y, d.y);
+            h[e][0] = fma2(exp2_pair(mul2(dd, A2[e][0])), h[e][0], mul2(ww, make_float2(Bv.x, Bv.y)));
+            h[e][1] = fma2(exp2_pair(mul2(dd, A2[e][1])), h[e][1], mul2(ww, make_float2(Bv.z, Bv.w)));
+            const float2 v =
+                fma2(h[e][1], make_float2(Cv.z, Cv.w), mul2(h[e][0], make_float2(Cv.x, Cv.y)));
+            y[e] = v.x + v.y;
+          }
+          acc[u] = y[0] + __shfl_xor_sync(0xffffffffu, y[1], 1);
+        }
+        scatter_sum<AT_ONCE, AT_ONCE, 2>(acc, nl >> 1);
+        ydst[(tg + ti) * VECS * kFloatUnit] = acc[0];
+      }
     }
     __syncthreads();
 #pragma unroll
@@ -146,11 +187,15 @@ __global__ void __launch_bounds__(kThreads, LPC == 4 ? 7 : 1) scan_fwd_kernel(Sc
     // the next tile's sd and sbc were last read before the barrier above; its sy is written
     // after the next one
   }
-  if (a.state_out != nullptr && live && last == a.T) {
-    const float hv[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
+  if (a.state_out != nullptr && last == a.T) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (nl * 4 + k < a.N) a.state_out[((long long)b * a.D + c) * a.N + nl * 4 + k] = hv[k];
+    for (int e = 0; e < 2; ++e) {
+      const float hv[4] = {h[e][0].x, h[e][0].y, h[e][1].x, h[e][1].y};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (l.ch[e] < q.n && nl * 4 + k < a.N)
+          a.state_out[((long long)b * a.D + q.c0 + l.ch[e]) * a.N + nl * 4 + k] = hv[k];
+    }
   }
 }
 
@@ -158,28 +203,33 @@ __global__ void __launch_bounds__(kThreads, LPC == 4 ? 7 : 1) scan_fwd_kernel(Sc
 // last; true, the gradient that all segments but the first hand back, from zero and dy alone.  With
 // them the segment's sum of delta, whose exponential carries a state across it.
 template <typename T, int LPC, bool REVERSE, bool GATE, bool WIDE>
-__global__ void __launch_bounds__(kThreads, LPC == 4 ? 7 : 1) scan_segment_kernel(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads, 7) scan_segment_kernel(ScanArgs a, int tiles) {
   using S = Shape<LPC>;
   constexpr int NP = S::NP, CT = S::CT, VECS = S::VECS, ITEMS = S::ITEMS;
-  __shared__ __align__(16) float2 sd[kTile * VECS * kPairUnit];  // delta and delta x, or delta and dy
-  __shared__ __align__(16) float sv[kTile][NP];                  // B, or C
+  __shared__ __align__(16) float sd[kTile * VECS * kPairUnit];  // delta and delta x, or delta and dy
+  __shared__ __align__(16) float sv[kTile][NP];                 // B, or C
   __shared__ __align__(16) float sbias[CT];
-  const int tid = threadIdx.x, lane = tid & 31, nl = lane % LPC;
-  const int cl = (tid / 32) * (32 / LPC) + lane / LPC;
+  const int tid = threadIdx.x;
+  const Lanes<LPC> l(tid);
+  const int nl = l.nl;
   const int per_seg = a.B * a.G * tiles, bi = blockIdx.x % per_seg;
   const int seg = blockIdx.x / per_seg + (REVERSE ? 1 : 0);
   const int b = bi / (tiles * a.G);
   const ChannelTile q = channel_tile(a, bi % (tiles * a.G), tiles, CT);
-  const bool live = cl < q.n;
-  const int c = q.c0 + cl;
   const int first = seg * a.seg_len, last = min(first + a.seg_len, a.T);
-  float av[4];
+  float2 A2[2][2], h[2][2] = {};
+  float sum[2] = {0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    av[k] = live && nl * 4 + k < a.N ? a.A[(long long)c * a.N + nl * 4 + k] * kLog2e : 0.f;
-  const float2 A2[2] = {make_float2(av[0], av[1]), make_float2(av[2], av[3])};
-  float2 h[2] = {};
-  float sum = 0.f;
+  for (int e = 0; e < 2; ++e) {
+    float av[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      av[k] = l.ch[e] < q.n && nl * 4 + k < a.N
+                  ? a.A[(long long)(q.c0 + l.ch[e]) * a.N + nl * 4 + k] * kLog2e
+                  : 0.f;
+    A2[e][0] = make_float2(av[0], av[1]);
+    A2[e][1] = make_float2(av[2], av[3]);
+  }
   for (int i = tid; i < CT; i += kThreads)
     sbias[i] = a.dt_bias != nullptr && i < q.n ? a.dt_bias[q.c0 + i] : 0.f;
   // the second factor: x, or dy (with its gate)
@@ -227,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, LPC == 4 ? 7 : 1) scan_segment_kerne
             for (int k = 0; k < 4; ++k)
               g[k] = mul2(g[k], make_float2(act_value<kActSilu>(z[k].x), act_value<kActSilu>(z[k].y)));
           }
-          stage_pair<T>(a, g, now.dt[m], sbias + cv, t0 + t < last, n, sd + item * kPairUnit);
+          stage_pairs<T>(a, g, now.dt[m], sbias + cv, t0 + t < last, n, sd + item * kPairUnit);
         }
       }
     }
@@ -237,29 +287,38 @@ __global__ void __launch_bounds__(kThreads, LPC == 4 ? 7 : 1) scan_segment_kerne
     }
     if (i + 1 < count) fetch(origin(i + 1));
     __syncthreads();
+    const float* dsrc[2] = {sd + (l.cl / 8) * kPairUnit + (l.ch[0] % 8) * 2,
+                            sd + (l.cl / 8) * kPairUnit + (l.ch[1] % 8) * 2};
 #pragma unroll 4
     for (int u = 0; u < kTile; ++u) {
       const int t = REVERSE ? kTile - 1 - u : u;
-      const float2 d = sd[(t * VECS + cl / 8) * kPairUnit + cl % 8];
       const float4 V = *reinterpret_cast<const float4*>(&sv[t][nl * 4]);
-      const float2 dd = make_float2(d.x, d.x), ww = make_float2(d.y, d.y);
-      const float2 e0 = exp2_pair(mul2(dd, A2[0])), e1 = exp2_pair(mul2(dd, A2[1]));
       const float2 v0 = make_float2(V.x, V.y), v1 = make_float2(V.z, V.w);
-      if (REVERSE) {
-        h[0] = mul2(e0, fma2(ww, v0, h[0]));
-        h[1] = mul2(e1, fma2(ww, v1, h[1]));
-      } else {
-        h[0] = fma2(e0, h[0], mul2(ww, v0));
-        h[1] = fma2(e1, h[1], mul2(ww, v1));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 d = *reinterpret_cast<const float2*>(dsrc[e] + t * VECS * kPairUnit);
+        const float2 dd = make_float2(d.x, d.x), ww = make_float2(d.y, d.y);
+        const float2 e0 = exp2_pair(mul2(dd, A2[e][0])), e1 = exp2_pair(mul2(dd, A2[e][1]));
+        if (REVERSE) {
+          h[e][0] = mul2(e0, fma2(ww, v0, h[e][0]));
+          h[e][1] = mul2(e1, fma2(ww, v1, h[e][1]));
+        } else {
+          h[e][0] = fma2(e0, h[e][0], mul2(ww, v0));
+          h[e][1] = fma2(e1, h[e][1], mul2(ww, v1));
+        }
+        sum[e] += d.x;
       }
-      sum += d.x;
     }
     __syncthreads();
   }
-  if (live) {
-    const long long row = ((long long)seg * a.B + b) * a.D + c;
-    *reinterpret_cast<float4*>(a.seg_state + row * NP + nl * 4) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-    if (nl == 0) a.seg_sum[row] = sum;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (l.ch[e] < q.n) {
+      const long long row = ((long long)seg * a.B + b) * a.D + q.c0 + l.ch[e];
+      *reinterpret_cast<float4*>(a.seg_state + row * NP + nl * 4) =
+          make_float4(h[e][0].x, h[e][0].y, h[e][1].x, h[e][1].y);
+      if (nl == 0) a.seg_sum[row] = sum[e];
+    }
   }
 }
 
@@ -378,8 +437,8 @@ cudaError_t by_type(const ScanArgs& a, cudaStream_t s) {
 
 ScanSegments scan_segments(int B, int T, int D, int N) {
   // Warps of an undivided scan, and how many tokens a segment keeps at least.
-  const long long warps = ((long long)B * D * scan_pad(N) + 127) / 128;
-  constexpr int want = 148 * 20, least = 4 * kTile;
+  const long long warps = ((long long)B * D * scan_pad(N) + 255) / 256;
+  constexpr int want = 148 * 12, least = 4 * kTile;
   long long segs = warps > 0 ? (want + warps - 1) / warps : 1;
   if (segs > T / least) segs = T / least;
   ScanSegments z;
