@@ -57,21 +57,33 @@ struct ScanArgs {
   float *dA, *dskip, *ddt_bias, *dstate_in;
   const float* dstate_out;
   float *part_bc, *part_a, *part_d;
-  // the sequence's segments (one: the whole of it)
-  float *seg_state, *seg_sum;   // [segs, B, D, scan_pad(N)], [segs, B, D]
+  // the sequence's segments (one: the whole of it).  At once: seg_state and seg_sum hold each
+  // segment's own state and its sum of delta, [segs, B, D, scan_pad(N)] and [segs, B, D].  In turn:
+  // seg_state is the state handed from a segment to the next, [B, D, scan_pad(N)], and `turn` a
+  // counter of taken items followed by each channel tile's finished segments, zero at the launch.
+  float *seg_state, *seg_sum;
+  unsigned int* turn;
   int seg_len, segs;
+  bool in_turn;
   int B, T, D, G, N, softplus, dtype;
   bool wide, wide_bc;           // 16-byte accesses of the [B, T, D] tensors / of B and C
 };
 constexpr int kScanEvery = 8;  // tokens between two saved states
 // States per channel as the kernels hold them: four to a lane, 2, 4, 8 or 16 lanes to a channel.
 inline int scan_pad(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
-// How the sequence is cut: into segments of `len` tokens (a multiple of the kernels' tiles) that
-// are scanned at once, where whole sequences are too few to fill the GPU.
+// How a pass cuts the sequence: into `count` segments of `len` tokens (a multiple of the kernels'
+// tiles), worked on at once where whole sequences are too few to fill the GPU, or in turn, each
+// segment's work taken up by whichever CTA is free, where they are so many that the last round of
+// CTAs would leave SMs idle.
 struct ScanSegments {
   int len, count;
+  bool in_turn;
+  int tiles;                    // CTAs of a segment (channel tiles of all batches)
 };
-ScanSegments scan_segments(int B, int T, int D, int N);
+ScanSegments scan_fwd_segments(int B, int T, int D, int G, int N);
+ScanSegments scan_bwd_segments(int B, int T, int D, int G, int N);
+// ctas: those of an undivided scan; slots: CTAs that the GPU holds at once.
+ScanSegments scan_cut(int T, long long ctas, int slots);
 struct ScanBwdSizes {
   int tiles;                    // channel tiles of one group
   size_t part_bc, part_a, part_d;  // floats
@@ -81,6 +93,9 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_reverse_segments(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t s);
+// Epochs of the scan kernels' last launches that gave up a wait (see tc::Abort).
+cudaError_t fetch_scan_fwd_error(unsigned int* flag);
+cudaError_t fetch_scan_bwd_error(unsigned int* flag);
 
 // ---- group norm --------------------------------------------------------------
 struct NormArgs {

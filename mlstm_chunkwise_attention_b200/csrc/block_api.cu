@@ -85,15 +85,19 @@ int fill(void* dst, const void* src, size_t bytes, void* stream, const char* whe
 }
 
 struct ScanWorkspace {
-  size_t seg_state, seg_sum, bc, a, d, total;
+  mlstm::ScanSegments cut;
+  size_t seg_state, seg_sum, turn, bc, a, d, total;
 };
-// The forward's workspace holds the segments alone (nothing for a whole sequence).
+// The forward's workspace holds what the segments need alone (nothing for a whole sequence).
 ScanWorkspace scan_workspace(int B, int T, int D, int G, int N, bool backward) {
   ScanWorkspace w = {};
-  const mlstm::ScanSegments g = mlstm::scan_segments(B, T, D, N);
-  const size_t rows = g.count > 1 ? (size_t)g.count * B * D : 0;
+  if ((long long)B * T == 0) return w;
+  w.cut = backward ? mlstm::scan_bwd_segments(B, T, D, G, N) : mlstm::scan_fwd_segments(B, T, D, G, N);
+  size_t rows = 0;
+  if (w.cut.count > 1) rows = (size_t)(w.cut.in_turn ? 1 : w.cut.count) * B * D;
   w.seg_sum = align256(rows * mlstm::scan_pad(N) * 4);
-  w.bc = align256(w.seg_sum + rows * 4);
+  w.turn = align256(w.seg_sum + (w.cut.in_turn ? 0 : rows * 4));
+  w.bc = align256(w.turn + (w.cut.in_turn ? ((size_t)w.cut.tiles + 1) * 4 : 0));
   w.total = w.bc;
   if (backward) {
     const mlstm::ScanBwdSizes z = mlstm::scan_bwd_sizes(B, T, D, G, N);
@@ -103,12 +107,15 @@ ScanWorkspace scan_workspace(int B, int T, int D, int G, int N, bool backward) {
   }
   return w;
 }
-void use_segments(mlstm::ScanArgs* a, char* ws, const ScanWorkspace& w) {
-  const mlstm::ScanSegments g = mlstm::scan_segments(a->B, a->T, a->D, a->N);
-  a->seg_len = g.len;
-  a->segs = g.count;
+int use_segments(mlstm::ScanArgs* a, char* ws, const ScanWorkspace& w, void* stream) {
+  a->seg_len = w.cut.len;
+  a->segs = w.cut.count;
+  a->in_turn = w.cut.in_turn;
   a->seg_state = (float*)(ws + w.seg_state);
   a->seg_sum = (float*)(ws + w.seg_sum);
+  a->turn = (unsigned int*)(ws + w.turn);
+  if (!a->in_turn) return MLSTM_OK;
+  return fill(a->turn, nullptr, ((size_t)w.cut.tiles + 1) * 4, stream, "scan turns");
 }
 
 // The inputs of a scan call; T is that of the call (1 for a step).
@@ -270,10 +277,10 @@ int mlstm_scan_fwd(const mlstm_scan_t* p, const mlstm_rows_t* y, void* saved, fl
   const ScanWorkspace w = scan_workspace(p->B, p->T, p->D, p->G, p->N, false);
   if (off16(workspace)) return MLSTM_ERR_INVALID;
   if (w.total > 0 && (workspace == nullptr || workspace_bytes < w.total)) return MLSTM_ERR_WORKSPACE;
-  use_segments(&a, (char*)workspace, w);
   a.state_out = state_out;
   a.saved = (float*)saved;
   if ((st = pending_error("before mlstm_scan_fwd")) != MLSTM_OK) return st;
+  if ((st = use_segments(&a, (char*)workspace, w, stream)) != MLSTM_OK) return st;
   return cuda_result(mlstm::launch_scan_fwd(a, (cudaStream_t)stream), "scan_fwd");
 }
 
@@ -341,11 +348,11 @@ int mlstm_scan_bwd(const mlstm_scan_t* p, const mlstm_rows_t* dy, const void* sa
   a.dA = grads->da; a.dskip = grads->dskip; a.ddt_bias = grads->ddt_bias;
   a.dstate_in = grads->dstate_in;
   char* ws = (char*)workspace;
-  use_segments(&a, ws, w);
   a.part_bc = (float*)(ws + w.bc);
   a.part_a = (float*)(ws + w.a);
   a.part_d = (float*)(ws + w.d);
   if ((st = pending_error("before mlstm_scan_bwd")) != MLSTM_OK) return st;
+  if ((st = use_segments(&a, ws, w, stream)) != MLSTM_OK) return st;
   return cuda_result(mlstm::launch_scan_bwd(a, (cudaStream_t)stream), "scan_bwd");
 }
 

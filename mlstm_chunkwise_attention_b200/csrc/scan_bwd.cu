@@ -7,11 +7,12 @@
 //   ddelta_t = sum_n u_t A + x_t sum_n g_t B_t               dx_t = delta_t sum_n g_t B_t + skip dy_t
 //
 // The forward kept the state entering every eighth token, so eight tokens at a time are
-// recomputed forwards into registers (e and s, 128 of them) and walked backwards: one ex2 per
-// state and token.  A lane holds four states of two channels; sums over a channel's states
-// run along LPC lanes, sums over channels along the others, both as transposing reductions,
-// then over the CTA's warps in shared memory.  Each CTA writes its share of dB and dC; a
-// second kernel adds the shares in a fixed order.
+// recomputed forwards into registers (s; e is computed again on the way back, since the
+// exponentials' pipe has room and 64 registers do not) and walked backwards.  A lane holds four
+// states of two channels; sums over a channel's states run along LPC lanes, sums over channels
+// along the others, both as transposing reductions, then over the CTA's warps in shared memory.
+// Each CTA writes its share of dB and dC; a second kernel adds the shares in a fixed order.
+#include "internal.h"
 #include "scan_common.cuh"
 
 namespace mlstm {
@@ -19,13 +20,9 @@ namespace mlstm {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = 16;
-#ifndef KEEP
-#define KEEP 1
-#endif
-#ifndef CTAS
-#define CTAS 2
-#endif
-constexpr bool kKeepDecay = KEEP;
+constexpr int kCtas = 3;  // of an SM
+constexpr int kSlots = 148 * kCtas;
+__device__ unsigned int g_scan_bwd_error = 0;  // epoch of the last launch that gave up a wait
 static_assert(kTile == 2 * kScanEvery, "two saved states to a tile");
 
 template <typename T, int LPC>
@@ -41,17 +38,17 @@ struct Cfg {
   static constexpr int ORDER = kTile * 2 * NP + 8;  // floats of a copy, with 8 to spread the banks
   // shared memory, in floats: delta and delta x of the tile, dy of the tile; sums over states of g B,
   // u A and C s; B and C; dB and dC of each warp [warps][tile][2 NP]; dskip and ddt_bias shares of
-  // each thread's channels [4][threads] of four; dt_bias and skip; two saved states ahead
-  // [2][2][threads] of four floats; and two tiles of x, dt, dy, z as they lie in memory
+  // each thread's channels [4][threads] of four; dt_bias and skip; the next saved state [2][threads] of
+  // four floats; and the tile's x, dt, dy, z as they lie in memory
   static constexpr int DX = 0, DY = DX + UNITS * kPairUnit, SUM = DY + UNITS * kFloatUnit,
                        BC = SUM + 3 * UNITS * kFloatUnit, RED = BC + 4 * ORDER,
                        ACC = RED + kWarps * kTile * 2 * NP, BIAS = ACC + 16 * kThreads, SKIP = BIAS + CT,
-                       SAVED = SKIP + CT, RAW = SAVED + 16 * kThreads,
-                       TOTAL = RAW + 2 * 4 * UNITS * 8 * (int)sizeof(T) / 4;
+                       SAVED = SKIP + CT, RAW = SAVED + 8 * kThreads,
+                       TOTAL = RAW + 4 * UNITS * 8 * (int)sizeof(T) / 4;
 };
 
 template <typename T, int LPC, bool GATE, bool WIDE>
-__global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, int tiles, unsigned int epoch) {
   using C = Cfg<T, LPC>;
   constexpr int NP = C::NP, CL = C::CL, CT = C::CT, VECS = C::VECS, UNITS = C::UNITS;
   extern __shared__ __align__(16) float sm[];
@@ -60,11 +57,18 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
   const int swap = nl & 1;              // it takes them in this order: cl + swap, then the other
   const int perm = (cr & 1) * 2 + (CL >= 4 ? (cr >> 1) & 1 : 0);  // and state k ^ perm as its k-th
   const int ch[2] = {cl + swap, cl + 1 - swap};
-  const int per_seg = a.B * a.G * tiles, seg = blockIdx.x / per_seg, bi = blockIdx.x % per_seg;
+  __shared__ int box[2];
+  const tc::Abort abort{&g_scan_bwd_error, epoch};
+  const int per_seg = a.B * a.G * tiles, NC = (a.T + kScanEvery - 1) / kScanEvery;
+  for (bool once = true;; once = false) {
+  const int work = next_item(a, blockIdx.x, once, per_seg * a.segs, box);
+  if (work >= per_seg * a.segs) return;
+  const int seg = a.segs - 1 - work / per_seg, bi = work % per_seg;
   const int b = bi / (tiles * a.G), ti = bi % (tiles * a.G);
   const ChannelTile q = channel_tile(a, ti, tiles, CT);
-  const int NC = (a.T + kScanEvery - 1) / kScanEvery;
   const int first = seg * a.seg_len, last = min(first + a.seg_len, a.T);
+  const bool handed = a.in_turn && seg < a.segs - 1;  // the segment behind hands its gradient on
+  if (handed && !wait_turn(a, bi, a.segs - 1 - seg, abort, box + 1)) return;
   float2 A2[2][2], G[2][2], dA[2][2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -84,7 +88,15 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
       G[e][p] = make_float2(gv[2 * p], gv[2 * p + 1]);
       dA[e][p] = make_float2(0.f, 0.f);
     }
-    if (ch[e] < q.n) enter_segment<NP, true>(a, b, q.c0 + ch[e], nl, seg, A2[e], G[e], perm);
+    if (ch[e] < q.n && handed) {
+      const float4 v = permuted(
+          __ldcg(reinterpret_cast<const float4*>(a.seg_state + ((long long)b * a.D + q.c0 + ch[e]) * NP + nl * 4)),
+          perm);
+      G[e][0] = make_float2(v.x, v.y);
+      G[e][1] = make_float2(v.z, v.w);
+    } else if (ch[e] < q.n && !a.in_turn) {
+      enter_segment<NP, true>(a, b, q.c0 + ch[e], nl, seg, A2[e], G[e], perm);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -97,24 +109,26 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
                     (const T*)a.y.p + b * a.y.sb + q.c0,
                     GATE ? (const T*)a.z.p + b * a.z.sb + q.c0 : nullptr};
   const long long stride[4] = {a.x.st, a.dt.st, a.y.st, a.z.st};
-  auto raw = [&](int stage, int tensor, int item) {
-    return reinterpret_cast<Raw<T, 8>*>(sm + C::RAW) + (stage * 4 + tensor) * UNITS + item;
+  auto raw = [&](int tensor, int item) {
+    return reinterpret_cast<Raw<T, 8>*>(sm + C::RAW) + tensor * UNITS + item;
   };
   // A thread fetches and reads only its own units, so no barrier is needed for them.
-  auto fetch = [&](int t0, int stage) {
+  auto fetch = [&](int t0) {
 #pragma unroll
     for (int m = 0; m < C::ITEMS; ++m) {
       const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
       if (item < UNITS) {
 #pragma unroll
         for (int k = 0; k < 3 + GATE; ++k) {
-          Raw<T, 8>* to = raw(stage, k, item);
+          Raw<T, 8>* to = raw(k, item);
           const T* from = in[k] + t * stride[k] + cv;
           if (t < last && n > 0) {
             if (WIDE) {
 #pragma unroll
               for (int h = 0; h < (int)sizeof(Raw<T, 8>) / 16; ++h)
                 copy16_async((char*)to + 16 * h, (const char*)from + 16 * h);
+              // the same units of the next tile, into L2
+              if (t - kTile >= first) prefetch_l2(from - kTile * stride[k]);
             } else {
               Raw<T, 8> r;
               load_raw<false>(from, r, n);
@@ -128,36 +142,36 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
     }
   };
   // The lane's states entering the eight tokens from t on; each thread reads its own slots.
-  auto fetch_saved = [&](int t, int stage) {
-    if (t < first) return;
+  auto fetch_saved = [&](int t) {
+    if (t < first || t >= last) return;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      if (ch[e] < q.n && t < last)
-        copy16_async(sm + C::SAVED + ((stage * 2 + e) * kThreads + tid) * 4,
+      if (ch[e] < q.n)
+        copy16_async(sm + C::SAVED + (e * kThreads + tid) * 4,
                      a.saved + (((long long)b * NC + t / kScanEvery) * a.D + q.c0 + ch[e]) * NP + nl * 4);
   };
 #pragma unroll
-  for (int i = 0; i < 4; ++i)  // channels that do not exist keep a state of zero
+  for (int i = 0; i < 2; ++i)  // channels that do not exist keep a state of zero
     *reinterpret_cast<float4*>(sm + C::SAVED + (i * kThreads + tid) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
   const int top = (last - 1 - first) / kTile * kTile + first;
-  fetch(top, 0);
-  fetch_saved(top + kTile - kScanEvery, 0);  // the first eight tokens taken lie in stage 0
-  copies_commit();
-  int stage = 0;
+  // the upper eight tokens of the first tile may lie behind the end; then the lower come first
+  fetch_saved(top + kScanEvery < last ? top + kScanEvery : top);
   __syncthreads();
-  for (int t0 = top; t0 >= first; t0 -= kTile, stage ^= 1) {
+  for (int t0 = top; t0 >= first; t0 -= kTile) {
+    fetch(t0);
+    copies_commit();
     stage_bc<T, NP, kTile, 4, C::ORDER>(a, b, q.g, t0, last, sm + C::BC, tid, kThreads);
     copies_wait<0>();
 #pragma unroll
     for (int m = 0; m < C::ITEMS; ++m) {
       const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
       if (item < UNITS) {
-        stage_delta<T>(a, *raw(stage, 0, item), *raw(stage, 1, item), sm + C::BIAS + cv, t < last, n,
+        stage_delta<T>(a, *raw(0, item), *raw(1, item), sm + C::BIAS + cv, t < last, n,
                        sm + C::DX + item * kPairUnit);
         float2 g[4], z[4];
-        expand(*raw(stage, 2, item), g);
+        expand(*raw(2, item), g);
         if (GATE) {
-          expand(*raw(stage, 3, item), z);
+          expand(*raw(3, item), z);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             g[i] = mul2(g[i], make_float2(act_value<kActSilu>(z[i].x), act_value<kActSilu>(z[i].y)));
@@ -165,24 +179,21 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
         store_unit(sm + C::DY + item * kFloatUnit, g);
       }
     }
-    if (t0 - kTile >= first) fetch(t0 - kTile, stage ^ 1);
-    copies_commit();
     __syncthreads();
 #pragma unroll 1
     for (int sub = kTile - kScanEvery; sub >= 0; sub -= kScanEvery) {
-      const int half = sub / kScanEvery;  // the upper eight tokens' states lie in stage 0, the lower's in 1
-      fetch_saved(t0 + sub - kScanEvery, half);
-      copies_commit();
-      if (half == 0) copies_wait<1>();  // the upper's were waited for with the tile
       if (t0 + sub >= last) continue;
-      float2 h0[2][2], s[kScanEvery][2][2], ev[kKeepDecay ? kScanEvery : 1][2][2];
+      copies_wait<0>();
+      float2 h0[2][2], s[kScanEvery][2][2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float4 v = permuted(
-            *reinterpret_cast<const float4*>(sm + C::SAVED + (((half ^ 1) * 2 + e) * kThreads + tid) * 4), perm);
+            *reinterpret_cast<const float4*>(sm + C::SAVED + (e * kThreads + tid) * 4), perm);
         h0[e][0] = make_float2(v.x, v.y);
         h0[e][1] = make_float2(v.z, v.w);
       }
+      fetch_saved(t0 + sub - kScanEvery);
+      copies_commit();
       const float* bcs = sm + C::BC + perm * C::ORDER + sub * 2 * NP + nl * 4;
       const float* dxs[2] = {sm + C::DX + (sub * VECS + cl / 8) * kPairUnit + (ch[0] % 8) * 2,
                              sm + C::DX + (sub * VECS + cl / 8) * kPairUnit + (ch[1] % 8) * 2};
@@ -199,9 +210,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
           const float2 dd = make_float2(d.x, d.x), dx = make_float2(d.y, d.y);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const float2 w = exp2_pair(mul2(dd, A2[e][p]));
-            if (kKeepDecay) ev[i][e][p] = w;
-            s[i][e][p] = fma2(w, i == 0 ? h0[e][p] : s[i - 1][e][p], mul2(dx, Bv[p]));
+            s[i][e][p] = fma2(exp2_pair(mul2(dd, A2[e][p])), i == 0 ? h0[e][p] : s[i - 1][e][p], mul2(dx, Bv[p]));
           }
         }
         if (GATE) {  // the ungated output, for dz
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
             db[p] = e == 0 ? mul2(dx, g) : fma2(dx, g, db[p]);
             dc[p] = e == 0 ? mul2(dy, s[i][e][p]) : fma2(dy, s[i][e][p], dc[p]);
             gb[e] = p == 0 ? mul2(g, Bv[p]) : fma2(g, Bv[p], gb[e]);
-            G[e][p] = mul2(kKeepDecay ? ev[i][e][p] : exp2_pair(mul2(dd, A2[e][p])), g);
+            G[e][p] = mul2(exp2_pair(mul2(dd, A2[e][p])), g);
             const float2 u = mul2(G[e][p], i == 0 ? h0[e][p] : s[i - 1][e][p]);
             ua[e] = p == 0 ? mul2(u, A2[e][p]) : fma2(u, A2[e][p], ua[e]);
             dA[e][p] = fma2(u, dd, dA[e][p]);
@@ -302,13 +311,13 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
       const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
       if (item < UNITS && t < last && n > 0) {
         float2 x[4], d[4], v[4], sgb[4], dy[4], o[4];
-        expand(*raw(stage, 0, item), x);
+        expand(*raw(0, item), x);
         load_unit(sm + C::SUM + item * kFloatUnit, sgb);
         load_unit(sm + C::DY + item * kFloatUnit, dy);
         if (GATE) {
           float2 g[4], z[4], y[4];
-          expand(*raw(stage, 2, item), g);
-          expand(*raw(stage, 3, item), z);
+          expand(*raw(2, item), g);
+          expand(*raw(3, item), z);
           load_unit(sm + C::SUM + (2 * UNITS + item) * kFloatUnit, y);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
           }
           store_pairs<WIDE, 8>((T*)a.dz.p + b * a.dz.sb + t * a.dz.st + q.c0 + cv, o, n);
         }
-        expand(*raw(stage, 1, item), d);
+        expand(*raw(1, item), d);
         load_unit(sm + C::SUM + (UNITS + item) * kFloatUnit, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -368,7 +377,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
         if (seg == 0 && a.dstate_in != nullptr) a.dstate_in[b * all + at] = gs[k];
       }
     }
+    if (a.in_turn && seg > 0 && ch[e] < q.n)
+      __stcg(reinterpret_cast<float4*>(a.seg_state + ((long long)b * a.D + q.c0 + ch[e]) * NP + nl * 4),
+             permuted(make_float4(gs[0], gs[1], gs[2], gs[3]), perm));
   }
+  if (a.in_turn && seg > 0) pass_turn(a, bi);
   // threads with the same channels: tid % VECS (a thread keeps its vector through all items)
   static_assert(kThreads % VECS == 0, "a thread's channels are the same in every item");
   for (int e = tid; e < 2 * CT; e += kThreads) {
@@ -378,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) scan_bwd_kernel(ScanArgs a, in
       for (int w = c / 8; w < kThreads; w += VECS) v += sm[C::ACC + ((which * 2 + c % 8 / 4) * kThreads + w) * 4 + c % 4];
       a.part_d[((long long)row * 2 + which) * a.D + q.c0 + c] = v;
     }
+  }
   }
 }
 
@@ -417,8 +431,9 @@ cudaError_t bwd_kernel(const ScanArgs& a, int tiles, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<T, LPC, GATE, WIDE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  scan_bwd_kernel<T, LPC, GATE, WIDE>
-      <<<(unsigned)((long long)a.B * a.G * tiles * a.segs), kThreads, bytes, s>>>(a, tiles);
+  const long long items = (long long)a.B * a.G * tiles * a.segs;
+  const long long grid = a.in_turn && items > kSlots ? kSlots : items;
+  scan_bwd_kernel<T, LPC, GATE, WIDE><<<(unsigned)grid, kThreads, bytes, s>>>(a, tiles, next_epoch());
   return cudaGetLastError();
 }
 
@@ -426,7 +441,7 @@ template <typename T, int LPC>
 cudaError_t bwd(const ScanArgs& a, cudaStream_t s) {
   const int tiles = (a.D / a.G + Cfg<T, LPC>::CT - 1) / Cfg<T, LPC>::CT;
   cudaError_t e;
-  if (a.segs > 1 && (e = launch_scan_reverse_segments(a, s)) != cudaSuccess) return e;
+  if (a.segs > 1 && !a.in_turn && (e = launch_scan_reverse_segments(a, s)) != cudaSuccess) return e;
   if (a.z.p != nullptr)
     e = a.wide ? bwd_kernel<T, LPC, true, true>(a, tiles, s) : bwd_kernel<T, LPC, true, false>(a, tiles, s);
   else
@@ -454,12 +469,21 @@ cudaError_t by_states(const ScanArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+ScanSegments scan_bwd_segments(int B, int T, int D, int G, int N) {
+  const int CT = kWarps * 2 * 32 * 4 / scan_pad(N);
+  return scan_cut(T, (long long)B * G * ((D / G + CT - 1) / CT), kSlots);
+}
+
+cudaError_t fetch_scan_bwd_error(unsigned int* flag) {
+  return cudaMemcpyFromSymbol(flag, g_scan_bwd_error, sizeof(unsigned int));
+}
+
 ScanBwdSizes scan_bwd_sizes(int B, int T, int D, int G, int N) {
   const int NP = scan_pad(N), CT = kWarps * 2 * 32 * 4 / NP;
   ScanBwdSizes z;
   z.tiles = (D / G + CT - 1) / CT;
   z.part_bc = (size_t)z.tiles * B * T * G * 2 * NP;
-  const int segs = scan_segments(B, T, D, N).count;
+  const int segs = scan_bwd_segments(B, T, D, G, N).count;
   z.part_a = (size_t)segs * B * D * N;
   z.part_d = (size_t)segs * B * 2 * D;
   return z;

@@ -8,6 +8,7 @@
 #pragma once
 
 #include "block_common.cuh"
+#include "tc_common.cuh"
 
 namespace mlstm {
 
@@ -184,11 +185,62 @@ __device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0
   }
 }
 
+// ---- segments in turn ----
+// Work items are (segment, channel tile), all tiles of a segment before the next segment's, and a CTA
+// takes the next one from a counter when it is free.  An item waits for its tile's item of the
+// segment before, which was taken earlier by a CTA that runs: so some CTA can always go on,
+// however many of them are resident, and the wait is bounded as the tensor-core kernels' are.
+
+// The next item, for all threads of the CTA (a barrier inside, which also ends the last item's use of
+// shared memory); `only`: the CTA's one item where segments are not taken in turn.
+__device__ __forceinline__ int next_item(const ScanArgs& a, int only, bool first, int total, int* box) {
+  __syncthreads();
+  if (threadIdx.x == 0) *box = a.in_turn ? (int)atomicAdd(a.turn, 1u) : first ? only : total;
+  __syncthreads();
+  return *box;
+}
+
+// Waits until `tile` has finished `count` segments; false if the wait was given up.  `box` is not
+// next_item's: its slow readers may not be through.
+__device__ __forceinline__ bool wait_turn(const ScanArgs& a, int tile, unsigned int count,
+                                          const tc::Abort& abort, int* box) {
+  if (threadIdx.x == 0) {
+    const unsigned int* done = a.turn + 1 + tile;
+    bool ok = true;
+    const uint64_t t0 = tc::global_timer_ns();
+    for (unsigned int i = 1;; ++i) {
+      unsigned int v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+      if (v >= count) break;
+      if ((i & 63) == 0 && (abort.raised() || tc::global_timer_ns() - t0 > tc::kWaitTimeoutNs)) {
+        abort.raise();
+        ok = false;
+        break;
+      }
+      __nanosleep(200);
+    }
+    *box = ok;
+  }
+  __syncthreads();
+  return *box != 0;
+}
+
+// Hands the tile on: every thread's stores before this are visible to the CTA that waits for it.
+__device__ __forceinline__ void pass_turn(const ScanArgs& a, int tile) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0)
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.turn + 1 + tile) : "memory");
+}
+
 // A 16-byte copy into shared memory that completes in the background.
 __device__ __forceinline__ void copy16_async(void* smem, const void* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)),
                "l"(gmem)
                : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* gmem) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(gmem));
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>

@@ -12,6 +12,7 @@
 // With few rows the sequence is cut into segments that are scanned at once.  A first pass finds
 // each segment's state from zero and its sum of delta; segment j then starts from
 // sum_i exp(A sum of delta over i + 1 .. j - 1) state_i, which each CTA adds up for itself.
+#include "internal.h"
 #include "scan_common.cuh"
 
 namespace mlstm {
@@ -21,6 +22,9 @@ namespace {
 constexpr int kTile = 32;
 
 constexpr int kThreads = 64;
+constexpr int kCtas = 8;  // of an SM
+constexpr int kSlots = 148 * kCtas;
+__device__ unsigned int g_scan_fwd_error = 0;  // epoch of the last launch that gave up a wait
 
 template <int LPC>
 struct Shape {
@@ -49,7 +53,8 @@ struct TileLoads {
 };
 
 template <typename T, int LPC, bool GATE, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 7) scan_fwd_kernel(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads, kCtas)
+    scan_fwd_kernel(ScanArgs a, int tiles, unsigned int epoch) {
   using S = Shape<LPC>;
   constexpr int NP = S::NP, CT = S::CT, VECS = S::VECS, ITEMS = S::ITEMS;
   __shared__ __align__(16) float sd[kTile * VECS * kPairUnit];  // delta, delta x
@@ -59,11 +64,18 @@ __global__ void __launch_bounds__(kThreads, 7) scan_fwd_kernel(ScanArgs a, int t
   const int tid = threadIdx.x;
   const Lanes<LPC> l(tid);
   const int nl = l.nl;
-  const int per_seg = a.B * a.G * tiles, seg = blockIdx.x / per_seg, bi = blockIdx.x % per_seg;
+  __shared__ int box[2];
+  const tc::Abort abort{&g_scan_fwd_error, epoch};
+  const int per_seg = a.B * a.G * tiles, NC = (a.T + kScanEvery - 1) / kScanEvery;
+  for (bool once = true;; once = false) {
+  const int work = next_item(a, blockIdx.x, once, per_seg * a.segs, box);
+  if (work >= per_seg * a.segs) return;
+  const int seg = work / per_seg, bi = work % per_seg;
   const int b = bi / (tiles * a.G);
   const ChannelTile q = channel_tile(a, bi % (tiles * a.G), tiles, CT);
-  const int NC = (a.T + kScanEvery - 1) / kScanEvery;
   const int first = seg * a.seg_len, last = min(first + a.seg_len, a.T);
+  const bool handed = a.in_turn && seg > 0;  // the segment before hands its state on
+  if (handed && !wait_turn(a, bi, seg, abort, box + 1)) return;
   float2 A2[2][2], h[2][2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -81,7 +93,14 @@ __global__ void __launch_bounds__(kThreads, 7) scan_fwd_kernel(ScanArgs a, int t
       A2[e][p] = make_float2(av[2 * p], av[2 * p + 1]);
       h[e][p] = make_float2(hv[2 * p], hv[2 * p + 1]);
     }
-    if (l.ch[e] < q.n) enter_segment<NP, false>(a, b, q.c0 + l.ch[e], nl, seg, A2[e], h[e]);
+    if (l.ch[e] < q.n && handed) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(
+          a.seg_state + ((long long)b * a.D + q.c0 + l.ch[e]) * NP + nl * 4));
+      h[e][0] = make_float2(v.x, v.y);
+      h[e][1] = make_float2(v.z, v.w);
+    } else if (l.ch[e] < q.n && !a.in_turn) {
+      enter_segment<NP, false>(a, b, q.c0 + l.ch[e], nl, seg, A2[e], h[e]);
+    }
   }
   for (int i = tid; i < CT; i += kThreads) {
     sbias[i] = a.dt_bias != nullptr && i < q.n ? a.dt_bias[q.c0 + i] : 0.f;
@@ -197,13 +216,22 @@ __global__ void __launch_bounds__(kThreads, 7) scan_fwd_kernel(ScanArgs a, int t
           a.state_out[((long long)b * a.D + q.c0 + l.ch[e]) * a.N + nl * 4 + k] = hv[k];
     }
   }
+  if (a.in_turn && last < a.T) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (l.ch[e] < q.n)
+        __stcg(reinterpret_cast<float4*>(a.seg_state + ((long long)b * a.D + q.c0 + l.ch[e]) * NP + nl * 4),
+               make_float4(h[e][0].x, h[e][0].y, h[e][1].x, h[e][1].y));
+    pass_turn(a, bi);
+  }
+  }
 }
 
 // A segment's own state: REVERSE false, the forward state from zero over all segments but the
 // last; true, the gradient that all segments but the first hand back, from zero and dy alone.  With
 // them the segment's sum of delta, whose exponential carries a state across it.
 template <typename T, int LPC, bool REVERSE, bool GATE, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 7) scan_segment_kernel(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(kThreads, kCtas) scan_segment_kernel(ScanArgs a, int tiles) {
   using S = Shape<LPC>;
   constexpr int NP = S::NP, CT = S::CT, VECS = S::VECS, ITEMS = S::ITEMS;
   __shared__ __align__(16) float sd[kTile * VECS * kPairUnit];  // delta and delta x, or delta and dy
@@ -388,18 +416,19 @@ cudaError_t segments(const ScanArgs& a, cudaStream_t s) {
 
 template <typename T, int LPC>
 cudaError_t fwd(const ScanArgs& a, cudaStream_t s) {
-  if (a.segs > 1) {
+  if (a.segs > 1 && !a.in_turn) {
     const cudaError_t e = segments<T, LPC, false>(a, s);
     if (e != cudaSuccess) return e;
   }
   const int tiles = (a.D / a.G + Shape<LPC>::CT - 1) / Shape<LPC>::CT;
-  const unsigned grid = (unsigned)((long long)a.B * a.G * tiles * a.segs);
+  const long long items = (long long)a.B * a.G * tiles * a.segs;
+  const unsigned grid = (unsigned)(a.in_turn && items > kSlots ? kSlots : items), epoch = next_epoch();
   if (a.z.p != nullptr) {
-    if (a.wide) scan_fwd_kernel<T, LPC, true, true><<<grid, kThreads, 0, s>>>(a, tiles);
-    else scan_fwd_kernel<T, LPC, true, false><<<grid, kThreads, 0, s>>>(a, tiles);
+    if (a.wide) scan_fwd_kernel<T, LPC, true, true><<<grid, kThreads, 0, s>>>(a, tiles, epoch);
+    else scan_fwd_kernel<T, LPC, true, false><<<grid, kThreads, 0, s>>>(a, tiles, epoch);
   } else {
-    if (a.wide) scan_fwd_kernel<T, LPC, false, true><<<grid, kThreads, 0, s>>>(a, tiles);
-    else scan_fwd_kernel<T, LPC, false, false><<<grid, kThreads, 0, s>>>(a, tiles);
+    if (a.wide) scan_fwd_kernel<T, LPC, false, true><<<grid, kThreads, 0, s>>>(a, tiles, epoch);
+    else scan_fwd_kernel<T, LPC, false, false><<<grid, kThreads, 0, s>>>(a, tiles, epoch);
   }
   return cudaGetLastError();
 }
@@ -435,22 +464,35 @@ cudaError_t by_type(const ScanArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-ScanSegments scan_segments(int B, int T, int D, int N) {
-  // Warps of an undivided scan, and how many tokens a segment keeps at least.
-  const long long warps = ((long long)B * D * scan_pad(N) + 255) / 256;
-  constexpr int want = 148 * 12, least = 4 * kTile;
-  long long segs = warps > 0 ? (want + warps - 1) / warps : 1;
-  if (segs > T / least) segs = T / least;
-  ScanSegments z;
-  if (segs <= 1) {
-    z.len = T;
-    z.count = 1;
-    return z;
+ScanSegments scan_cut(int T, long long ctas, int slots) {
+  constexpr int most = 256, least = 4 * kTile;  // tokens of a segment in turn / at once, at least
+  ScanSegments z = {T, 1, false, (int)ctas};
+  long long segs = 1;
+  if (ctas > slots) {
+    // In turn: about eight rounds of items, so that the last, partly empty one is an eighth.
+    segs = (8LL * slots + ctas - 1) / ctas;
+    if (segs > T / most) segs = T / most;
+    z.in_turn = segs > 1;
+  } else if (2 * ctas <= slots) {
+    // At once: as many segments as fill the GPU; the first pass over them adds about half of the
+    // scan's own work.
+    segs = slots / (ctas > 0 ? ctas : 1);
+    if (segs > T / least) segs = T / least;
   }
+  if (segs <= 1) return z;
   const long long tiles = (T + kTile - 1) / kTile;
   z.len = (int)((tiles + segs - 1) / segs) * kTile;
   z.count = (T + z.len - 1) / z.len;
   return z;
+}
+
+ScanSegments scan_fwd_segments(int B, int T, int D, int G, int N) {
+  const int CT = 2 * kThreads * 4 / scan_pad(N);
+  return scan_cut(T, (long long)B * G * ((D / G + CT - 1) / CT), kSlots);
+}
+
+cudaError_t fetch_scan_fwd_error(unsigned int* flag) {
+  return cudaMemcpyFromSymbol(flag, g_scan_fwd_error, sizeof(unsigned int));
 }
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s) { return by_type<kFwd>(a, s); }
