@@ -170,32 +170,62 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return as_f2(d);
 }
 
-// 1 / (1 + exp(-v)); 0 and 1 at the far ends, NaN for NaN.
-__device__ __forceinline__ float sigmoidf(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// The activation and its slope.  silu(v) = v sigmoid(v): 0 at -inf, where the product would be NaN.
+// 2^x, relative error about 2^-22, 0 far below zero; 1 / x, one ulp.  The .ftz forms: the others
+// spend instructions on results below 2^-126.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 exp2_pair(float2 v) {
+  return make_float2(exp2_fast(v.x), exp2_fast(v.y));
+}
+
+// 1 / (1 + exp(-v)); 0 and 1 at the far ends, NaN for NaN.
+__device__ __forceinline__ float2 sigmoid_pair(float2 v) {
+  const float2 e = add2(exp2_pair(mul2(v, make_float2(-kLog2e, -kLog2e))), make_float2(1.f, 1.f));
+  return make_float2(rcp_fast(e.x), rcp_fast(e.y));
+}
+
+// max(v, -100), NaN for NaN: silu is below 2^-126 from there on, and -inf would make it inf times 0.
+__device__ __forceinline__ float2 above_minus_100(float2 v) {
+  asm("max.NaN.f32 %0, %0, 0fC2C80000;" : "+f"(v.x));
+  asm("max.NaN.f32 %0, %0, 0fC2C80000;" : "+f"(v.y));
+  return v;
+}
+
+// The activation, and with its slope.
 template <int ACT>
-__device__ __forceinline__ float act_value(float v) {
+__device__ __forceinline__ float2 act_pair(float2 v) {
   if (ACT == kActNone) return v;
-  const float s = sigmoidf(v);
-  if (ACT == kActSigmoid) return s;
-  return s == 0.f ? 0.f : v * s;
+  if (ACT == kActSigmoid) return sigmoid_pair(v);
+  v = above_minus_100(v);
+  return mul2(v, sigmoid_pair(v));
 }
 template <int ACT>
-__device__ __forceinline__ void act_slope(float v, float* value, float* slope) {
+__device__ __forceinline__ void slope_pair(float2 v, float2* value, float2* slope) {
+  const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
   if (ACT == kActNone) {
     *value = v;
-    *slope = 1.f;
+    *slope = one;
     return;
   }
-  const float s = sigmoidf(v);
+  if (ACT == kActSilu) v = above_minus_100(v);
+  const float2 s = sigmoid_pair(v), rest = fma2(s, minus, one);
   if (ACT == kActSigmoid) {
     *value = s;
-    *slope = s * (1.f - s);
-    return;
+    *slope = mul2(s, rest);
+  } else {
+    *value = mul2(v, s);
+    *slope = fma2(*value, rest, s);
   }
-  *value = s == 0.f ? 0.f : v * s;
-  *slope = s == 0.f ? 0.f : fmaf(*value, 1.f - s, s);
 }
 
 }  // namespace mlstm

@@ -79,7 +79,7 @@ __device__ __forceinline__ void conv_token(const float2 (*w)[kPairs], const floa
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) s = fma2(w[j][p], win[j][p], s);
     s = fma2(w[W - 1][p], x[p], s);
-    o[p] = make_float2(act_value<ACT>(s.x), act_value<ACT>(s.y));
+    o[p] = act_pair<ACT>(s);
 #pragma unroll
     for (int j = 0; j + 2 < W; ++j) win[j][p] = win[j + 1][p];
     win[W - 2][p] = x[p];
@@ -89,7 +89,7 @@ __device__ __forceinline__ void conv_token(const float2 (*w)[kPairs], const floa
 constexpr int kAhead = 8;  // tokens whose loads a thread has in flight
 
 template <typename T, int W, int ACT, bool WIDE>
-__global__ void __launch_bounds__(128) conv_fwd_kernel(ConvArgs a, int run, int runs, int vecs) {
+__global__ void __launch_bounds__(128, 6) conv_fwd_kernel(ConvArgs a, int run, int runs, int vecs) {
   const long long item = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= (long long)vecs * runs * a.B) return;
   const int c0 = (int)(item % vecs) * kC;
@@ -176,8 +176,7 @@ struct BwdWalk {
       float2 s = bias[p], val, slope;
 #pragma unroll
       for (int j = 0; j < W; ++j) s = fma2(w[j][p], win[j][p], s);
-      act_slope<ACT>(s.x, &val.x, &slope.x);
-      act_slope<ACT>(s.y, &val.y, &slope.y);
+      slope_pair<ACT>(s, &val, &slope);
       dp[W - 1][p] = mul2(g[p], slope);
       if (own) {
         db[p] = add2(db[p], dp[W - 1][p]);

@@ -21,16 +21,29 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSMs = 148;
 
-__device__ __forceinline__ float act_run(int act, float v) {
-  return act == kActSilu ? act_value<kActSilu>(v) : act == kActSigmoid ? act_value<kActSigmoid>(v) : v;
+// The activation of eight channels.  The choice is made once for all eight: a choice for each
+// element cost more instructions than the norm itself.
+__device__ __forceinline__ void act8(int act, float2* v) {
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_pair<kActSilu>(v[i]);
+  } else if (act == kActSigmoid) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_pair<kActSigmoid>(v[i]);
+  }
 }
-__device__ __forceinline__ void slope_run(int act, float v, float* value, float* slope) {
-  if (act == kActSilu)
-    act_slope<kActSilu>(v, value, slope);
-  else if (act == kActSigmoid)
-    act_slope<kActSigmoid>(v, value, slope);
-  else
-    act_slope<kActNone>(v, value, slope);
+// v becomes the value.
+__device__ __forceinline__ void slope8(int act, float2* v, float2* slope) {
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) slope_pair<kActSilu>(v[i], &v[i], &slope[i]);
+  } else if (act == kActSigmoid) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) slope_pair<kActSigmoid>(v[i], &v[i], &slope[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) slope[i] = make_float2(1.f, 1.f);
+  }
 }
 
 template <int LANES>
@@ -42,17 +55,20 @@ __device__ __forceinline__ float lanes_sum(float x) {
 
 // Channels c .. c + n - 1 of the weight and bias (1 and 0 where there is none).
 template <bool WIDE>
-__device__ __forceinline__ void load_affine(const NormArgs& a, int c, int n, float* w, float* b) {
-  if (a.w != nullptr && n > 0)
-    load8<WIDE>(a.w + c, w, n);
-  else
+__device__ __forceinline__ void load_affine(const NormArgs& a, int c, int n, float2* w, float2* b) {
+  float f[8], g[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
-  if (a.bias != nullptr && n > 0)
-    load8<WIDE>(a.bias + c, b, n);
-  else
+  for (int i = 0; i < 8; ++i) {
+    f[i] = 1.f;
+    g[i] = 0.f;
+  }
+  if (a.w != nullptr && n > 0) load8<WIDE>(a.w + c, f, n);
+  if (a.bias != nullptr && n > 0) load8<WIDE>(a.bias + c, g, n);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    w[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    b[i] = make_float2(g[2 * i], g[2 * i + 1]);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -100,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) norm_token_fwd_kernel(NormArgs a, in
   const int head = blockIdx.x % a.NH, lane = threadIdx.x % LANES;
   const int tokens = a.B * a.T, d = a.d, step = blocks * ROWS;
   int c[K], n[K];
-  float w[K][8], bias[K][8];
+  float2 w[K][4], bias[K][4];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     c[k] = (k * LANES + lane) * 8;
@@ -152,16 +168,16 @@ __global__ void __launch_bounds__(kThreads) norm_token_fwd_kernel(NormArgs a, in
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (n[k] > 0) {
-        float2 g[4];
-        if (GATED) expand(now.r[GATED][k], g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float2 o = fma2(mul2(v[k][i], rs), make_float2(w[k][2 * i], w[k][2 * i + 1]),
-                          make_float2(bias[k][2 * i], bias[k][2 * i + 1]));
-          if (GATED)
-            v[k][i] = mul2(o, make_float2(act_run(a.act, g[i].x), act_run(a.act, g[i].y)));
-          else
-            v[k][i] = make_float2(act_run(a.act, o.x), act_run(a.act, o.y));
+        for (int i = 0; i < 4; ++i) v[k][i] = fma2(mul2(v[k][i], rs), w[k][i], bias[k][i]);
+        if (GATED) {
+          float2 g[4];
+          expand(now.r[GATED][k], g);
+          act8(a.act, g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[k][i] = mul2(v[k][i], g[i]);
+        } else {
+          act8(a.act, v[k]);
         }
         store_pairs<WIDE, 8>(y + c[k], v[k], n[k]);
       }
@@ -180,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_token_bwd_kerne
   const int head = blockIdx.x % a.NH, block = blockIdx.x / a.NH, lane = threadIdx.x % LANES;
   const int tokens = a.B * a.T, d = a.d, step = blocks * ROWS;
   int c[K], n[K];
-  float w[K][8], bias[K][8];
+  float2 w[K][4], bias[K][4];
   float2 dw[K][4], db[K][4];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -214,30 +230,29 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_token_bwd_kerne
     const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float2 g[4], dg[4];
+      float2 f[4], slope[4], nn[4], dg[4];  // f: the activation's argument, then its value
       expand(now.r[0][k], v[k]);
       expand(now.r[1][k], q[k]);
-      if (GATED) expand(now.r[1 + GATED][k], g);
+      if (GATED) expand(now.r[1 + GATED][k], f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 wi = make_float2(w[k][2 * i], w[k][2 * i + 1]);
-        const float2 xh = mul2(add2(v[k][i], neg), rs);
-        const float2 nn = fma2(xh, wi, make_float2(bias[k][2 * i], bias[k][2 * i + 1]));
-        const float2 of = GATED ? g[i] : nn;
-        float2 val, slope;
-        slope_run(a.act, of.x, &val.x, &slope.x);
-        slope_run(a.act, of.y, &val.y, &slope.y);
-        float2 dn = mul2(q[k][i], GATED ? val : slope);
-        if (GATED) dg[i] = mul2(mul2(q[k][i], nn), slope);
-        if (!live || 2 * i >= n[k]) dn.x = 0.f;  // nothing from rows or channels that do not exist
-        if (!live || 2 * i + 1 >= n[k]) dn.y = 0.f;
-        dw[k][i] = fma2(dn, xh, dw[k][i]);
+        v[k][i] = mul2(add2(v[k][i], neg), rs);
+        nn[i] = fma2(v[k][i], w[k][i], bias[k][i]);
+        if (!GATED) f[i] = nn[i];
+      }
+      slope8(a.act, f, slope);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 dn = mul2(q[k][i], GATED ? f[i] : slope[i]);
+        if (GATED) dg[i] = mul2(mul2(q[k][i], nn[i]), slope[i]);
+        // nothing from rows or channels that do not exist
+        if (!live || (WIDE ? n[k] <= 0 : 2 * i >= n[k])) dn.x = 0.f;
+        if (!live || (WIDE ? n[k] <= 0 : 2 * i + 1 >= n[k])) dn.y = 0.f;
+        dw[k][i] = fma2(dn, v[k][i], dw[k][i]);
         db[k][i] = add2(db[k][i], dn);
-        const float2 dxh = mul2(dn, wi);
-        s1 = add2(s1, dxh);
-        s2 = fma2(dxh, xh, s2);
-        v[k][i] = xh;
-        q[k][i] = dxh;
+        q[k][i] = mul2(dn, w[k][i]);
+        s1 = add2(s1, q[k][i]);
+        s2 = fma2(q[k][i], v[k][i], s2);
       }
       if (GATED && live && n[k] > 0)
         store_pairs<WIDE, 8>((T*)a.dgate.p + at.at(a.dgate, head) + c[k], dg, n[k]);
@@ -338,21 +353,39 @@ template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads) norm_stats_kernel(NormArgs a, Spread p) {
   const Cta q = cta_of(a, p);
   float cnt = 0.f, mean = 0.f, m2 = 0.f;
-  if (q.n > 0) {
+  if (q.n > 0 && q.t0 + q.row < q.t1) {
+    // A thread sums its distances from the mean of its first vector.  Were that vector far from the
+    // rest, its own distances would make m2 as large: m2 loses at most a factor of the thread's
+    // tokens in precision, whatever the values.
     const T* x = (const T*)a.x.p;
-    const float len = (float)q.n, inv = 1.f / len;
+    Raw<T, 8> r;
+    float2 v[4], s = make_float2(0.f, 0.f), e = s;
+    load_raw<WIDE>(x + at(a.x, q, q.t0 + q.row), r, q.n);
+    expand(r, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = add2(s, v[i]);
+    const float pivot = (s.x + s.y) / q.n;
+    const float2 neg = make_float2(-pivot, -pivot);
+    s = e;
+    int tokens = 0;
 #pragma unroll 4
     for (int t = q.t0 + q.row; t < q.t1; t += p.rows) {
-      float v[8], s = 0.f, e = 0.f;
-      load8<WIDE>(x + at(a.x, q, t), v, q.n);
+      load_raw<WIDE>(x + at(a.x, q, t), r, q.n);
+      expand(r, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[i];
-      s *= inv;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (WIDE || i < q.n) e = fmaf(v[i] - s, v[i] - s, e);
-      join(cnt, mean, m2, len, s, e);
+      for (int i = 0; i < 4; ++i) {
+        float2 d = add2(v[i], neg);
+        if (!WIDE && 2 * i >= q.n) d.x = 0.f;
+        if (!WIDE && 2 * i + 1 >= q.n) d.y = 0.f;
+        s = add2(s, d);
+        e = fma2(d, d, e);
+      }
+      ++tokens;
     }
+    cnt = (float)tokens * q.n;
+    const float off = (s.x + s.y) / cnt;
+    mean = pivot + off;
+    m2 = fmaxf((e.x + e.y) - off * (s.x + s.y), 0.f);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -403,44 +436,48 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs a, Spread
   __syncthreads();
   if (q.n == 0) return;
   const float mean = sh[0], rstd = sh[1];
-  float w[8], bias[8];
+  float2 w[4], bias[4];
   load_affine<WIDE>(a, q.head * a.d + q.c0, q.n, w, bias);
+  const float2 neg = make_float2(-mean, -mean), rs = make_float2(rstd, rstd);
   const T* x = (const T*)a.x.p;
 #pragma unroll 4
   for (int t = q.t0 + q.row; t < q.t1; t += p.rows) {
-    float v[8], g[8];
-    load8<WIDE>(x + at(a.x, q, t), v, q.n);
-    if (GATED) load8<WIDE>((const T*)a.gate.p + at(a.gate, q, t), g, q.n);
+    Raw<T, 8> xr, gr;
+    float2 v[4], g[4];
+    load_raw<WIDE>(x + at(a.x, q, t), xr, q.n);
+    if (GATED) load_raw<WIDE>((const T*)a.gate.p + at(a.gate, q, t), gr, q.n);
+    expand(xr, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = fmaf((v[i] - mean) * rstd, w[i], bias[i]);
-      if (GATED)
-        v[i] *= act_run(a.act, g[i]);
-      else
-        v[i] = act_run(a.act, v[i]);
+    for (int i = 0; i < 4; ++i) v[i] = fma2(mul2(add2(v[i], neg), rs), w[i], bias[i]);
+    if (GATED) {
+      expand(gr, g);
+      act8(a.act, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], g[i]);
+    } else {
+      act8(a.act, v);
     }
-    store8<WIDE>((T*)a.y.p + at(a.y, q, t), v, q.n);
+    store_pairs<WIDE, 8>((T*)a.y.p + at(a.y, q, t), v, q.n);
   }
 }
 
-// What one vector contributes to the backward: dxh = dn w into q, xhat into v, dgate into g.
-template <bool GATED, bool WIDE>
-__device__ __forceinline__ void dxhat8(const NormArgs& a, float mean, float rstd, const float* w,
-                                       const float* bias, float* v, float* q, float* g, float* dn) {
+// What one vector contributes to the backward: dn, xhat into v, dxh = dn w into q, dgate into f.
+template <bool GATED>
+__device__ __forceinline__ void dxhat8(int act, float2 neg, float2 rs, const float2* w, const float2* bias,
+                                       float2* v, float2* q, float2* f, float2* dn) {
+  float2 nn[4], slope[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float xh = (v[i] - mean) * rstd, nn = fmaf(xh, w[i], bias[i]);
-    float val, slope;
-    if (GATED) {
-      slope_run(a.act, g[i], &val, &slope);
-      g[i] = q[i] * nn * slope;
-      dn[i] = q[i] * val;
-    } else {
-      slope_run(a.act, nn, &val, &slope);
-      dn[i] = q[i] * slope;
-    }
-    v[i] = xh;
-    q[i] = dn[i] * w[i];
+  for (int i = 0; i < 4; ++i) {
+    v[i] = mul2(add2(v[i], neg), rs);
+    nn[i] = fma2(v[i], w[i], bias[i]);
+    if (!GATED) f[i] = nn[i];
+  }
+  slope8(act, f, slope);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    dn[i] = mul2(q[i], GATED ? f[i] : slope[i]);
+    if (GATED) f[i] = mul2(mul2(q[i], nn[i]), slope[i]);
+    q[i] = mul2(dn[i], w[i]);
   }
 }
 
@@ -451,44 +488,47 @@ __global__ void __launch_bounds__(kThreads) norm_dsums_kernel(NormArgs a, Spread
   extern __shared__ float cols[];  // [rows][2][lanes][8]
   const Cta q = cta_of(a, p);
   const long long group = (long long)q.b * a.NH + q.head;
-  float s1 = 0.f, s2 = 0.f, dw[8], db[8];
+  float2 s1 = make_float2(0.f, 0.f), s2 = s1, dw[4], db[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.f;
+  for (int i = 0; i < 4; ++i) dw[i] = db[i] = make_float2(0.f, 0.f);
   if (q.n > 0) {
     const float2 ms = reinterpret_cast<const float2*>(a.stats)[group];
-    float w[8], bias[8];
+    const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
+    float2 w[4], bias[4];
     load_affine<WIDE>(a, q.head * a.d + q.c0, q.n, w, bias);
 #pragma unroll 2
     for (int t = q.t0 + q.row; t < q.t1; t += p.rows) {
-      float v[8], r[8], g[8], dn[8];
-      load8<WIDE>((const T*)a.x.p + at(a.x, q, t), v, q.n);
-      load8<WIDE>((const T*)a.y.p + at(a.y, q, t), r, q.n);
-      if (GATED) load8<WIDE>((const T*)a.gate.p + at(a.gate, q, t), g, q.n);
-      dxhat8<GATED, WIDE>(a, ms.x, ms.y, w, bias, v, r, g, dn);
+      Raw<T, 8> xr, yr, gr;
+      float2 v[4], r[4], g[4], dn[4];
+      load_raw<WIDE>((const T*)a.x.p + at(a.x, q, t), xr, q.n);
+      load_raw<WIDE>((const T*)a.y.p + at(a.y, q, t), yr, q.n);
+      if (GATED) load_raw<WIDE>((const T*)a.gate.p + at(a.gate, q, t), gr, q.n);
+      expand(xr, v);
+      expand(yr, r);
+      if (GATED) expand(gr, g);
+      dxhat8<GATED>(a.act, neg, rs, w, bias, v, r, g, dn);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (WIDE || i < q.n) {
-          s1 += r[i];
-          s2 = fmaf(r[i], v[i], s2);
-          dw[i] = fmaf(dn[i], v[i], dw[i]);
-          db[i] += dn[i];
-        }
+      for (int i = 0; i < 4; ++i) {  // absent channels have dy = 0 and so add nothing
+        s1 = add2(s1, r[i]);
+        s2 = fma2(r[i], v[i], s2);
+        dw[i] = fma2(dn[i], v[i], dw[i]);
+        db[i] = add2(db[i], dn[i]);
+      }
     }
   }
   const int lane = threadIdx.x % p.lanes;
   if (param != nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      cols[((q.row * 2 + 0) * p.lanes + lane) * 8 + i] = dw[i];
-      cols[((q.row * 2 + 1) * p.lanes + lane) * 8 + i] = db[i];
+      cols[((q.row * 2 + 0) * p.lanes + lane) * 8 + i] = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+      cols[((q.row * 2 + 1) * p.lanes + lane) * 8 + i] = i & 1 ? db[i / 2].y : db[i / 2].x;
     }
   }
   __shared__ float red[kThreads / 32][2];
-  s1 = warp_sum(s1);
-  s2 = warp_sum(s2);
+  const float w1 = warp_sum(s1.x + s1.y), w2 = warp_sum(s2.x + s2.y);
   if ((threadIdx.x & 31) == 0) {
-    red[threadIdx.x / 32][0] = s1;
-    red[threadIdx.x / 32][1] = s2;
+    red[threadIdx.x / 32][0] = w1;
+    red[threadIdx.x / 32][1] = w2;
   }
   __syncthreads();
   if (threadIdx.x < 2) {
@@ -535,19 +575,25 @@ __global__ void __launch_bounds__(kThreads) norm_dx_kernel(NormArgs a, Spread p)
   if (q.n == 0) return;
   const float m1 = sh[0], m2 = sh[1];
   const float2 ms = reinterpret_cast<const float2*>(a.stats)[group];
-  float w[8], bias[8];
+  const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
+  const float2 n1 = make_float2(-m1, -m1), n2 = make_float2(-m2, -m2);
+  float2 w[4], bias[4];
   load_affine<WIDE>(a, q.head * a.d + q.c0, q.n, w, bias);
 #pragma unroll 2
   for (int t = q.t0 + q.row; t < q.t1; t += p.rows) {
-    float v[8], r[8], g[8], dn[8];
-    load8<WIDE>((const T*)a.x.p + at(a.x, q, t), v, q.n);
-    load8<WIDE>((const T*)a.y.p + at(a.y, q, t), r, q.n);
-    if (GATED) load8<WIDE>((const T*)a.gate.p + at(a.gate, q, t), g, q.n);
-    dxhat8<GATED, WIDE>(a, ms.x, ms.y, w, bias, v, r, g, dn);
+    Raw<T, 8> xr, yr, gr;
+    float2 v[4], r[4], g[4], dn[4];
+    load_raw<WIDE>((const T*)a.x.p + at(a.x, q, t), xr, q.n);
+    load_raw<WIDE>((const T*)a.y.p + at(a.y, q, t), yr, q.n);
+    if (GATED) load_raw<WIDE>((const T*)a.gate.p + at(a.gate, q, t), gr, q.n);
+    expand(xr, v);
+    expand(yr, r);
+    if (GATED) expand(gr, g);
+    dxhat8<GATED>(a.act, neg, rs, w, bias, v, r, g, dn);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = ms.y * (r[i] - m1 - v[i] * m2);
-    store8<WIDE>((T*)a.dx.p + at(a.dx, q, t), r, q.n);
-    if (GATED) store8<WIDE>((T*)a.dgate.p + at(a.dgate, q, t), g, q.n);
+    for (int i = 0; i < 4; ++i) r[i] = mul2(rs, fma2(v[i], n2, add2(r[i], n1)));
+    store_pairs<WIDE, 8>((T*)a.dx.p + at(a.dx, q, t), r, q.n);
+    if (GATED) store_pairs<WIDE, 8>((T*)a.dgate.p + at(a.dgate, q, t), g, q.n);
   }
 }
 

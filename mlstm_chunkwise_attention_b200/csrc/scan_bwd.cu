@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
           expand(*raw(3, item), z);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            g[i] = mul2(g[i], make_float2(act_value<kActSilu>(z[i].x), act_value<kActSilu>(z[i].y)));
+            g[i] = mul2(g[i], act_pair<kActSilu>(z[i]));
         }
         store_unit(sm + C::DY + item * kFloatUnit, g);
       }
@@ -322,8 +322,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float2 val, slope;
-            act_slope<kActSilu>(z[i].x, &val.x, &slope.x);
-            act_slope<kActSilu>(z[i].y, &val.y, &slope.y);
+            slope_pair<kActSilu>(z[i], &val, &slope);
             o[i] = mul2(mul2(g[i], fma2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), x[i], y[i])),
                         slope);
           }
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
           v[i] = fma2(v[i], make_float2(kLn2, kLn2), mul2(x[i], sgb[i]));
           if (a.softplus) {
             const float2 rw = add2(d[i], *reinterpret_cast<const float2*>(sm + C::BIAS + cv + 2 * i));
-            v[i] = mul2(v[i], make_float2(sigmoidf(rw.x), sigmoidf(rw.y)));
+            v[i] = mul2(v[i], sigmoid_pair(rw));
           }
           o[i] = fma2(make_float2(pair.x, pair.z), sgb[i],
                       mul2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), dy[i]));

@@ -12,15 +12,6 @@
 
 namespace mlstm {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// 2^x, relative error about 2^-22, 0 far below zero.
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1], of two values.  log(1 + e) / e is
 // a polynomial of degree 8, the best one in relative error on [0, 1] (found with Remez' exchange
 // algorithm in 50 digits): 1.4e-7 of the value with fp32 arithmetic, for small e as well.  Half
@@ -69,10 +60,6 @@ __device__ __forceinline__ void scatter_sum(float (&v)[M], int rank) {
       scatter_sum<1, L / 2, STRIDE>(v, rank);
     }
   }
-}
-
-__device__ __forceinline__ float2 exp2_pair(float2 v) {
-  return make_float2(exp2_fast(v.x), exp2_fast(v.y));
 }
 
 __device__ __forceinline__ void load_unit(const float* u, float2* v) {

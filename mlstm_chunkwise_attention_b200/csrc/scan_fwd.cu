@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         for (int i = 0; i < 4; ++i) {
           o[i] = fma2(*reinterpret_cast<const float2*>(sskip + cv + 2 * i), x[i], o[i]);
           if (GATE)
-            o[i] = mul2(o[i], make_float2(act_value<kActSilu>(z[i].x), act_value<kActSilu>(z[i].y)));
+            o[i] = mul2(o[i], act_pair<kActSilu>(z[i]));
         }
         store_pairs<WIDE, 8>(yp + t * a.y.st + cv, o, n);
       }
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_segment_kernel(ScanArgs 
             expand(zr, z);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              g[k] = mul2(g[k], make_float2(act_value<kActSilu>(z[k].x), act_value<kActSilu>(z[k].y)));
+              g[k] = mul2(g[k], act_pair<kActSilu>(z[k]));
           }
           stage_pairs<T>(a, g, now.dt[m], sbias + cv, t0 + t < last, n, sd + item * kPairUnit);
         }
@@ -395,7 +395,10 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
   for (int o = LPC / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
   if (live && nl == 0) {
     if (a.skip != nullptr) acc = fmaf(a.skip[c], x, acc);
-    if (a.z.p != nullptr) acc *= act_value<kActSilu>(to_f32(((const T*)a.z.p)[b * a.z.sb + c]));
+    if (a.z.p != nullptr) {
+      const float z = to_f32(((const T*)a.z.p)[b * a.z.sb + c]);
+      acc *= act_pair<kActSilu>(make_float2(z, z)).x;
+    }
     ((T*)a.y.p)[b * a.y.sb + c] = from_f32<T>(acc);
   }
 }
