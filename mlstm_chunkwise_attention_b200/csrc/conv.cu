@@ -86,10 +86,16 @@ __device__ __forceinline__ void conv_token(const float2 (*w)[kPairs], const floa
   }
 }
 
-constexpr int kAhead = 8;  // tokens whose loads a thread has in flight
+// Tokens a thread has on their way from memory, in its own slots of shared memory, and how many of
+// them it takes at a time.  Loads into registers left the memory idle while a batch was worked on
+// (4.0 TB/s at B8 T4096 D4096 bf16); what lies in shared memory does not cost registers.
+template <typename T> constexpr int kRing = sizeof(T) == 2 ? 16 : 8;
+constexpr int kBatch = 4;
 
 template <typename T, int W, int ACT, bool WIDE>
-__global__ void __launch_bounds__(128, 6) conv_fwd_kernel(ConvArgs a, int run, int runs, int vecs) {
+__global__ void __launch_bounds__(128, 7) conv_fwd_kernel(ConvArgs a, int run, int runs, int vecs) {
+  constexpr int RING = kRing<T>;
+  __shared__ Raw<T, kC> ring[RING][128];
   const long long item = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= (long long)vecs * runs * a.B) return;
   const int c0 = (int)(item % vecs) * kC;
@@ -100,29 +106,40 @@ __global__ void __launch_bounds__(128, 6) conv_fwd_kernel(ConvArgs a, int run, i
   const T* st = a.state_in ? (const T*)a.state_in + (long long)b * (W - 1) * D + c0 : nullptr;
   T* y = (T*)a.y.p + (long long)b * a.y.sb;
   const long long off = (c0 / a.d) * a.y.sh + c0 % a.d;
+  const int t1 = min(t0 + run, a.T);
+  const T* src = x + t0 * a.x.st;  // of the next token to fetch
+  int ahead = t0;
+  auto fetch = [&](int slot) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (ahead < t1) fetch_raw<WIDE>(&ring[slot + u][threadIdx.x], src, n);
+      src += a.x.st;
+      ++ahead;
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < RING; i += kBatch) fetch(i);
   float2 w[W][kPairs], bias[kPairs], win[W - 1][kPairs];
   load_taps<W, WIDE>(a, c0, n, w, bias);
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) load_input<T, W, WIDE>(a, x, st, t0 - (W - 1) + j, n, win[j]);
-  const int t1 = min(t0 + run, a.T);
-  int t = t0;
-  for (; t + kAhead <= t1; t += kAhead) {
-    Raw<T, kC> r[kAhead];
+  int slot = 0;
+  T* dst = y + t0 * a.y.st;
+  for (int tb = t0; tb < t1; tb += kBatch) {
+    copies_wait<RING / kBatch - 1>();
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load_raw<WIDE>(x + (t + u) * a.x.st, r[u], n);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      float2 v[kPairs], o[kPairs];
-      expand(r[u], v);
-      conv_token<W, ACT>(w, bias, win, v, o);
-      store_heads<T, WIDE>(y + (t + u) * a.y.st, off, a.y.sh, a.d, c0, n, o);
+    for (int u = 0; u < kBatch; ++u) {
+      if (tb + u < t1) {
+        float2 v[kPairs], o[kPairs];
+        expand(ring[slot + u][threadIdx.x], v);
+        conv_token<W, ACT>(w, bias, win, v, o);
+        store_heads<T, WIDE>(dst, off, a.y.sh, a.d, c0, n, o);
+      }
+      dst += a.y.st;
     }
-  }
-  for (; t < t1; ++t) {
-    float2 v[kPairs], o[kPairs];
-    load_input<T, W, WIDE>(a, x, st, t, n, v);
-    conv_token<W, ACT>(w, bias, win, v, o);
-    store_heads<T, WIDE>(y + t * a.y.st, off, a.y.sh, a.d, c0, n, o);
+    fetch(slot);
+    slot = slot + kBatch == RING ? 0 : slot + kBatch;
   }
   if (a.state_out != nullptr && t1 == a.T) {  // the window is the last W - 1 inputs
     T* so = (T*)a.state_out + (long long)b * (W - 1) * D + c0;
@@ -156,14 +173,13 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, int vecs) {
 constexpr int kBwdRun = 64;    // tokens of one thread's run
 constexpr int kBwdLanes = 32;  // channel vectors of a CTA
 constexpr int kBwdRuns = 4;    // runs of a CTA, joined in shared memory
-constexpr int kBwdAhead = 4;   // tokens whose x and dy a thread has in flight
 
 // One thread's walk through its run: windows of W inputs and W values of dp, sums for the taps.
 template <typename T, int W, int ACT, bool WIDE>
 struct BwdWalk {
   float2 w[W][kPairs], bias[kPairs], win[W][kPairs], dp[W][kPairs], dw[W][kPairs], db[kPairs];
 
-  // Takes token t in (x and dy; zero past the end of the sequence), `own`: its sums are this run's.
+  // Takes a token in (x and dy); `own`: its sums are this run's.
   __device__ __forceinline__ void take(const float2* x, const float2* g, bool own) {
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
@@ -185,6 +201,15 @@ struct BwdWalk {
       }
     }
   }
+  // A token behind the end: nothing comes from it.
+  __device__ __forceinline__ void skip() {
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+#pragma unroll
+      for (int j = 0; j + 1 < W; ++j) dp[j][p] = dp[j + 1][p];
+      dp[W - 1][p] = make_float2(0.f, 0.f);
+    }
+  }
   __device__ __forceinline__ void dx(float2* o) const {
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
@@ -203,8 +228,11 @@ struct BwdWalk {
 template <typename T, int W, int ACT, bool WIDE>
 __global__ void __launch_bounds__(kBwdLanes * kBwdRuns, 4) conv_bwd_kernel(ConvArgs a, int run, int runs,
                                                                           int vecs, int cblocks) {
-  __shared__ float red[kBwdRuns][W + 1][kC][kBwdLanes];
-  const int lane = threadIdx.x, rr = threadIdx.y;
+  constexpr int RING = kRing<T>;
+  __shared__ Raw<T, kC> ring[2][RING][kBwdLanes * kBwdRuns];  // x and dy on their way
+  static_assert(sizeof(ring) >= kBwdRuns * (W + 1) * kC * kBwdLanes * sizeof(float), "the sums reuse it");
+  float(*red)[W + 1][kC][kBwdLanes] = reinterpret_cast<float(*)[W + 1][kC][kBwdLanes]>(ring);
+  const int lane = threadIdx.x, rr = threadIdx.y, tid = rr * kBwdLanes + lane;
   const int vec = (int)(blockIdx.x % cblocks) * kBwdLanes + lane;
   const long long row = blockIdx.x / cblocks;          // partial row of this CTA
   const long long br = row * kBwdRuns + rr;            // run of all batches
@@ -226,26 +254,42 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns, 4) conv_bwd_kernel(ConvA
     const long long off = (c0 / a.d) * a.y.sh + c0 % a.d;
     T* dx = (T*)a.dx.p + (long long)b * a.dx.sb + c0;
     load_taps<W, WIDE>(a, c0, n, k.w, k.bias);
-    auto load_dy = [&](int t, Raw<T, kC>& r) {
-      if (WIDE) {
-        load_raw<true>(dy + t * a.y.st + off, r, n);
-      } else {
-        float2 v[kPairs];
+    const int end = min(t1 + W - 1, a.T);  // tokens read: dx of t1 - 1 is complete at t1 + W - 2
+    const T *sx = x + t0 * a.x.st, *sg = dy + t0 * a.y.st + off;
+    int ahead = t0;
+    auto fetch = [&](int slot) {
 #pragma unroll
-        for (int p = 0; p < kPairs; ++p) {
-          const int c = c0 + 2 * p;
-          v[p].x = 2 * p < n ? to_f32(dy[t * a.y.st + (c / a.d) * a.y.sh + c % a.d]) : 0.f;
-          v[p].y = 2 * p + 1 < n ? to_f32(dy[t * a.y.st + ((c + 1) / a.d) * a.y.sh + (c + 1) % a.d]) : 0.f;
+      for (int u = 0; u < kBatch; ++u) {
+        if (ahead < end) {
+          fetch_raw<WIDE>(&ring[0][slot + u][tid], sx, n);
+          if (WIDE) {
+            fetch_raw<true>(&ring[1][slot + u][tid], sg, n);
+          } else {  // the channels may lie in several heads
+            float2 v[kPairs];
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) {
+              const int c = c0 + 2 * p;
+              const T* row = sg - off;
+              v[p].x = 2 * p < n ? to_f32(row[(c / a.d) * a.y.sh + c % a.d]) : 0.f;
+              v[p].y = 2 * p + 1 < n ? to_f32(row[((c + 1) / a.d) * a.y.sh + (c + 1) % a.d]) : 0.f;
+            }
+            // exact: the values come from T
+            store_pairs<true, kC>(reinterpret_cast<T*>(&ring[1][slot + u][tid]), v, kC);
+          }
         }
-        store_pairs<true, kC>(reinterpret_cast<T*>(&r), v, kC);  // exact: the values come from T
+        sx += a.x.st;
+        sg += a.y.st;
+        ++ahead;
       }
+      copies_commit();
     };
+#pragma unroll
+    for (int i = 0; i < RING; i += kBatch) fetch(i);
     // win[j] = x_{tau - (W - 1) + j}; one step before tau = t0 it holds tokens t0 - W .. t0 - 1,
     // of which the first is shifted out unread
 #pragma unroll
     for (int j = 1; j < W; ++j) load_input<T, W, WIDE>(a, x, st, t0 - W + j, n, k.win[j]);
     const int emit0 = t0 == 0 ? -(W - 1) : t0;  // first token whose gradient this run writes
-    const int end = t1 + W - 1;                 // dx of t1 - 1 is complete at tau = t1 + W - 2
     auto emit = [&](int e) {                    // the token whose gradient is complete
       if (e < emit0) return;
       float2 o[kPairs];
@@ -264,41 +308,28 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns, 4) conv_bwd_kernel(ConvA
       else if (a.dstate_in != nullptr)
         store_pairs<WIDE, kC>((T*)a.dstate_in + ((long long)b * (W - 1) + e + W - 1) * D + c0, o, n);
     };
-    int t = t0;
-    for (; t + kBwdAhead <= t1; t += kBwdAhead) {
-      Raw<T, kC> rx[kBwdAhead], rg[kBwdAhead];
+    int slot = 0;
+    for (int tb = t0; tb < t1 + W - 1; tb += kBatch) {
+      copies_wait<RING / kBatch - 1>();
 #pragma unroll
-      for (int u = 0; u < kBwdAhead; ++u) {
-        load_raw<WIDE>(x + (t + u) * a.x.st, rx[u], n);
-        load_dy(t + u, rg[u]);
+      for (int u = 0; u < kBatch; ++u) {
+        const int t = tb + u;
+        if (t < end) {
+          float2 v[kPairs], g[kPairs];
+          expand(ring[0][slot + u][tid], v);
+          expand(ring[1][slot + u][tid], g);
+          k.take(v, g, t < t1);
+        } else {
+          k.skip();
+        }
+        if (t < t1 + W - 1) emit(t - (W - 1));
       }
-#pragma unroll
-      for (int u = 0; u < kBwdAhead; ++u) {
-        float2 v[kPairs], g[kPairs];
-        expand(rx[u], v);
-        expand(rg[u], g);
-        k.take(v, g, true);
-        emit(t + u - (W - 1));
-      }
+      fetch(slot);
+      slot = slot + kBatch == RING ? 0 : slot + kBatch;
     }
-    for (; t < end; ++t) {
-      float2 v[kPairs], g[kPairs];
-      Raw<T, kC> rx, rg;
-      zero_raw(rx);
-      zero_raw(rg);
-      if (t < a.T) {
-        load_raw<WIDE>(x + t * a.x.st, rx, n);
-        load_dy(t, rg);
-      }
-      expand(rx, v);
-      expand(rg, g);
-      k.take(v, g, t < t1);
-      if (t >= a.T)  // nothing comes from behind the end, whatever the recomputed slope is
-#pragma unroll
-        for (int p = 0; p < kPairs; ++p) k.dp[W - 1][p] = make_float2(0.f, 0.f);
-      emit(t - (W - 1));
-    }
+    copies_wait<0>();  // empty groups by now; the slots are reused below
   }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
     red[rr][W][i][lane] = i & 1 ? k.db[i / 2].y : k.db[i / 2].x;
@@ -307,7 +338,7 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns, 4) conv_bwd_kernel(ConvA
   }
   __syncthreads();
   // [W + 1][channels] sums of this CTA, channels contiguous
-  const int tid = rr * kBwdLanes + lane, cbase = (int)(blockIdx.x % cblocks) * kBwdLanes * kC;
+  const int cbase = (int)(blockIdx.x % cblocks) * kBwdLanes * kC;
   for (int e = tid; e < (W + 1) * kBwdLanes * kC; e += kBwdLanes * kBwdRuns) {
     const int q = e / (kBwdLanes * kC), c = e % (kBwdLanes * kC);
     float s = 0.f;

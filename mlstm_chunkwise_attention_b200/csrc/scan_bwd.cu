@@ -123,17 +123,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
           Raw<T, 8>* to = raw(k, item);
           const T* from = in[k] + t * stride[k] + cv;
           if (t < last && n > 0) {
-            if (WIDE) {
-#pragma unroll
-              for (int h = 0; h < (int)sizeof(Raw<T, 8>) / 16; ++h)
-                copy16_async((char*)to + 16 * h, (const char*)from + 16 * h);
-              // the same units of the next tile, into L2
-              if (t - kTile >= first) prefetch_l2(from - kTile * stride[k]);
-            } else {
-              Raw<T, 8> r;
-              load_raw<false>(from, r, n);
-              *to = r;
-            }
+            fetch_raw<WIDE>(to, from, n);
+            // the same units of the next tile, into L2
+            if (WIDE && t - kTile >= first) prefetch_l2(from - kTile * stride[k]);
           } else {
             zero_raw(*to);
           }
@@ -147,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (ch[e] < q.n)
-        copy16_async(sm + C::SAVED + (e * kThreads + tid) * 4,
+        copy_async(sm + C::SAVED + (e * kThreads + tid) * 4,
                      a.saved + (((long long)b * NC + t / kScanEvery) * a.D + q.c0 + ch[e]) * NP + nl * 4);
   };
 #pragma unroll

@@ -220,21 +220,9 @@ __device__ __forceinline__ void pass_turn(const ScanArgs& a, int tile) {
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.turn + 1 + tile) : "memory");
 }
 
-// A 16-byte copy into shared memory that completes in the background.
-__device__ __forceinline__ void copy16_async(void* smem, const void* gmem) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)),
-               "l"(gmem)
-               : "memory");
-}
 __device__ __forceinline__ void prefetch_l2(const void* gmem) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(gmem));
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copies_wait() {  // all but the newest LEFT groups are done
-  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
-
 // Channels of a CTA: tiles do not cross groups.
 struct ChannelTile {
   int g, c0, n;  // group, first channel, channels
