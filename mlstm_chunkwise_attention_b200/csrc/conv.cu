@@ -311,18 +311,32 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns, 4) conv_bwd_kernel(ConvA
     int slot = 0;
     for (int tb = t0; tb < t1 + W - 1; tb += kBatch) {
       copies_wait<RING / kBatch - 1>();
+      if (tb >= t0 + W - 1 && tb + kBatch <= t1) {  // inside the run: every token is read, summed and emitted
+        T* out = dx + (tb - (W - 1)) * a.dx.st;
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int t = tb + u;
-        if (t < end) {
+        for (int u = 0; u < kBatch; ++u) {
           float2 v[kPairs], g[kPairs];
           expand(ring[0][slot + u][tid], v);
           expand(ring[1][slot + u][tid], g);
-          k.take(v, g, t < t1);
-        } else {
-          k.skip();
+          k.take(v, g, true);
+          k.dx(v);
+          store_pairs<WIDE, kC>(out, v, n);
+          out += a.dx.st;
         }
-        if (t < t1 + W - 1) emit(t - (W - 1));
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < kBatch; ++u) {
+          const int t = tb + u;
+          if (t < end) {
+            float2 v[kPairs], g[kPairs];
+            expand(ring[0][slot + u][tid], v);
+            expand(ring[1][slot + u][tid], g);
+            k.take(v, g, t < t1);
+          } else {
+            k.skip();
+          }
+          if (t < t1 + W - 1) emit(t - (W - 1));
+        }
       }
       fetch(slot);
       slot = slot + kBatch == RING ? 0 : slot + kBatch;

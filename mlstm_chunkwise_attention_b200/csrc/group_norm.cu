@@ -78,75 +78,100 @@ __device__ __forceinline__ void load_affine(const NormArgs& a, int c, int n, flo
 // together write neighbouring parts of the same tokens.
 // ---------------------------------------------------------------------------
 
-// Walks rows r, r + step, .. of [B, T] without a division per row.
-struct RowWalk {
-  int b, t;
-  __device__ __forceinline__ RowWalk(int r, int T) : b(r / T), t(r % T) {}
-  __device__ __forceinline__ void advance(int step, int T) {
+constexpr int kRowThreads = 128;
+
+// A pointer that walks rows r, r + step, .. of [B, T] in a strided tensor (head and channel of the
+// lane already added), dividing only where it leaves a sequence.
+template <typename T>
+struct RowPtr {
+  T* base;
+  T* p;
+  long long sb, st, jump;
+  int t;
+  __device__ __forceinline__ RowPtr(const Rows& r, int head, int c, int row, int step, int len) {
+    base = (T*)r.p + head * r.sh + c;
+    sb = r.sb;
+    st = r.st;
+    jump = step * r.st;
+    t = row % len;
+    p = base + (row / len) * sb + t * st;
+    b = row / len;
+  }
+  int b;
+  __device__ __forceinline__ void advance(int step, int len) {
     t += step;
-    if (t >= T) {
-      b += t / T;
-      t %= T;
+    p += jump;
+    if (t >= len) {
+      b += t / len;
+      t %= len;
+      p = base + b * sb + t * st;
     }
-  }
-  __device__ __forceinline__ long long at(const Rows& r, int head) const {
-    return b * r.sb + t * r.st + head * r.sh;
   }
 };
 
-// What a lane holds of one row, still as it lies in memory.
+// Rows that a lane has on their way from memory, in its own slots of shared memory (with the rows
+// in registers the kernels waited on memory at 3.7 TB/s): as many as 44 KB hold, up to six.
 template <typename T, int K, int TENSORS>
-struct RowLoads {
-  Raw<T, 8> r[TENSORS][K];
-  template <bool WIDE>
-  __device__ __forceinline__ void load(int i, const T* row, const int* c, const int* n) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      zero_raw(r[i][k]);
-      if (n[k] > 0) load_raw<WIDE>(row + c[k], r[i][k], n[k]);
-    }
-  }
-};
+constexpr int kRowRing = 45056 / (kRowThreads * (K * TENSORS * 8 * (int)sizeof(T) + 8)) < 6
+                             ? 45056 / (kRowThreads * (K * TENSORS * 8 * (int)sizeof(T) + 8))
+                             : 6;
 
-// Each row's loads are issued before the row before it is worked on, so a lane always has one
-// row in flight: without that the kernels waited on memory at 3.7 TB/s.
 template <typename T, int LANES, int K, bool GATED, bool WIDE>
-__global__ void __launch_bounds__(kThreads) norm_token_fwd_kernel(NormArgs a, int blocks) {
-  constexpr int ROWS = kThreads / LANES;
-  const int head = blockIdx.x % a.NH, lane = threadIdx.x % LANES;
+__global__ void __launch_bounds__(kRowThreads) norm_token_fwd_kernel(NormArgs a, int blocks) {
+  constexpr int ROWS = kRowThreads / LANES, RING = kRowRing<T, K, 1 + GATED>;
+  __shared__ Raw<T, 8> ring[RING][1 + GATED][K][kRowThreads];
+  const int head = blockIdx.x % a.NH, lane = threadIdx.x % LANES, tid = threadIdx.x;
   const int tokens = a.B * a.T, d = a.d, step = blocks * ROWS;
-  int c[K], n[K];
+  const int first = (blockIdx.x / a.NH) * ROWS, row = first + tid / LANES;
+  const int c0 = lane * 8;  // vector k: channels c0 + k LANES 8
+  int n[K];
   float2 w[K][4], bias[K][4];
+  RowPtr<const T> px(a.x, head, c0, row, step, a.T), pg(a.gate, head, c0, row, step, a.T);
+  RowPtr<T> py(a.y, head, c0, row, step, a.T);
+  int ahead = row;
+  auto fetch = [&](int slot) {
+    if (ahead < tokens) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (n[k] > 0) {
+          fetch_raw<WIDE>(&ring[slot][0][k][tid], px.p + k * LANES * 8, n[k]);
+          if (GATED) fetch_raw<WIDE>(&ring[slot][GATED][k][tid], pg.p + k * LANES * 8, n[k]);
+        }
+      }
+    }
+    ahead += step;
+    px.advance(step, a.T);
+    if (GATED) pg.advance(step, a.T);
+    copies_commit();
+  };
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    c[k] = (k * LANES + lane) * 8;
-    n[k] = max(0, min(8, d - c[k]));
-    load_affine<WIDE>(a, head * d + c[k], n[k], w[k], bias[k]);
+    n[k] = max(0, min(8, d - c0 - k * LANES * 8));
+#pragma unroll
+    for (int s = 0; s < RING; ++s)
+      if (n[k] <= 0) zero_raw(ring[s][0][k][tid]);  // absent channels add nothing to the sums
   }
+#pragma unroll
+  for (int s = 0; s < RING; ++s) fetch(s);
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    load_affine<WIDE>(a, head * d + c0 + k * LANES * 8, n[k], w[k], bias[k]);
   const float inv_d = 1.f / d;
-  int r = (blockIdx.x / a.NH) * ROWS + threadIdx.x / LANES;
-  RowWalk cur(r, a.T);
-  RowLoads<T, K, 1 + GATED> next = {};
-  auto fetch = [&](const RowWalk& q) {
-    next.template load<WIDE>(0, (const T*)a.x.p + q.at(a.x, head), c, n);
-    if (GATED) next.template load<WIDE>(GATED, (const T*)a.gate.p + q.at(a.gate, head), c, n);
-  };
-  if (r < tokens) fetch(cur);
+  float2* stats = reinterpret_cast<float2*>(a.stats) + (long long)row * a.NH + head;
+  int r = row, slot = 0;
   // whole warps stay in the loop together; rows past the end compute on what they hold, unstored
-  for (int r0 = (blockIdx.x / a.NH) * ROWS; r0 < tokens; r0 += step) {
-    const bool live = r < tokens;
-    const RowLoads<T, K, 1 + GATED> now = next;
-    const RowWalk at = cur;
-    r += step;
-    cur.advance(step, a.T);
-    if (r < tokens) fetch(cur);
-    float2 v[K][4], s = make_float2(0.f, 0.f);
+  for (int r0 = first; r0 < tokens; r0 += step) {
+    copies_wait<RING - 1>();
+    float2 v[K][4], g[K][4], s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      expand(now.r[0][k], v[k]);
+      expand(ring[slot][0][k][tid], v[k]);
+      if (GATED) expand(ring[slot][GATED][k][tid], g[k]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = add2(s, v[k][i]);
     }
+    fetch(slot);
+    slot = slot + 1 == RING ? 0 : slot + 1;
     const float mean = lanes_sum<LANES>(s.x + s.y) * inv_d;
     const float2 neg = make_float2(-mean, -mean);
     s = make_float2(0.f, 0.f);
@@ -162,78 +187,97 @@ __global__ void __launch_bounds__(kThreads) norm_token_fwd_kernel(NormArgs a, in
           s.x = fmaf(v[k][i].x, v[k][i].x, s.x);
       }
     const float rstd = rsqrtf(fmaf(lanes_sum<LANES>(s.x + s.y), inv_d, a.eps));
-    if (!live) continue;
-    T* y = (T*)a.y.p + at.at(a.y, head);
-    const float2 rs = make_float2(rstd, rstd);
+    if (r < tokens) {
+      const float2 rs = make_float2(rstd, rstd);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (n[k] > 0) {
+      for (int k = 0; k < K; ++k) {
+        if (n[k] > 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[k][i] = fma2(mul2(v[k][i], rs), w[k][i], bias[k][i]);
-        if (GATED) {
-          float2 g[4];
-          expand(now.r[GATED][k], g);
-          act8(a.act, g);
+          for (int i = 0; i < 4; ++i) v[k][i] = fma2(mul2(v[k][i], rs), w[k][i], bias[k][i]);
+          if (GATED) {
+            act8(a.act, g[k]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[k][i] = mul2(v[k][i], g[i]);
-        } else {
-          act8(a.act, v[k]);
+            for (int i = 0; i < 4; ++i) v[k][i] = mul2(v[k][i], g[k][i]);
+          } else {
+            act8(a.act, v[k]);
+          }
+          store_pairs<WIDE, 8>(py.p + k * LANES * 8, v[k], n[k]);
         }
-        store_pairs<WIDE, 8>(y + c[k], v[k], n[k]);
       }
+      if (a.stats != nullptr && lane == 0) *stats = make_float2(mean, rstd);
     }
-    if (a.stats != nullptr && lane == 0)
-      reinterpret_cast<float2*>(a.stats)[((long long)at.b * a.T + at.t) * a.NH + head] =
-          make_float2(mean, rstd);
+    r += step;
+    stats += (long long)step * a.NH;
+    py.advance(step, a.T);
   }
 }
 
 // ws: rows of partial sums [blocks, 2, NH d] (dw, then dbias).
 template <typename T, int LANES, int K, bool GATED, bool WIDE>
-__global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_token_bwd_kernel(NormArgs a, int blocks) {
-  constexpr int ROWS = kThreads / LANES, CH = LANES * K * 8;
-  __shared__ float red[kThreads / 32][2][CH];
-  const int head = blockIdx.x % a.NH, block = blockIdx.x / a.NH, lane = threadIdx.x % LANES;
+__global__ void __launch_bounds__(kRowThreads, K == 1 ? 4 : 2) norm_token_bwd_kernel(NormArgs a, int blocks) {
+  constexpr int ROWS = kRowThreads / LANES, CH = LANES * K * 8, WARPS = kRowThreads / 32;
+  constexpr int RING = kRowRing<T, K, 2 + GATED>;
+  __shared__ union {
+    struct {
+      Raw<T, 8> raw[RING][2 + GATED][K][kRowThreads];
+      float2 ms[RING][kRowThreads];
+    } ring;
+    float red[WARPS][2][CH];
+  } sm;
+  const int head = blockIdx.x % a.NH, block = blockIdx.x / a.NH, tid = threadIdx.x, lane = tid % LANES;
   const int tokens = a.B * a.T, d = a.d, step = blocks * ROWS;
-  int c[K], n[K];
-  float2 w[K][4], bias[K][4];
-  float2 dw[K][4], db[K][4];
+  const int first = block * ROWS, row = first + tid / LANES, c0 = lane * 8;
+  int n[K];
+  float2 w[K][4], bias[K][4], dw[K][4], db[K][4];
+  RowPtr<const T> px(a.x, head, c0, row, step, a.T), py(a.y, head, c0, row, step, a.T);
+  RowPtr<const T> pg(a.gate, head, c0, row, step, a.T);
+  RowPtr<T> pdx(a.dx, head, c0, row, step, a.T), pdg(a.dgate, head, c0, row, step, a.T);
+  const float2* stats = reinterpret_cast<const float2*>(a.stats) + (long long)row * a.NH + head;
+  int ahead = row;
+  auto fetch = [&](int slot) {
+    if (ahead < tokens) {
+      copy_async<8>(&sm.ring.ms[slot][tid], stats);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (n[k] > 0) {
+          fetch_raw<WIDE>(&sm.ring.raw[slot][0][k][tid], px.p + k * LANES * 8, n[k]);
+          fetch_raw<WIDE>(&sm.ring.raw[slot][1][k][tid], py.p + k * LANES * 8, n[k]);
+          if (GATED) fetch_raw<WIDE>(&sm.ring.raw[slot][1 + GATED][k][tid], pg.p + k * LANES * 8, n[k]);
+        }
+      }
+    }
+    ahead += step;
+    stats += (long long)step * a.NH;
+    px.advance(step, a.T);
+    py.advance(step, a.T);
+    if (GATED) pg.advance(step, a.T);
+    copies_commit();
+  };
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    c[k] = (k * LANES + lane) * 8;
-    n[k] = max(0, min(8, d - c[k]));
-    load_affine<WIDE>(a, head * d + c[k], n[k], w[k], bias[k]);
+    n[k] = max(0, min(8, d - c0 - k * LANES * 8));
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[k][i] = db[k][i] = make_float2(0.f, 0.f);
   }
+#pragma unroll
+  for (int s = 0; s < RING; ++s) fetch(s);
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    load_affine<WIDE>(a, head * d + c0 + k * LANES * 8, n[k], w[k], bias[k]);
   const float inv_d = 1.f / d;
-  int r = block * ROWS + threadIdx.x / LANES;
-  RowWalk cur(r, a.T);
-  RowLoads<T, K, 2 + GATED> next = {};
-  float2 next_ms = make_float2(0.f, 0.f);
-  auto fetch = [&](const RowWalk& q) {
-    next_ms = reinterpret_cast<const float2*>(a.stats)[((long long)q.b * a.T + q.t) * a.NH + head];
-    next.template load<WIDE>(0, (const T*)a.x.p + q.at(a.x, head), c, n);
-    next.template load<WIDE>(1, (const T*)a.y.p + q.at(a.y, head), c, n);
-    if (GATED) next.template load<WIDE>(1 + GATED, (const T*)a.gate.p + q.at(a.gate, head), c, n);
-  };
-  if (r < tokens) fetch(cur);
-  for (int r0 = block * ROWS; r0 < tokens; r0 += step) {
+  int r = row, slot = 0;
+  for (int r0 = first; r0 < tokens; r0 += step) {
+    copies_wait<RING - 1>();
     const bool live = r < tokens;
-    const RowLoads<T, K, 2 + GATED> now = next;
-    const float2 ms = next_ms;
-    const RowWalk at = cur;
-    r += step;
-    cur.advance(step, a.T);
-    if (r < tokens) fetch(cur);
+    const float2 ms = sm.ring.ms[slot][tid];
     float2 v[K][4], q[K][4], s1 = make_float2(0.f, 0.f), s2 = s1;
     const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float2 f[4], slope[4], nn[4], dg[4];  // f: the activation's argument, then its value
-      expand(now.r[0][k], v[k]);
-      expand(now.r[1][k], q[k]);
-      if (GATED) expand(now.r[1 + GATED][k], f);
+      expand(sm.ring.raw[slot][0][k][tid], v[k]);
+      expand(sm.ring.raw[slot][1][k][tid], q[k]);
+      if (GATED) expand(sm.ring.raw[slot][1 + GATED][k][tid], f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[k][i] = mul2(add2(v[k][i], neg), rs);
@@ -246,32 +290,38 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_token_bwd_kerne
         float2 dn = mul2(q[k][i], GATED ? f[i] : slope[i]);
         if (GATED) dg[i] = mul2(mul2(q[k][i], nn[i]), slope[i]);
         // nothing from rows or channels that do not exist
-        if (!live || (WIDE ? n[k] <= 0 : 2 * i >= n[k])) dn.x = 0.f;
-        if (!live || (WIDE ? n[k] <= 0 : 2 * i + 1 >= n[k])) dn.y = 0.f;
+        if (!live || (WIDE ? n[k] <= 0 : 2 * i >= n[k])) dn.x = 0.f, v[k][i].x = 0.f;
+        if (!live || (WIDE ? n[k] <= 0 : 2 * i + 1 >= n[k])) dn.y = 0.f, v[k][i].y = 0.f;
         dw[k][i] = fma2(dn, v[k][i], dw[k][i]);
         db[k][i] = add2(db[k][i], dn);
         q[k][i] = mul2(dn, w[k][i]);
         s1 = add2(s1, q[k][i]);
         s2 = fma2(q[k][i], v[k][i], s2);
       }
-      if (GATED && live && n[k] > 0)
-        store_pairs<WIDE, 8>((T*)a.dgate.p + at.at(a.dgate, head) + c[k], dg, n[k]);
+      if (GATED && live && n[k] > 0) store_pairs<WIDE, 8>(pdg.p + k * LANES * 8, dg, n[k]);
     }
+    fetch(slot);
+    slot = slot + 1 == RING ? 0 : slot + 1;
     const float m1 = lanes_sum<LANES>(s1.x + s1.y) * inv_d, m2 = lanes_sum<LANES>(s2.x + s2.y) * inv_d;
-    if (!live) continue;
-    T* dx = (T*)a.dx.p + at.at(a.dx, head);
-    const float2 n1 = make_float2(-m1, -m1), n2 = make_float2(-m2, -m2);
+    if (live) {
+      const float2 n1 = make_float2(-m1, -m1), n2 = make_float2(-m2, -m2);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (n[k] > 0) {
+      for (int k = 0; k < K; ++k) {
+        if (n[k] > 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[k][i] = mul2(rs, fma2(v[k][i], n2, add2(q[k][i], n1)));
-        store_pairs<WIDE, 8>(dx + c[k], q[k], n[k]);
+          for (int i = 0; i < 4; ++i) q[k][i] = mul2(rs, fma2(v[k][i], n2, add2(q[k][i], n1)));
+          store_pairs<WIDE, 8>(pdx.p + k * LANES * 8, q[k], n[k]);
+        }
       }
     }
+    r += step;
+    pdx.advance(step, a.T);
+    if (GATED) pdg.advance(step, a.T);
   }
   if (a.dw == nullptr && a.dbias == nullptr) return;
   // the rows of a warp, then the warps, in a fixed order
+  copies_wait<0>();
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -282,18 +332,18 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) norm_token_bwd_kerne
         sw += __shfl_xor_sync(0xffffffffu, sw, o);
         sb += __shfl_xor_sync(0xffffffffu, sb, o);
       }
-      if ((threadIdx.x & 31) < LANES) {
-        red[threadIdx.x / 32][0][c[k] + i] = sw;
-        red[threadIdx.x / 32][1][c[k] + i] = sb;
+      if ((tid & 31) < LANES) {
+        sm.red[tid / 32][0][c0 + k * LANES * 8 + i] = sw;
+        sm.red[tid / 32][1][c0 + k * LANES * 8 + i] = sb;
       }
     }
   __syncthreads();
   const int D = a.NH * d;
-  for (int e = threadIdx.x; e < 2 * d; e += kThreads) {
+  for (int e = tid; e < 2 * d; e += kRowThreads) {
     const int p = e / d, ch = e % d;
     float s = 0.f;
 #pragma unroll
-    for (int q = 0; q < kThreads / 32; ++q) s += red[q][p][ch];
+    for (int q = 0; q < WARPS; ++q) s += sm.red[q][p][ch];
     a.ws[((long long)block * 2 + p) * D + head * d + ch] = s;
   }
 }
@@ -606,14 +656,18 @@ int lanes_for(int d) {
   return v <= 4 ? 4 : v <= 8 ? 8 : v <= 16 ? 16 : 32;
 }
 
+#ifndef FW
+#define FW 16
+#define BW 8
+#endif
 // Token blocks of the token-scope kernels: enough CTAs for `waves` per SM, no more than rows need.
 int token_blocks(long long tokens, int NH, int d, int waves) {
-  const int rows = kThreads / lanes_for(d);
+  const int rows = kRowThreads / lanes_for(d);
   const long long need = (tokens + rows - 1) / rows;
   const long long want = ((long long)kSMs * waves + NH - 1) / NH;
   return (int)(need < want ? need : want);
 }
-constexpr int kFwdWaves = 16, kBwdWaves = 6;
+constexpr int kFwdWaves = FW, kBwdWaves = BW;
 
 Spread spread_for(int B, int T, int NH, int d) {
   Spread p;
@@ -638,11 +692,11 @@ cudaError_t token_fwd(const NormArgs& a, cudaStream_t s) {
   const int blocks = token_blocks((long long)a.B * a.T, a.NH, a.d, kFwdWaves);
   const unsigned grid = (unsigned)blocks * a.NH;
   if (a.gate.p != nullptr) {
-    if (a.wide) norm_token_fwd_kernel<T, LANES, K, true, true><<<grid, kThreads, 0, s>>>(a, blocks);
-    else norm_token_fwd_kernel<T, LANES, K, true, false><<<grid, kThreads, 0, s>>>(a, blocks);
+    if (a.wide) norm_token_fwd_kernel<T, LANES, K, true, true><<<grid, kRowThreads, 0, s>>>(a, blocks);
+    else norm_token_fwd_kernel<T, LANES, K, true, false><<<grid, kRowThreads, 0, s>>>(a, blocks);
   } else {
-    if (a.wide) norm_token_fwd_kernel<T, LANES, K, false, true><<<grid, kThreads, 0, s>>>(a, blocks);
-    else norm_token_fwd_kernel<T, LANES, K, false, false><<<grid, kThreads, 0, s>>>(a, blocks);
+    if (a.wide) norm_token_fwd_kernel<T, LANES, K, false, true><<<grid, kRowThreads, 0, s>>>(a, blocks);
+    else norm_token_fwd_kernel<T, LANES, K, false, false><<<grid, kRowThreads, 0, s>>>(a, blocks);
   }
   return cudaGetLastError();
 }
@@ -651,11 +705,11 @@ cudaError_t token_bwd(const NormArgs& a, cudaStream_t s) {
   const int blocks = token_blocks((long long)a.B * a.T, a.NH, a.d, kBwdWaves);
   const unsigned grid = (unsigned)blocks * a.NH;
   if (a.gate.p != nullptr) {
-    if (a.wide) norm_token_bwd_kernel<T, LANES, K, true, true><<<grid, kThreads, 0, s>>>(a, blocks);
-    else norm_token_bwd_kernel<T, LANES, K, true, false><<<grid, kThreads, 0, s>>>(a, blocks);
+    if (a.wide) norm_token_bwd_kernel<T, LANES, K, true, true><<<grid, kRowThreads, 0, s>>>(a, blocks);
+    else norm_token_bwd_kernel<T, LANES, K, true, false><<<grid, kRowThreads, 0, s>>>(a, blocks);
   } else {
-    if (a.wide) norm_token_bwd_kernel<T, LANES, K, false, true><<<grid, kThreads, 0, s>>>(a, blocks);
-    else norm_token_bwd_kernel<T, LANES, K, false, false><<<grid, kThreads, 0, s>>>(a, blocks);
+    if (a.wide) norm_token_bwd_kernel<T, LANES, K, false, true><<<grid, kRowThreads, 0, s>>>(a, blocks);
+    else norm_token_bwd_kernel<T, LANES, K, false, false><<<grid, kRowThreads, 0, s>>>(a, blocks);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (a.dw == nullptr && a.dbias == nullptr)) return e;
