@@ -118,7 +118,8 @@ __device__ __forceinline__ void expand(const Raw<float, C>& r, float2* v) {
 #pragma unroll
   for (int i = 0; i < C / 2; ++i) v[i] = w[i];
 }
-template <bool WIDE, int C>
+// STREAM: what is stored will not be read soon, and makes room in L2 first.
+template <bool WIDE, int C, bool STREAM = false>
 __device__ __forceinline__ void store_pairs(bf16* p, const float2* v, int n) {
   if (WIDE) {
     uint32_t w[C / 2];
@@ -129,19 +130,27 @@ __device__ __forceinline__ void store_pairs(bf16* p, const float2* v, int n) {
     }
     Raw<bf16, C> r;
     r.u = *reinterpret_cast<decltype(r.u)*>(w);
-    *reinterpret_cast<decltype(r.u)*>(p) = r.u;
+    if (STREAM)
+      __stcs(reinterpret_cast<decltype(r.u)*>(p), r.u);
+    else
+      *reinterpret_cast<decltype(r.u)*>(p) = r.u;
   } else {
 #pragma unroll
     for (int i = 0; i < C; ++i)
       if (i < n) p[i] = from_f32<bf16>(i & 1 ? v[i / 2].y : v[i / 2].x);
   }
 }
-template <bool WIDE, int C>
+template <bool WIDE, int C, bool STREAM = false>
 __device__ __forceinline__ void store_pairs(float* p, const float2* v, int n) {
   if (WIDE) {
 #pragma unroll
-    for (int i = 0; i < C / 4; ++i)
-      reinterpret_cast<float4*>(p)[i] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+    for (int i = 0; i < C / 4; ++i) {
+      const float4 r = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+      if (STREAM)
+        __stcs(reinterpret_cast<float4*>(p) + i, r);
+      else
+        reinterpret_cast<float4*>(p)[i] = r;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < C; ++i)

@@ -758,7 +758,7 @@ namespace {
 // mlstm_device_status saw last.  A flag holds the epoch of the last launch of
 // its family that gave up, so a value that differs from the last one seen is a
 // failure not yet reported.
-constexpr int kFlagDevices = 64, kFlagFamilies = 9;
+constexpr int kFlagDevices = 64, kFlagFamilies = 10;
 std::mutex g_flag_mu;
 unsigned int g_flag_seen[kFlagDevices][kFlagFamilies] = {};
 }  // namespace
@@ -778,7 +778,7 @@ int mlstm_device_status(void* stream) {
                                       mlstm::fetch_tc_state_error,  mlstm::fetch_tc_fwd_xl_error,
                                       mlstm::fetch_tc_walk_error,   mlstm::fetch_tc_fwalk_error,
                                       mlstm::fetch_tc_bwd_xl_error, mlstm::fetch_scan_fwd_error,
-                                      mlstm::fetch_scan_bwd_error};
+                                      mlstm::fetch_scan_bwd_error, mlstm::fetch_norm_error};
   unsigned int flag[kFlagFamilies] = {};
   for (int i = 0; i < kFlagFamilies; ++i) {
     st = cuda_status(fetch[i](&flag[i]), "device error flag");
