@@ -15,6 +15,8 @@ tensors' device, or on ``stream``: outputs and workspaces are then allocated for
 
 import struct
 
+import torch
+
 from .binding import (
     BF16, FP32, STATUS_OK, STATUS_UNSUPPORTED, MLSTMError, Rows, ScanGrads, ScanProblem, load)
 
@@ -30,7 +32,6 @@ SCOPE_SEQUENCE = 1
 # --------------------------------------------------------------------------
 
 def _dtype_code(t):
-    import torch
     if t.dtype == torch.bfloat16:
         return BF16
     if t.dtype == torch.float32:
@@ -38,39 +39,33 @@ def _dtype_code(t):
     raise TypeError(f"unsupported dtype {t.dtype}: use bfloat16 or float32")
 
 
+# The checks run on every call, of which a small one takes 15 us: each asks the tensor for as
+# little as it can (get_device() is -1 off the GPU) and leaves the wording to _refuse.
+
 def _activation(name, t, shape, like):
     """An activation of `like`'s dtype and device, last dimension contiguous, of this shape."""
-    if (t.shape == shape and t.dtype == like.dtype and t.get_device() == like.get_device() and t.is_cuda
-            and (t.stride(-1) == 1 or shape[-1] <= 1)):
-        return
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous in its last dimension")
+    if not (t.shape == shape and t.dtype == like.dtype and t.get_device() == like.get_device()
+            and (t.is_contiguous() or t.stride(-1) == 1 or shape[-1] <= 1) and t.is_cuda):
+        _refuse(name, t, shape, like, like.dtype, "contiguous in its last dimension")
 
 
 def _fp32(name, t, shape, like):
     """A contiguous float32 parameter or state (None passes)."""
-    import torch
-    if t is None:
-        return
-    if (t.shape == shape and t.dtype == torch.float32 and t.get_device() == like.get_device()
-            and t.is_cuda and t.is_contiguous()):
-        return
+    if t is not None and not (t.shape == shape and t.dtype == torch.float32 and t.is_contiguous()
+                              and t.get_device() == like.get_device()):
+        _refuse(name, t, shape, like, torch.float32, "contiguous")
+
+
+def _refuse(name, t, shape, like, dtype, layout):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected float32")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {str(dtype).removeprefix('torch.')}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be {layout}")
 
 
 def _contiguous(name, t, shape, like):
@@ -94,7 +89,8 @@ def _rows(t):
     """[B, T, D] (or [B, D], one token) as mlstm_rows_t."""
     if t is None:
         return Rows(None, 0, 0, 0)
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0, 0)
+    st = t.stride()
+    return Rows(t.data_ptr(), st[0], st[1] if len(st) == 3 else 0, 0)
 
 
 def _head_rows(t, layout, d):
@@ -108,7 +104,6 @@ def _head_rows(t, layout, d):
 def _on(stream, like, tensors, launch):
     """launch(stream handle), with `like`'s device current.  With an explicit stream, what launch
     allocates belongs to that stream, and the inputs are kept from reuse until its work is done."""
-    import torch
     device = like.get_device()
     if stream is None and device == torch.cuda.current_device():
         # the handle of torch.cuda.current_stream() without building a Stream (3 us of a 15 us call)
@@ -131,7 +126,6 @@ def _check(status, where):
 
 
 def _bytes(n, like):
-    import torch
     return like.new_empty(max(n, 16), dtype=torch.uint8)
 
 
@@ -246,38 +240,37 @@ _SCAN_PROBLEM = struct.Struct("@20q4q7i4x")
 
 def _scan_problem(x, dt, A, Bm, Cm, skip, z, dt_bias, softplus, state):
     """mlstm_scan_t of a call on [B, T, D] tensors (or [B, D]: one token)."""
-    _activation("x", x, x.shape, x)
-    D = x.shape[-1]
-    _activation("dt", dt, x.shape, x)
+    shape = x.shape
+    _activation("x", x, shape, x)
+    D = shape[-1]
+    _activation("dt", dt, shape, x)
     if z is not None:
-        _activation("z", z, x.shape, x)
+        _activation("z", z, shape, x)
     _dims("A", A, 2)
     N = A.shape[1]
     _fp32("A", A, (D, N), x)
     _fp32("skip", skip, (D,), x)
     _fp32("dt_bias", dt_bias, (D,), x)
-    lead = tuple(x.shape[:-1])
-    if Bm.dim() == x.dim() + 1:
-        G = Bm.shape[-2]
-        shape = (*lead, G, N)
-    else:
-        G = 1
-        shape = (*lead, N)
+    G = Bm.shape[-2] if Bm.dim() > len(shape) else 1
+    shape = (*shape[:-1], G, N) if Bm.dim() > len(shape) else (*shape[:-1], N)
     _activation("B", Bm, shape, x)
     _activation("C", Cm, shape, x)
     if G <= 0 or D % G:
         raise ValueError(f"{G} groups do not divide {D} channels")
     _fp32("state", state, (x.shape[0], D, N), x)
-    token = x.dim() == 3
-    st = x.stride(1) if token else 0
-    bst, cst = (Bm.stride(1), Cm.stride(1)) if token else (0, 0)
-    bsh, csh = (Bm.stride(-2), Cm.stride(-2)) if Bm.dim() == x.dim() + 1 else (0, 0)
-    zp, zsb, zst = (0, 0, 0) if z is None else (z.data_ptr(), z.stride(0), z.stride(1) if token else 0)
+    xs, ds, bs, cs = x.stride(), dt.stride(), Bm.stride(), Cm.stride()
+    zp, zs = (0, xs) if z is None else (z.data_ptr(), z.stride())
+    if len(xs) == 3:
+        T, xt, dtt, zt, bt, ct = x.shape[1], xs[1], ds[1], zs[1], bs[1], cs[1]
+    else:
+        T, xt, dtt, zt, bt, ct = 1, 0, 0, 0, 0, 0
+    bg, cg = (bs[-2], cs[-2]) if len(bs) > len(xs) else (0, 0)
     return ScanProblem.from_buffer_copy(_SCAN_PROBLEM.pack(
-        x.data_ptr(), x.stride(0), st, 0, dt.data_ptr(), dt.stride(0), dt.stride(1) if token else 0, 0,
-        zp, zsb, zst, 0, Bm.data_ptr(), Bm.stride(0), bst, bsh, Cm.data_ptr(), Cm.stride(0), cst, csh,
-        A.data_ptr(), _ptr(skip) or 0, _ptr(dt_bias) or 0, _ptr(state) or 0,
-        x.shape[0], x.shape[1] if token else 1, D, G, N, 1 if softplus else 0, _dtype_code(x)))
+        x.data_ptr(), xs[0], xt, 0, dt.data_ptr(), ds[0], dtt, 0, zp, zs[0], zt, 0,
+        Bm.data_ptr(), bs[0], bt, bg, Cm.data_ptr(), cs[0], ct, cg, A.data_ptr(),
+        0 if skip is None else skip.data_ptr(), 0 if dt_bias is None else dt_bias.data_ptr(),
+        0 if state is None else state.data_ptr(), x.shape[0], T, D, G, N, 1 if softplus else 0,
+        _dtype_code(x)))
 
 
 def selective_scan_forward(x, dt, A, B, C, *, skip=None, z=None, dt_bias=None, softplus=True,
@@ -290,7 +283,6 @@ def selective_scan_forward(x, dt, A, B, C, *, skip=None, z=None, dt_bias=None, s
     ``saved`` is what the backward needs (None unless keep_saved); state_out [B, D, N] is None
     unless want_state.
     """
-    import torch
     _dims("x", x, 3)
     p = _scan_problem(x, dt, A, B, C, skip, z, dt_bias, softplus, state_in)
 
@@ -403,7 +395,6 @@ def group_norm_forward(x, weight=None, bias=None, *, gate=None, act=ACT_NONE, sc
     (SCOPE_SEQUENCE).  Returns (y [B, T, NH d], stats): stats are what the backward needs (None
     unless keep_stats).
     """
-    import torch
     layout, B, T, NH, d, dt = _norm_args(x, weight, bias, gate, act, scope, groups)
 
     def launch(s):

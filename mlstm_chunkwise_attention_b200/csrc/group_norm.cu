@@ -366,8 +366,8 @@ cudaError_t norm_pass(const NormArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t norm_workspace(int B, int T, int NH, int d, int scope, int, bool backward) {
-  if (scope == 1) return norm_sequence_workspace(B, T, NH, d, backward);
+size_t norm_workspace(int B, int T, int NH, int d, int scope, int dtype, bool backward) {
+  if (scope == 1) return norm_sequence_workspace(B, T, NH, d, dtype, backward);
   return backward ? (size_t)token_blocks((long long)B * T, NH, d, kBwdWaves) * 2 * NH * d * 4 : 0;
 }
 

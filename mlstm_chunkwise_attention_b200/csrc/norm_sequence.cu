@@ -41,7 +41,12 @@ struct Layout {
   size_t zeroed, pair, part, param, total;  // bytes; the counters lie at 0
 };
 
-Plan plan_for(int B, int T, int NH, int d, bool backward) {
+// Tokens of an item that a thread takes, all of them on their way from memory at once: as many as 64 KB
+// of shared memory hold.
+constexpr int tokens_of(int n) { return n >= 16 ? 16 : n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1; }
+constexpr int each_of(int elem, int tensors) { return tokens_of(65536 / (kThreads * tensors * 8 * elem)); }
+
+Plan plan_for(int B, int T, int NH, int d, int elem, bool gated, bool backward) {
   const int slots = slots_of(backward);
   Plan p;
   const int v = (d + 7) / 8;
@@ -50,9 +55,8 @@ Plan plan_for(int B, int T, int NH, int d, bool backward) {
   p.rows = kThreads / p.lanes;
   p.cblocks = (v + p.lanes - 1) / p.lanes;
   p.groups = B * NH;
-  // Eight tokens to a thread (32 KB of a bf16 tensor to an item), fewer where that leaves too few
-  // items to fill the GPU.
-  int each = 8;
+  // As many tokens to a thread as its slots hold, fewer where that leaves too few items to fill the GPU.
+  int each = each_of(elem, 1 + backward + gated);
   while (each > 1 && (long long)p.groups * p.cblocks * ((T + p.rows * each - 1) / (p.rows * each)) < slots)
     each /= 2;
   p.slab = p.rows * each;
@@ -126,324 +130,373 @@ struct Item {
   }
 };
 
-// Tokens that a thread has on their way from memory: as many as 64 KB hold, up to the eight of an item.
-template <typename T, int TENSORS>
-constexpr int kRing = 65536 / (kThreads * TENSORS * 8 * (int)sizeof(T)) < 8
-                          ? 65536 / (kThreads * TENSORS * 8 * (int)sizeof(T))
-                          : 8;
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
+// Eight warps work on an item.  Meanwhile a ninth joins the sums of the item before it, and a tenth, the
+// manager, takes and works out the item after the next one and looks whether the next one's sums are
+// ready: each of these waits on memory about as long as the work on an item takes.  One barrier ends an
+// item.
 template <typename T, bool GATED, bool WIDE, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) norm_sequence_kernel(NormArgs a, Plan p, Work w,
-                                                                            unsigned int epoch) {
-  constexpr int TENSORS = 1 + BWD + GATED, RING = kRing<T, TENSORS>;
+__global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
+    norm_sequence_kernel(NormArgs a, Plan p, Work w, unsigned int epoch) {
+  constexpr int TENSORS = 1 + BWD + GATED, EACH = each_of((int)sizeof(T), TENSORS), ALL = kThreads + 64;
   extern __shared__ __align__(16) unsigned char dynamic[];
   // x, then dy, then the gate on their way; and in the backward the channels' sums [rows][2][lanes][8]
-  auto ring = reinterpret_cast<Raw<T, 8>(*)[TENSORS][kThreads]>(dynamic);
-  float* cols = reinterpret_cast<float*>(dynamic + sizeof(Raw<T, 8>) * RING * TENSORS * kThreads);
-  __shared__ float red[kThreads / 32][3];
-  __shared__ float2 result;
-  __shared__ Item items[3];  // the one worked on, the one after it, and room for the next
-  __shared__ int waited;
-  const tc::Abort abort{&g_norm_error, epoch};
-  const int tid = threadIdx.x, warp = tid / 32, row = tid / p.lanes, lane = tid % p.lanes;
-  // -- fetching: one commit group to a token, and RING of them ahead --------------------------
-  const T* src[3];
-  const long long step[3] = {p.rows * a.x.st, p.rows * a.y.st, p.rows * a.gate.st};
-  int ahead = 0, end = 0, width = 0, slot = 0;
-  bool with_gate = false;
-  auto fetch = [&](int to) {
-    if (ahead < end && width > 0) {
-      fetch_raw<WIDE>(&ring[to][0][tid], src[0], width);
-      if (BWD) fetch_raw<WIDE>(&ring[to][BWD][tid], src[1], width);
-      if (with_gate) fetch_raw<WIDE>(&ring[to][TENSORS - 1][tid], src[2], width);
+  auto slots = reinterpret_cast<Raw<T, 8>(*)[TENSORS][kThreads]>(dynamic);
+  float* cols = reinterpret_cast<float*>(dynamic + sizeof(Raw<T, 8>) * EACH * TENSORS * kThreads);
+  __shared__ float red[2][kThreads / 32][3];
+  __shared__ float2 result[2];
+  __shared__ int ready[2];  // whether result is the item's, as seen a barrier before
+  __shared__ int waited;    // how the wait of an item that was not ready ended
+  __shared__ Item items[4];
+  const int tid = threadIdx.x, warp = tid / 32;
+
+  if (warp == kThreads / 32) {  // ---- the warp that joins sums --------------------------------
+    const int lane = tid & 31;
+    // Joins an item's sums, and those of its group if it is the last to finish.
+    auto finish = [&](const Item& q, const float (*r)[3]) {
+      float s[3] = {0.f, 0.f, 0.f};
+      if (lane < kThreads / 32)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) s[k] = r[lane][k];
+#pragma unroll
+      for (int o = kThreads / 64; o > 0; o >>= 1) {
+        const float v0 = __shfl_down_sync(0xffffffffu, s[0], o), v1 = __shfl_down_sync(0xffffffffu, s[1], o),
+                    v2 = __shfl_down_sync(0xffffffffu, s[2], o);
+        if (BWD) {
+          s[0] += v0;
+          s[1] += v1;
+        } else {
+          join(s[0], s[1], s[2], v0, v1, v2);
+        }
+      }
+      float* all = w.part + (long long)q.group * p.parts() * 3;
+      unsigned int before = 0;
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) __stcg(all + q.part * 3 + k, s[k]);
+        __threadfence();
+        before = atomicAdd(w.done + q.group, 1u);
+      }
+      before = __shfl_sync(0xffffffffu, before, 0);
+      if (before != (unsigned int)p.parts() - 1) return;
+      __threadfence();
+      double s0 = 0, s1 = 0, s2 = 0;
+      for (int i = lane; i < p.parts(); i += 32) {
+        const double v0 = __ldcg(all + 3 * i), v1 = __ldcg(all + 3 * i + 1), v2 = __ldcg(all + 3 * i + 2);
+        if (BWD) {
+          s0 += v0;
+          s1 += v1;
+        } else {
+          join(s0, s1, s2, v0, v1, v2);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const double v0 = __shfl_down_sync(0xffffffffu, s0, o), v1 = __shfl_down_sync(0xffffffffu, s1, o),
+                     v2 = __shfl_down_sync(0xffffffffu, s2, o);
+        if (BWD) {
+          s0 += v0;
+          s1 += v1;
+        } else {
+          join(s0, s1, s2, v0, v1, v2);
+        }
+      }
+      if (lane == 0) {
+        float2 r;
+        if (BWD) {
+          const double inv = 1.0 / ((double)a.T * a.d);
+          r = make_float2((float)(s0 * inv), (float)(s1 * inv));
+        } else {
+          r = make_float2((float)s1, (float)(1.0 / sqrt(s2 / s0 + (double)a.eps)));
+          if (a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[q.group] = r;
+        }
+        __stcg(w.pair + q.group, r);
+        __threadfence();
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(w.ready + q.group) : "memory");
+      }
+    };
+    named_barrier(0, ALL);
+    for (int i = 0;; ++i) {
+      if (i > 0) {
+        const Item& last = items[(i - 1) & 3];
+        if (last.output == 0 && last.group >= 0) finish(last, red[(i - 1) & 1]);
+      }
+      const Item& q = items[i & 3];
+      if (q.output < 0) return;
+      if (q.output && q.group >= 0 && ready[i & 1] == 0) {
+        named_barrier(1, ALL);
+        if (waited == 0) return;
+      }
+      named_barrier(0, ALL);
     }
-    ahead += p.rows;
-    src[0] += step[0];
-    if (BWD) src[1] += step[1];
-    if (GATED) src[2] += step[2];
-    copies_commit();
-  };
-  auto begin = [&](const Item& i) {  // the first tokens of an item, into the slots from `slot` on
-    if (i.output < 0) return;
-    ahead = i.t0 + row;
-    end = i.group >= 0 ? i.t1 : 0;
-    width = max(0, min(8, a.d - i.c0 - lane * 8));
-    with_gate = GATED && (BWD || i.output);
-    src[0] = i.template at<const T>(a.x, row, lane);
-    if (BWD) src[1] = i.template at<const T>(a.y, row, lane);
-    if (GATED) src[2] = i.template at<const T>(a.gate, row, lane);
-    for (int k = 0, to = slot; k < RING; ++k, to = to + 1 == RING ? 0 : to + 1) fetch(to);
-  };
-  auto advance = [&]() {
-    fetch(slot);
-    slot = slot + 1 == RING ? 0 : slot + 1;
-  };
-  // Each CTA holds the item it works on and the one after it, whose first tokens it fetches early.  That
-  // one may wait behind the first; but the earliest unfinished item of the queue never does, so it can
-  // go on.
-  if (tid == 0) {
-    items[0].set(a, p, atomicAdd(w.next, 1u));
-    items[1].set(a, p, atomicAdd(w.next, 1u));
   }
-  __syncthreads();
-  begin(items[0]);
-  for (int at = 0;; at = at == 2 ? 0 : at + 1) {
-    const Item& q = items[at];
-    const Item& behind = items[at == 2 ? 0 : at + 1];
-    if (q.output < 0) return;
-    unsigned int after = 0;
-    if (tid == 0) after = atomicAdd(w.next, 1u);
-    const bool real = q.group >= 0;
-    if (real) {
-      const int n = max(0, min(8, a.d - q.c0 - lane * 8)), first = q.t0 + row;
-      if (q.output) {
-        if (tid == 0) {
-          bool ok = true;
+  if (warp > kThreads / 32) {  // ---- the manager ---------------------------------------------
+    const int lane = tid & 31;
+    const tc::Abort abort{&g_norm_error, epoch};
+    auto look = [&](const Item& q) {
+      unsigned int v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(w.ready + q.group) : "memory");
+      return v != 0;
+    };
+    if (lane == 0) {
+      items[0].set(a, p, atomicAdd(w.next, 1u));
+      items[1].set(a, p, atomicAdd(w.next, 1u));
+      ready[0] = 0;
+    }
+    __syncwarp();
+    named_barrier(0, ALL);
+    // A CTA holds items behind the one it works on, which may wait; but the earliest unfinished item of
+    // the queue is never among them, so it can go on.
+    for (int i = 0;; ++i) {
+      const Item& q = items[i & 3];
+      if (q.output < 0) return;
+      if (q.output && q.group >= 0 && ready[i & 1] == 0) {
+        if (lane == 0) {
+          int ok = 1;
           const uint64_t began = tc::global_timer_ns();
-          for (unsigned int i = 1;; ++i) {
-            unsigned int v;
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(w.ready + q.group) : "memory");
-            if (v != 0) break;
-            if ((i & 63) == 0 && (abort.raised() || tc::global_timer_ns() - began > tc::kWaitTimeoutNs)) {
+          for (unsigned int n = 1; !look(q); ++n) {
+            if ((n & 63) == 0 && (abort.raised() || tc::global_timer_ns() - began > tc::kWaitTimeoutNs)) {
               abort.raise();
-              ok = false;
+              ok = 0;
               break;
             }
             __nanosleep(100);
           }
+          result[i & 1] = __ldcg(w.pair + q.group);
           waited = ok;
-          result = __ldcg(w.pair + q.group);
         }
-        __syncthreads();
-        if (!waited) {
-          copies_wait<0>();
-          return;
-        }
+        __syncwarp();
+        named_barrier(1, ALL);
+        if (waited == 0) return;
       }
+      if (lane == 0) {
+        items[(i + 2) & 3].set(a, p, atomicAdd(w.next, 1u));
+        const Item& next = items[(i + 1) & 3];
+        int ok = 0;
+        if (next.output > 0 && next.group >= 0 && look(next)) {
+          result[(i + 1) & 1] = __ldcg(w.pair + next.group);
+          ok = 1;
+        }
+        ready[(i + 1) & 1] = ok;
+      }
+      __syncwarp();
+      named_barrier(0, ALL);
+    }
+  }
+
+  // ---- the eight warps ---------------------------------------------------------------------
+  const int row = tid / p.lanes, lane = tid % p.lanes;
+  // All tokens of an item, a commit group each.
+  auto begin = [&](const Item& q) {
+    if (q.output < 0) return;
+    const int n = min(8, a.d - q.c0 - lane * 8), end = q.group >= 0 && n > 0 ? q.t1 : 0;
+    const T* x = q.template at<const T>(a.x, row, lane);
+    const T* dy = BWD ? q.template at<const T>(a.y, row, lane) : nullptr;
+    const T* gate = GATED ? q.template at<const T>(a.gate, row, lane) : nullptr;
+    const long long sx = p.rows * a.x.st, sy = p.rows * a.y.st, sg = p.rows * a.gate.st;
+    int t = q.t0 + row;
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+      if (t < end) {
+        fetch_raw<WIDE>(&slots[u][0][tid], x, n);
+        if (BWD) fetch_raw<WIDE>(&slots[u][BWD][tid], dy, n);
+        if (GATED && (BWD || q.output)) fetch_raw<WIDE>(&slots[u][TENSORS - 1][tid], gate, n);
+      }
+      copies_commit();
+      t += p.rows;
+      x += sx;
+      if (BWD) dy += sy;
+      if (GATED) gate += sg;
+    }
+  };
+  named_barrier(0, ALL);
+  begin(items[0]);
+  for (int i = 0;; ++i) {
+    const Item& q = items[i & 3];
+    const Item& behind = items[(i + 1) & 3];
+    if (q.output < 0) return;
+    if (q.group < 0) {
+      begin(behind);
+      named_barrier(0, ALL);
+      continue;
+    }
+    if (q.output && ready[i & 1] == 0) {
+      named_barrier(1, ALL);
+      if (waited == 0) {
+        copies_wait<0>();
+        return;
+      }
+    }
+    const int n = max(0, min(8, a.d - q.c0 - lane * 8));
+    const int end = n > 0 ? q.t1 : 0;  // threads without channels have no tokens
+    int t = q.t0 + row;
+    if (!BWD && !q.output) {
+      // -- forward, first reading: a warp sums its distances from the mean of one of its vectors.  Were
+      // that vector far from the rest, its own distances would make m2 as large: m2 loses at most a
+      // factor of the warp's vectors in precision, whatever the values.
+      const unsigned int valid = __ballot_sync(0xffffffffu, t < end);
+      float2 neg = make_float2(0.f, 0.f), s = neg, e = neg;
+      int tokens = 0;
+#pragma unroll
+      for (int u = 0; u < EACH; ++u) {
+        copies_wait<EACH - 1>();
+        copies_commit();  // keeps EACH groups behind this token's, so that the count above is right
+        float2 v[4];
+        if (t < end) expand(slots[u][0][tid], v);
+        if (u == 0) {
+          float m = 0.f;
+          if (t < end) {
+            const float2 q4 = add2(add2(v[0], v[1]), add2(v[2], v[3]));
+            m = -(q4.x + q4.y) / n;
+          }
+          m = __shfl_sync(0xffffffffu, m, valid != 0 ? __ffs(valid) - 1 : 0);
+          neg = make_float2(m, m);
+        }
+        if (t < end) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float2 d = add2(v[k], neg);
+            if (!WIDE && 2 * k >= n) d.x = 0.f;
+            if (!WIDE && 2 * k + 1 >= n) d.y = 0.f;
+            s = add2(s, d);
+            e = fma2(d, d, e);
+          }
+          ++tokens;
+        }
+        t += p.rows;
+      }
+      copies_wait<0>();
+      begin(behind);
+      const float cnt = (float)__reduce_add_sync(0xffffffffu, tokens * n);
+      const float sum = warp_sum(s.x + s.y), sq = warp_sum(e.x + e.y);
+      if ((tid & 31) == 0) {
+        const float off = cnt > 0.f ? sum / cnt : 0.f;
+        red[i & 1][warp][0] = cnt;
+        red[i & 1][warp][1] = off - neg.x;
+        red[i & 1][warp][2] = fmaxf(sq - off * sum, 0.f);
+      }
+    } else if (!BWD) {
+      // -- forward, second reading
+      const float2 r = result[i & 1];
+      const float2 neg = make_float2(-r.x, -r.x), rs = make_float2(r.y, r.y);
       float2 wt[4], bias[4];
       load_affine<WIDE>(a, q.head * a.d + q.c0 + lane * 8, n, wt, bias);
-      if constexpr (!BWD) {
-        if (!q.output) {
-          // -- forward, first reading: a thread sums its distances from the mean of its first
-          // vector.  Were that vector far from the rest, its own distances would make m2 as large:
-          // m2 loses at most a factor of the thread's tokens in precision, whatever the values.
-          float cnt = 0.f, mean = 0.f, m2 = 0.f;
-          if (n > 0 && first < q.t1) {
-            float2 neg = make_float2(0.f, 0.f), s = neg, e = neg;
-            int tokens = 0;
-            for (int t = first; t < q.t1; t += p.rows) {
-              copies_wait<RING - 1>();
-              float2 v[4];
-              expand(ring[slot][0][tid], v);
-              if (tokens == 0) {
-                float2 m = add2(add2(v[0], v[1]), add2(v[2], v[3]));
-                m.x = -(m.x + m.y) / n;
-                neg = make_float2(m.x, m.x);
-              }
+      T* y = q.template at<T>(a.y, row, lane);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float2 d = add2(v[i], neg);
-                if (!WIDE && 2 * i >= n) d.x = 0.f;
-                if (!WIDE && 2 * i + 1 >= n) d.y = 0.f;
-                s = add2(s, d);
-                e = fma2(d, d, e);
-              }
-              ++tokens;
-              advance();
-            }
-            cnt = (float)tokens * n;
-            const float off = (s.x + s.y) / cnt;
-            mean = off - neg.x;
-            m2 = fmaxf((e.x + e.y) - off * (s.x + s.y), 0.f);
-          }
-          begin(behind);
+      for (int u = 0; u < EACH; ++u) {
+        copies_wait<EACH - 1>();
+        copies_commit();
+        if (t < end) {
+          float2 v[4], g[4];
+          expand(slots[u][0][tid], v);
+          if (GATED) expand(slots[u][TENSORS - 1][tid], g);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            const float nb = __shfl_down_sync(0xffffffffu, cnt, o), mb = __shfl_down_sync(0xffffffffu, mean, o),
-                        sb = __shfl_down_sync(0xffffffffu, m2, o);
-            join(cnt, mean, m2, nb, mb, sb);
-          }
-          if ((tid & 31) == 0) {
-            red[warp][0] = cnt;
-            red[warp][1] = mean;
-            red[warp][2] = m2;
-          }
-        } else {
-          // -- forward, second reading
-          const float2 neg = make_float2(-result.x, -result.x), rs = make_float2(result.y, result.y);
-          T* dst = q.template at<T>(a.y, row, lane);
-          for (int t = first; t < q.t1 && n > 0; t += p.rows) {
-            copies_wait<RING - 1>();
-            float2 v[4], g[4];
-            expand(ring[slot][0][tid], v);
-            if (GATED) expand(ring[slot][TENSORS - 1][tid], g);
-            advance();
+          for (int k = 0; k < 4; ++k) v[k] = fma2(mul2(add2(v[k], neg), rs), wt[k], bias[k]);
+          if (GATED) {
+            act8(a.act, g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = fma2(mul2(add2(v[i], neg), rs), wt[i], bias[i]);
-            if (GATED) {
-              act8(a.act, g);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], g[i]);
-            } else {
-              act8(a.act, v);
-            }
-            store_pairs<WIDE, 8, true>(dst, v, n);
-            dst += p.rows * a.y.st;
+            for (int k = 0; k < 4; ++k) v[k] = mul2(v[k], g[k]);
+          } else {
+            act8(a.act, v);
           }
-          begin(behind);
+          store_pairs<WIDE, 8, true>(y, v, n);
         }
-      } else {
-        const float2 ms = reinterpret_cast<const float2*>(a.stats)[q.group];
-        const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
-        const float2 n1 = make_float2(-result.x, -result.x), n2 = make_float2(-result.y, -result.y);
-        float2 s1 = make_float2(0.f, 0.f), s2 = s1, dw[4], db[4];
+        t += p.rows;
+        y += p.rows * a.y.st;
+      }
+      begin(behind);
+    } else {
+      const float2 ms = reinterpret_cast<const float2*>(a.stats)[q.group], r = result[i & 1];
+      const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
+      const float2 n1 = make_float2(-r.x, -r.x), n2 = make_float2(-r.y, -r.y);
+      float2 wt[4], bias[4], s1 = make_float2(0.f, 0.f), s2 = s1, dw[4], db[4];
+      load_affine<WIDE>(a, q.head * a.d + q.c0 + lane * 8, n, wt, bias);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dw[i] = db[i] = make_float2(0.f, 0.f);
-        T* ddx = q.template at<T>(a.dx, row, lane);
-        T* ddg = GATED ? q.template at<T>(a.dgate, row, lane) : nullptr;
-        for (int t = first; t < q.t1 && n > 0; t += p.rows) {
-          copies_wait<RING - 1>();
-          float2 v[4], r[4], f[4], slope[4], nn[4];  // f: the activation's argument, then its value
-          expand(ring[slot][0][tid], v);
-          expand(ring[slot][BWD][tid], r);
-          if (GATED) expand(ring[slot][TENSORS - 1][tid], f);
-          advance();
+      for (int k = 0; k < 4; ++k) dw[k] = db[k] = make_float2(0.f, 0.f);
+      T* dx = q.template at<T>(a.dx, row, lane);
+      T* dgate = GATED ? q.template at<T>(a.dgate, row, lane) : nullptr;
+#pragma unroll 2
+      for (int u = 0; u < EACH; ++u) {
+        copies_wait<EACH - 1>();
+        copies_commit();
+        if (t < end) {
+          float2 v[4], g[4], f[4], slope[4], nn[4];  // f: the activation's argument, then its value
+          expand(slots[u][0][tid], v);
+          expand(slots[u][BWD][tid], g);
+          if (GATED) expand(slots[u][TENSORS - 1][tid], f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] = mul2(add2(v[i], neg), rs);
-            nn[i] = fma2(v[i], wt[i], bias[i]);
-            if (!GATED) f[i] = nn[i];
+          for (int k = 0; k < 4; ++k) {
+            v[k] = mul2(add2(v[k], neg), rs);
+            nn[k] = fma2(v[k], wt[k], bias[k]);
+            if (!GATED) f[k] = nn[k];
           }
           slope8(a.act, f, slope);
           if (!q.output) {
             // -- backward, first reading.  Absent channels have dy = 0 and so add nothing.
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 dn = mul2(r[i], GATED ? f[i] : slope[i]), g = mul2(dn, wt[i]);
-              s1 = add2(s1, g);
-              s2 = fma2(g, v[i], s2);
-              dw[i] = fma2(dn, v[i], dw[i]);
-              db[i] = add2(db[i], dn);
+            for (int k = 0; k < 4; ++k) {
+              const float2 dn = mul2(g[k], GATED ? f[k] : slope[k]), h = mul2(dn, wt[k]);
+              s1 = add2(s1, h);
+              s2 = fma2(h, v[k], s2);
+              dw[k] = fma2(dn, v[k], dw[k]);
+              db[k] = add2(db[k], dn);
             }
           } else {
             // -- backward, second reading
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 g = mul2(mul2(r[i], GATED ? f[i] : slope[i]), wt[i]);
-              if (GATED) nn[i] = mul2(mul2(r[i], nn[i]), slope[i]);
-              v[i] = mul2(rs, fma2(v[i], n2, add2(g, n1)));
+            for (int k = 0; k < 4; ++k) {
+              const float2 h = mul2(mul2(g[k], GATED ? f[k] : slope[k]), wt[k]);
+              if (GATED) nn[k] = mul2(mul2(g[k], nn[k]), slope[k]);
+              v[k] = mul2(rs, fma2(v[k], n2, add2(h, n1)));
             }
-            store_pairs<WIDE, 8, true>(ddx, v, n);
-            ddx += p.rows * a.dx.st;
-            if (GATED) {
-              store_pairs<WIDE, 8, true>(ddg, nn, n);
-              ddg += p.rows * a.dgate.st;
-            }
+            store_pairs<WIDE, 8, true>(dx, v, n);
+            if (GATED) store_pairs<WIDE, 8, true>(dgate, nn, n);
           }
         }
-        begin(behind);
-        if (!q.output) {
-          const float w1 = warp_sum(s1.x + s1.y), w2 = warp_sum(s2.x + s2.y);
-          if ((tid & 31) == 0) {
-            red[warp][0] = w1;
-            red[warp][1] = w2;
-          }
-          if (w.param != nullptr) {  // each channel's sums over the item's tokens
-            const int line = p.lanes * 8;
-            reinterpret_cast<float4*>(cols + (row * 2 + 0) * line + lane * 8)[0] =
-                make_float4(dw[0].x, dw[0].y, dw[1].x, dw[1].y);
-            reinterpret_cast<float4*>(cols + (row * 2 + 0) * line + lane * 8)[1] =
-                make_float4(dw[2].x, dw[2].y, dw[3].x, dw[3].y);
-            reinterpret_cast<float4*>(cols + (row * 2 + 1) * line + lane * 8)[0] =
-                make_float4(db[0].x, db[0].y, db[1].x, db[1].y);
-            reinterpret_cast<float4*>(cols + (row * 2 + 1) * line + lane * 8)[1] =
-                make_float4(db[2].x, db[2].y, db[3].x, db[3].y);
-            __syncthreads();
-            const int cb = q.c0, D = a.NH * a.d;
-            float* out = w.param + ((long long)q.b * p.slabs + q.slab) * 2 * D + q.head * a.d + cb;
-            for (int e = tid; e < 2 * line; e += kThreads) {
-              const int which = e / line, c = e % line;
-              if (cb + c < a.d) {
-                float s = 0.f;
-                for (int r = 0; r < p.rows; ++r) s += cols[(r * 2 + which) * line + c];
-                out[(long long)which * D + c] = s;
-              }
-            }
-          }
-        }
+        t += p.rows;
+        dx += p.rows * a.dx.st;
+        if (GATED) dgate += p.rows * a.dgate.st;
       }
+      copies_wait<0>();
+      begin(behind);
       if (!q.output) {
-        // -- the item's sums, and the group's by whoever finishes it
-        __syncthreads();
-        if (warp == 0) {
-          float* part = w.part + ((long long)q.group * p.parts() + q.part) * 3;
-          unsigned int before = 0;
-          if (tid == 0) {
-            float s[3] = {red[0][0], red[0][1], BWD ? 0.f : red[0][2]};
-            for (int i = 1; i < kThreads / 32; ++i) {
-              if (BWD) {
-                s[0] += red[i][0];
-                s[1] += red[i][1];
-              } else {
-                join(s[0], s[1], s[2], red[i][0], red[i][1], red[i][2]);
-              }
-            }
-            for (int i = 0; i < 3; ++i) __stcg(part + i, s[i]);
-            __threadfence();
-            before = atomicAdd(w.done + q.group, 1u);
-          }
-          before = __shfl_sync(0xffffffffu, before, 0);
-          if (before == (unsigned int)p.parts() - 1) {
-            __threadfence();
-            double s0 = 0, s1 = 0, s2 = 0;
-            const float* all = w.part + (long long)q.group * p.parts() * 3;
-            for (int i = tid; i < p.parts(); i += 32) {
-              const double v0 = __ldcg(all + 3 * i), v1 = __ldcg(all + 3 * i + 1), v2 = __ldcg(all + 3 * i + 2);
-              if (BWD) {
-                s0 += v0;
-                s1 += v1;
-              } else {
-                join(s0, s1, s2, v0, v1, v2);
-              }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              const double v0 = __shfl_down_sync(0xffffffffu, s0, o), v1 = __shfl_down_sync(0xffffffffu, s1, o),
-                           v2 = __shfl_down_sync(0xffffffffu, s2, o);
-              if (BWD) {
-                s0 += v0;
-                s1 += v1;
-              } else {
-                join(s0, s1, s2, v0, v1, v2);
-              }
-            }
-            if (tid == 0) {
-              float2 r;
-              if (BWD) {
-                const double inv = 1.0 / ((double)a.T * a.d);
-                r = make_float2((float)(s0 * inv), (float)(s1 * inv));
-              } else {
-                r = make_float2((float)s1, (float)(1.0 / sqrt(s2 / s0 + (double)a.eps)));
-                if (a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[q.group] = r;
-              }
-              __stcg(w.pair + q.group, r);
-              __threadfence();
-              asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(w.ready + q.group) : "memory");
+        const float w1 = warp_sum(s1.x + s1.y), w2 = warp_sum(s2.x + s2.y);
+        if ((tid & 31) == 0) {
+          red[i & 1][warp][0] = w1;
+          red[i & 1][warp][1] = w2;
+        }
+        if (w.param != nullptr) {  // each channel's sums over the item's tokens
+          const int line = p.lanes * 8;
+          float4* c = reinterpret_cast<float4*>(cols + row * 2 * line + lane * 8);
+          c[0] = make_float4(dw[0].x, dw[0].y, dw[1].x, dw[1].y);
+          c[1] = make_float4(dw[2].x, dw[2].y, dw[3].x, dw[3].y);
+          c += line / 4;
+          c[0] = make_float4(db[0].x, db[0].y, db[1].x, db[1].y);
+          c[1] = make_float4(db[2].x, db[2].y, db[3].x, db[3].y);
+          named_barrier(2, kThreads);
+          const int D = a.NH * a.d;
+          float* out = w.param + ((long long)q.b * p.slabs + q.slab) * 2 * D + q.head * a.d + q.c0;
+          for (int e = tid; e < 2 * line; e += kThreads) {
+            const int which = e / line, ch = e % line;
+            if (q.c0 + ch < a.d) {
+              float s = 0.f;
+              for (int k = 0; k < p.rows; ++k) s += cols[(k * 2 + which) * line + ch];
+              out[(long long)which * D + ch] = s;
             }
           }
         }
       }
     }
-    if (!real) begin(behind);
-    // the slot of the item before this one, which nobody reads any more
-    if (tid == 0) items[at == 0 ? 2 : at - 1].set(a, p, after);
-    __syncthreads();
+    named_barrier(0, ALL);
   }
 }
 
 template <typename T, bool GATED, bool WIDE, bool BWD>
 cudaError_t run(const NormArgs& a, cudaStream_t s) {
-  const Plan p = plan_for(a.B, a.T, a.NH, a.d, BWD);
+  const Plan p = plan_for(a.B, a.T, a.NH, a.d, (int)sizeof(T), GATED, BWD);
   const Layout l = layout_for(p, a.B, a.NH * a.d, BWD);
   char* ws = (char*)a.ws;
   Work w;
@@ -457,13 +510,14 @@ cudaError_t run(const NormArgs& a, cudaStream_t s) {
   cudaError_t e = cudaMemsetAsync(ws, 0, l.zeroed, s);
   if (e != cudaSuccess) return e;
   constexpr int tensors = 1 + BWD + GATED;
-  constexpr int bytes = kThreads * (kRing<T, tensors> * tensors * 8 * (int)sizeof(T) + (BWD ? 64 : 0));
+  constexpr int bytes =
+      kThreads * (each_of((int)sizeof(T), tensors) * tensors * 8 * (int)sizeof(T) + (BWD ? 64 : 0));
   e = cudaFuncSetAttribute(norm_sequence_kernel<T, GATED, WIDE, BWD>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   const long long items = p.items(), slots = slots_of(BWD);
   norm_sequence_kernel<T, GATED, WIDE, BWD>
-      <<<(unsigned)(items < slots ? items : slots), kThreads, bytes, s>>>(a, p, w, next_epoch());
+      <<<(unsigned)(items < slots ? items : slots), kThreads + 64, bytes, s>>>(a, p, w, next_epoch());
   e = cudaGetLastError();
   if (e != cudaSuccess || !params) return e;
   return launch_param_sums(w.param, a.B * p.slabs, a.NH * a.d, 1, a.dw, a.dbias, s);
@@ -476,8 +530,14 @@ cudaError_t by_kind(const NormArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t norm_sequence_workspace(int B, int T, int NH, int d, bool backward) {
-  return layout_for(plan_for(B, T, NH, d, backward), B, NH * d, backward).total;
+size_t norm_sequence_workspace(int B, int T, int NH, int d, int dtype, bool backward) {
+  size_t most = 0;  // with a gate or without
+  for (int gated = 0; gated < 2; ++gated) {
+    const Plan p = plan_for(B, T, NH, d, dtype == 0 ? 2 : 4, gated != 0, backward);
+    const size_t bytes = layout_for(p, B, NH * d, backward).total;
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 cudaError_t launch_norm_sequence(const NormArgs& a, bool backward, cudaStream_t s) {
