@@ -125,6 +125,13 @@ def _check(status, where):
         raise MLSTMError(status, where)
 
 
+def _like(t):
+    """A contiguous tensor like t (None for None)."""
+    if t is None:
+        return None
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _bytes(n, like):
     return like.new_empty(max(n, 16), dtype=torch.uint8)
 
@@ -170,7 +177,7 @@ def causal_conv_forward(x, weight, bias=None, *, act=ACT_SILU, state_in=None, wa
     NH, d = _heads_of(D, heads)
 
     def launch(s):
-        y = x.new_empty((B, T, D) if heads is None else (B, NH, T, d))
+        y = _like(x) if heads is None else x.new_empty((B, NH, T, d))
         state_out = x.new_empty((B, W - 1, D)) if want_state else None
         _check(load().mlstm_conv_fwd(_rows(x), weight.data_ptr(), _ptr(bias), _ptr(state_in),
                                      _head_rows(y, "last" if heads is None else "heads", d),
@@ -195,8 +202,7 @@ def causal_conv_backward(x, weight, bias, dy, *, act=ACT_SILU, state_in=None, ds
     _contiguous("dstate_out", dstate_out, (B, W - 1, D), x)
 
     def launch(s):
-        out = {"dx": x.new_empty((B, T, D)), "dweight": weight.new_empty((D, W)),
-               "dbias": bias.new_empty((D,)) if bias is not None else None,
+        out = {"dx": _like(x), "dweight": _like(weight), "dbias": _like(bias),
                "dstate_in": x.new_empty((B, W - 1, D)) if want_dstate else None}
         ws = _bytes(load().mlstm_conv_bwd_workspace_size(B, T, NH, d, W, dt), x)
         _check(load().mlstm_conv_bwd(_rows(x), weight.data_ptr(), _ptr(bias), _ptr(state_in),
@@ -219,7 +225,7 @@ def causal_conv_step(x, weight, bias, state, *, act=ACT_SILU, heads=None, stream
     NH, d = _heads_of(D, heads)
 
     def launch(s):
-        y = x.new_empty((B, D) if heads is None else (B, NH, d))
+        y = _like(x) if heads is None else x.new_empty((B, NH, d))
         at = state.data_ptr()
         _check(load().mlstm_conv_step(_rows(x), weight.data_ptr(), _ptr(bias), at,
                                       Rows(y.data_ptr(), D, 0, d), at, B, NH, d, W, act, dt, s),
@@ -287,7 +293,7 @@ def selective_scan_forward(x, dt, A, B, C, *, skip=None, z=None, dt_bias=None, s
     p = _scan_problem(x, dt, A, B, C, skip, z, dt_bias, softplus, state_in)
 
     def launch(s):
-        y = x.new_empty(x.shape)
+        y = _like(x)
         saved = (_bytes(load().mlstm_scan_saved_size(p.B, p.T, p.D, p.G, p.N, p.dtype), x)
                  if keep_saved else None)
         state_out = x.new_empty((p.B, p.D, p.N), dtype=torch.float32) if want_state else None
@@ -314,9 +320,8 @@ def selective_scan_backward(x, dt, A, B, C, dy, saved, *, skip=None, z=None, dt_
         raise ValueError(f"saved must hold the {need} bytes of the forward of the same inputs")
 
     def launch(s):
-        new = lambda t: None if t is None else t.new_empty(t.shape)
-        out = {"dx": new(x), "ddt": new(x), "dA": new(A), "dB": new(B), "dC": new(C),
-               "dskip": new(skip), "ddt_bias": new(dt_bias), "dz": new(z),
+        out = {"dx": _like(x), "ddt": _like(x), "dA": _like(A), "dB": _like(B), "dC": _like(C),
+               "dskip": _like(skip), "ddt_bias": _like(dt_bias), "dz": _like(z),
                "dstate_in": A.new_empty((p.B, p.D, p.N)) if want_dstate else None}
         g = ScanGrads(_rows(out["dx"]), _rows(out["ddt"]), _rows(out["dz"]), _group_rows(out["dB"]),
                       _group_rows(out["dC"]), _ptr(out["dA"]), _ptr(out["dskip"]),
@@ -344,7 +349,7 @@ def selective_scan_step(x, dt, A, B, C, state, *, skip=None, z=None, dt_bias=Non
     p = _scan_problem(x, dt, A, B, C, skip, z, dt_bias, softplus, state)
 
     def launch(s):
-        y = x.new_empty(x.shape)
+        y = _like(x)
         _check(load().mlstm_scan_step(p, _rows(y), state.data_ptr(), s), "mlstm_scan_step")
         return y
 
@@ -423,8 +428,7 @@ def group_norm_backward(x, weight, bias, dy, stats, *, gate=None, act=ACT_NONE, 
     _fp32("stats", stats, _stats_shape(B, T, NH, scope), x)
 
     def launch(s):
-        new = lambda t: None if t is None else t.new_empty(t.shape)
-        out = {"dx": new(x), "dweight": new(weight), "dbias": new(bias), "dgate": new(gate)}
+        out = {"dx": _like(x), "dweight": _like(weight), "dbias": _like(bias), "dgate": _like(gate)}
         need = load().mlstm_group_norm_workspace_size(B, T, NH, d, scope, dt, 1)
         ws = _bytes(need, x) if need else None
         _check(load().mlstm_group_norm_bwd(_head_rows(x, layout, d), _ptr(weight), _ptr(bias),
