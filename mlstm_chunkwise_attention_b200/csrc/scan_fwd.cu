@@ -160,27 +160,33 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                 a.saved + (((long long)b * NC + (t0 + tg) / kScanEvery) * a.D + q.c0 + l.ch[e]) * NP +
                 nl * 4) = make_float4(h[e][0].x, h[e][0].y, h[e][1].x, h[e][1].y);
       }
+      // The eight tokens' sums over the lanes come after all of their updates: then eight shuffles
+      // are under way at once instead of each token waiting for its own.
+      float2 y[kScanEvery];
+#pragma unroll
+      for (int u = 0; u < kScanEvery; ++u) {
+        const int t = tg + u;
+        const float4 Bv = *reinterpret_cast<const float4*>(&sbc[t][nl * 4]);
+        const float4 Cv = *reinterpret_cast<const float4*>(&sbc[t][NP + nl * 4]);
+        float yv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 d = *reinterpret_cast<const float2*>(dsrc[e] + t * VECS * kPairUnit);
+          const float2 dd = make_float2(d.x, d.x), ww = make_float2(d.y, d.y);
+          h[e][0] = fma2(exp2_pair(mul2(dd, A2[e][0])), h[e][0], mul2(ww, make_float2(Bv.x, Bv.y)));
+          h[e][1] = fma2(exp2_pair(mul2(dd, A2[e][1])), h[e][1], mul2(ww, make_float2(Bv.z, Bv.w)));
+          const float2 v = fma2(h[e][1], make_float2(Cv.z, Cv.w), mul2(h[e][0], make_float2(Cv.x, Cv.y)));
+          yv[e] = v.x + v.y;
+        }
+        y[u] = make_float2(yv[0], yv[1]);
+      }
+#pragma unroll
+      for (int u = 0; u < kScanEvery; ++u) y[u].x += __shfl_xor_sync(0xffffffffu, y[u].y, 1);
 #pragma unroll
       for (int ti = 0; ti < kScanEvery; ti += AT_ONCE) {
         float acc[AT_ONCE];
 #pragma unroll
-        for (int u = 0; u < AT_ONCE; ++u) {
-          const int t = tg + ti + u;
-          const float4 Bv = *reinterpret_cast<const float4*>(&sbc[t][nl * 4]);
-          const float4 Cv = *reinterpret_cast<const float4*>(&sbc[t][NP + nl * 4]);
-          float y[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 d = *reinterpret_cast<const float2*>(dsrc[e] + t * VECS * kPairUnit);
-            const float2 dd = make_float2(d.x, d.x), ww = make_float2(d.y, d.y);
-            h[e][0] = fma2(exp2_pair(mul2(dd, A2[e][0])), h[e][0], mul2(ww, make_float2(Bv.x, Bv.y)));
-            h[e][1] = fma2(exp2_pair(mul2(dd, A2[e][1])), h[e][1], mul2(ww, make_float2(Bv.z, Bv.w)));
-            const float2 v =
-                fma2(h[e][1], make_float2(Cv.z, Cv.w), mul2(h[e][0], make_float2(Cv.x, Cv.y)));
-            y[e] = v.x + v.y;
-          }
-          acc[u] = y[0] + __shfl_xor_sync(0xffffffffu, y[1], 1);
-        }
+        for (int u = 0; u < AT_ONCE; ++u) acc[u] = y[ti + u].x;
         scatter_sum<AT_ONCE, AT_ONCE, 2>(acc, nl >> 1);
         ydst[(tg + ti) * VECS * kFloatUnit] = acc[0];
       }
