@@ -162,19 +162,36 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       }
       // The eight tokens' sums over the lanes come after all of their updates: then eight shuffles
       // are under way at once instead of each token waiting for its own.
-      float2 y[kScanEvery];
+      float2 y[kScanEvery], ex[2][2], w[2];
+      auto ahead = [&](int t) {  // a token's decays, while the token before it is worked on
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 d = *reinterpret_cast<const float2*>(dsrc[e] + t * VECS * kPairUnit);
+          const float2 dd = make_float2(d.x, d.x);
+          ex[e][0] = exp2_pair(mul2(dd, A2[e][0]));
+          ex[e][1] = exp2_pair(mul2(dd, A2[e][1]));
+          w[e] = make_float2(d.y, d.y);
+        }
+      };
+      ahead(tg);
 #pragma unroll
       for (int u = 0; u < kScanEvery; ++u) {
         const int t = tg + u;
         const float4 Bv = *reinterpret_cast<const float4*>(&sbc[t][nl * 4]);
         const float4 Cv = *reinterpret_cast<const float4*>(&sbc[t][NP + nl * 4]);
+        float2 E[2][2], W[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          E[e][0] = ex[e][0];
+          E[e][1] = ex[e][1];
+          W[e] = w[e];
+        }
+        if (u + 1 < kScanEvery) ahead(t + 1);
         float yv[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float2 d = *reinterpret_cast<const float2*>(dsrc[e] + t * VECS * kPairUnit);
-          const float2 dd = make_float2(d.x, d.x), ww = make_float2(d.y, d.y);
-          h[e][0] = fma2(exp2_pair(mul2(dd, A2[e][0])), h[e][0], mul2(ww, make_float2(Bv.x, Bv.y)));
-          h[e][1] = fma2(exp2_pair(mul2(dd, A2[e][1])), h[e][1], mul2(ww, make_float2(Bv.z, Bv.w)));
+          h[e][0] = fma2(E[e][0], h[e][0], mul2(W[e], make_float2(Bv.x, Bv.y)));
+          h[e][1] = fma2(E[e][1], h[e][1], mul2(W[e], make_float2(Bv.z, Bv.w)));
           const float2 v = fma2(h[e][1], make_float2(Cv.z, Cv.w), mul2(h[e][0], make_float2(Cv.x, Cv.y)));
           yv[e] = v.x + v.y;
         }
