@@ -32,20 +32,19 @@ struct Cfg {
   static constexpr int CT = kWarps * CL * 2;  // channels of a CTA
   static constexpr int VECS = CT / 8, UNITS = kTile * VECS;
   static constexpr int ITEMS = (UNITS + kThreads - 1) / kThreads;  // units of a thread
-  static constexpr int SETS = VECS < 32 ? VECS : 32;               // lanes of a warp with channels of their own
   // A lane keeps its states in the order k ^ perm, perm from its channel rank, so that each step
   // of the sum over channels sends one half of what it holds and keeps the other without choosing;
   // B and C lie in one copy for each order.
   static constexpr int ORDER = kTile * 2 * NP + 8;  // floats of a copy, with 8 to spread the banks
   // shared memory, in floats: delta and delta x of the tile, dy of the tile; sums over states of g B,
   // u A and C s; B and C; dB and dC of each warp [warps][tile][2 NP]; dskip and ddt_bias shares of
-  // each warp's channels [4][warps][units a token] of four; dt_bias and skip; the next saved state
-  // [2][threads] of four floats; and two tiles of x, dt, dy, z as they lie in memory
+  // each thread's channels [4][threads] of four; dt_bias and skip; the next saved state [2][threads] of
+  // four floats; and the tile's x, dt, dy, z as they lie in memory
   static constexpr int DX = 0, DY = DX + UNITS * kPairUnit, SUM = DY + UNITS * kFloatUnit,
                        BC = SUM + 3 * UNITS * kFloatUnit, RED = BC + 4 * ORDER,
-                       ACC = RED + kWarps * kTile * 2 * NP, BIAS = ACC + 16 * kWarps * SETS, SKIP = BIAS + CT,
+                       ACC = RED + kWarps * kTile * 2 * NP, BIAS = ACC + 16 * kThreads, SKIP = BIAS + CT,
                        SAVED = SKIP + CT, RAW = SAVED + 8 * kThreads,
-                       TOTAL = RAW + 2 * 4 * UNITS * 8 * (int)sizeof(T) / 4;
+                       TOTAL = RAW + 4 * UNITS * 8 * (int)sizeof(T) / 4;
 };
 
 template <typename T, int LPC, bool GATE, bool WIDE>
@@ -99,7 +98,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
       enter_segment<NP, true>(a, b, q.c0 + ch[e], nl, seg, A2[e], G[e], perm);
     }
   }
-  for (int i = tid; i < 16 * kWarps * C::SETS; i += kThreads) sm[C::ACC + i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<float4*>(sm + C::ACC)[i * kThreads + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = tid; i < CT; i += kThreads) {
     sm[C::BIAS + i] = a.dt_bias != nullptr && i < q.n ? a.dt_bias[q.c0 + i] : 0.f;
     sm[C::SKIP + i] = a.skip != nullptr && i < q.n ? a.skip[q.c0 + i] : 0.f;
@@ -108,21 +109,23 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
                     (const T*)a.y.p + b * a.y.sb + q.c0,
                     GATE ? (const T*)a.z.p + b * a.z.sb + q.c0 : nullptr};
   const long long stride[4] = {a.x.st, a.dt.st, a.y.st, a.z.st};
-  auto raw = [&](int stage, int tensor, int item) {
-    return reinterpret_cast<Raw<T, 8>*>(sm + C::RAW) + (stage * 4 + tensor) * UNITS + item;
+  auto raw = [&](int tensor, int item) {
+    return reinterpret_cast<Raw<T, 8>*>(sm + C::RAW) + tensor * UNITS + item;
   };
   // A thread fetches and reads only its own units, so no barrier is needed for them.
-  auto fetch = [&](int t0, int stage) {
+  auto fetch = [&](int t0) {
 #pragma unroll
     for (int m = 0; m < C::ITEMS; ++m) {
       const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
       if (item < UNITS) {
 #pragma unroll
         for (int k = 0; k < 3 + GATE; ++k) {
-          Raw<T, 8>* to = raw(stage, k, item);
+          Raw<T, 8>* to = raw(k, item);
           const T* from = in[k] + t * stride[k] + cv;
           if (t < last && n > 0) {
             fetch_raw<WIDE>(to, from, n);
+            // the same units of the next tile, into L2
+            if (WIDE && t - kTile >= first) prefetch_l2(from - kTile * stride[k]);
           } else {
             zero_raw(*to);
           }
@@ -145,23 +148,22 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
   const int top = (last - 1 - first) / kTile * kTile + first;
   // the upper eight tokens of the first tile may lie behind the end; then the lower come first
   fetch_saved(top + kScanEvery < last ? top + kScanEvery : top);
-  fetch(top, 0);
-  copies_commit();
-  int stage = 0;
   __syncthreads();
-  for (int t0 = top; t0 >= first; t0 -= kTile, stage ^= 1) {
+  for (int t0 = top; t0 >= first; t0 -= kTile) {
+    fetch(t0);
+    copies_commit();
     stage_bc<T, NP, kTile, 4, C::ORDER>(a, b, q.g, t0, last, sm + C::BC, tid, kThreads);
     copies_wait<0>();
 #pragma unroll
     for (int m = 0; m < C::ITEMS; ++m) {
       const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
       if (item < UNITS) {
-        stage_delta<T>(a, *raw(stage, 0, item), *raw(stage, 1, item), sm + C::BIAS + cv, t < last, n,
+        stage_delta<T>(a, *raw(0, item), *raw(1, item), sm + C::BIAS + cv, t < last, n,
                        sm + C::DX + item * kPairUnit);
         float2 g[4], z[4];
-        expand(*raw(stage, 2, item), g);
+        expand(*raw(2, item), g);
         if (GATE) {
-          expand(*raw(stage, 3, item), z);
+          expand(*raw(3, item), z);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             g[i] = mul2(g[i], act_pair<kActSilu>(z[i]));
@@ -169,15 +171,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
         store_unit(sm + C::DY + item * kFloatUnit, g);
       }
     }
-    if (t0 - kTile >= first) fetch(t0 - kTile, stage ^ 1);  // on its way while this tile is worked on
-    copies_commit();
     __syncthreads();
 #pragma unroll 1
     for (int sub = kTile - kScanEvery; sub >= 0; sub -= kScanEvery) {
       if (t0 + sub >= last) continue;
-      // The upper eight tokens' states came with the tile (as did the lower's, where there is no upper);
-      // the lower's are the newest copies, behind the next tile's.
-      if (sub == 0 && t0 + kScanEvery < last) copies_wait<0>();
+      copies_wait<0>();
       float2 h0[2][2], s[kScanEvery][2][2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -222,19 +220,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
           if (nl < 2) sums[(2 * UNITS + i * VECS) * kFloatUnit] = y[0];
         }
       }
-      // Going back, a token's decays are worked out while the token behind it is.
-      float2 ex[2][2], dd[2], dx[2];
-      auto ahead = [&](int i) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 d = *reinterpret_cast<const float2*>(dxs[e] + i * VECS * kPairUnit);
-          dd[e] = make_float2(d.x, d.x);
-          dx[e] = make_float2(d.y, d.y);
-          ex[e][0] = exp2_pair(mul2(dd[e], A2[e][0]));
-          ex[e][1] = exp2_pair(mul2(dd[e], A2[e][1]));
-        }
-      };
-      ahead(kScanEvery - 1);
 #pragma unroll
       for (int i = kScanEvery - 1; i >= 0; --i) {
         const float4 Bq = *reinterpret_cast<const float4*>(bcs + i * 2 * NP);
@@ -242,23 +227,22 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
         const float2 Bv[2] = {make_float2(Bq.x, Bq.y), make_float2(Bq.z, Bq.w)};
         const float2 Cv[2] = {make_float2(Cq.x, Cq.y), make_float2(Cq.z, Cq.w)};
         float2 db[2], dc[2], gb[2], ua[2];
-        const float2 E[2][2] = {{ex[0][0], ex[0][1]}, {ex[1][0], ex[1][1]}};
-        const float2 DD[2] = {dd[0], dd[1]}, DX[2] = {dx[0], dx[1]};
-        if (i > 0) ahead(i - 1);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          const float2 d = *reinterpret_cast<const float2*>(dxs[e] + i * VECS * kPairUnit);
+          const float2 dd = make_float2(d.x, d.x), dx = make_float2(d.y, d.y);
           const float dy1 = dys[e][i * VECS * kFloatUnit];
           const float2 dy = make_float2(dy1, dy1);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const float2 g = fma2(dy, Cv[p], G[e][p]);
-            db[p] = e == 0 ? mul2(DX[e], g) : fma2(DX[e], g, db[p]);
+            db[p] = e == 0 ? mul2(dx, g) : fma2(dx, g, db[p]);
             dc[p] = e == 0 ? mul2(dy, s[i][e][p]) : fma2(dy, s[i][e][p], dc[p]);
             gb[e] = p == 0 ? mul2(g, Bv[p]) : fma2(g, Bv[p], gb[e]);
-            G[e][p] = mul2(E[e][p], g);
+            G[e][p] = mul2(exp2_pair(mul2(dd, A2[e][p])), g);
             const float2 u = mul2(G[e][p], i == 0 ? h0[e][p] : s[i - 1][e][p]);
             ua[e] = p == 0 ? mul2(u, A2[e][p]) : fma2(u, A2[e][p], ua[e]);
-            dA[e][p] = fma2(u, DD[e], dA[e][p]);
+            dA[e][p] = fma2(u, dd, dA[e][p]);
           }
         }
         // over the channel's lanes: the neighbour's first channel is this lane's second
@@ -317,16 +301,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
 #pragma unroll
     for (int m = 0; m < C::ITEMS; ++m) {
       const int item = tid + m * kThreads, t = t0 + item / VECS, cv = (item % VECS) * 8, n = q.n - cv;
-      float2 k[4] = {}, l[4] = {};  // dskip's and ddt_bias's terms
       if (item < UNITS && t < last && n > 0) {
         float2 x[4], d[4], v[4], sgb[4], dy[4], o[4];
-        expand(*raw(stage, 0, item), x);
+        expand(*raw(0, item), x);
         load_unit(sm + C::SUM + item * kFloatUnit, sgb);
         load_unit(sm + C::DY + item * kFloatUnit, dy);
         if (GATE) {
           float2 g[4], z[4], y[4];
-          expand(*raw(stage, 2, item), g);
-          expand(*raw(stage, 3, item), z);
+          expand(*raw(2, item), g);
+          expand(*raw(3, item), z);
           load_unit(sm + C::SUM + (2 * UNITS + item) * kFloatUnit, y);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -337,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
           }
           store_pairs<WIDE, 8>((T*)a.dz.p + b * a.dz.sb + t * a.dz.st + q.c0 + cv, o, n);
         }
-        expand(*raw(stage, 1, item), d);
+        expand(*raw(1, item), d);
         load_unit(sm + C::SUM + (UNITS + item) * kFloatUnit, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -351,35 +334,22 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
                       mul2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), dy[i]));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          k[i] = mul2(dy[i], x[i]);
-          l[i] = v[i];
+        for (int i = 0; i < 2; ++i) {
+          float4* acc = reinterpret_cast<float4*>(sm + C::ACC) + i * kThreads + tid;
+          float4 k = acc[0], l = acc[2 * kThreads];
+          k.x = fmaf(dy[2 * i].x, x[2 * i].x, k.x);
+          k.y = fmaf(dy[2 * i].y, x[2 * i].y, k.y);
+          k.z = fmaf(dy[2 * i + 1].x, x[2 * i + 1].x, k.z);
+          k.w = fmaf(dy[2 * i + 1].y, x[2 * i + 1].y, k.w);
+          l.x += v[2 * i].x;
+          l.y += v[2 * i].y;
+          l.z += v[2 * i + 1].x;
+          l.w += v[2 * i + 1].y;
+          acc[0] = k;
+          acc[2 * kThreads] = l;
         }
         store_pairs<WIDE, 8>((T*)a.dx.p + b * a.dx.sb + t * a.dx.st + q.c0 + cv, o, n);
         store_pairs<WIDE, 8>((T*)a.ddt.p + b * a.ddt.sb + t * a.ddt.st + q.c0 + cv, v, n);
-      }
-      // dskip and ddt_bias: the warp's lanes with the same channels together, then into the warp's share
-#pragma unroll
-      for (int o = C::SETS; o < 32; o <<= 1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          k[i].x += __shfl_xor_sync(0xffffffffu, k[i].x, o);
-          k[i].y += __shfl_xor_sync(0xffffffffu, k[i].y, o);
-          l[i].x += __shfl_xor_sync(0xffffffffu, l[i].x, o);
-          l[i].y += __shfl_xor_sync(0xffffffffu, l[i].y, o);
-        }
-      if (lane < C::SETS) {
-        float4* acc = reinterpret_cast<float4*>(sm + C::ACC) + warp * C::SETS + lane;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float4 f = acc[i * kWarps * C::SETS];
-          const float2 p0 = i < 2 ? k[2 * i] : l[2 * i - 4], p1 = i < 2 ? k[2 * i + 1] : l[2 * i - 3];
-          f.x += p0.x;
-          f.y += p0.y;
-          f.z += p1.x;
-          f.w += p1.y;
-          acc[i * kWarps * C::SETS] = f;
-        }
       }
     }
     __syncthreads();
@@ -403,14 +373,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
              permuted(make_float4(gs[0], gs[1], gs[2], gs[3]), perm));
   }
   if (a.in_turn && seg > 0) pass_turn(a, bi);
-  // a warp's lane keeps its channels through all items
-  static_assert(kThreads % VECS == 0 && (VECS >= 32 || 32 % VECS == 0), "lanes keep their channels");
+  // threads with the same channels: tid % VECS (a thread keeps its vector through all items)
+  static_assert(kThreads % VECS == 0, "a thread's channels are the same in every item");
   for (int e = tid; e < 2 * CT; e += kThreads) {
     const int which = e / CT, c = e % CT;
     if (c < q.n) {
       float v = 0.f;
-      for (int w = 0; w < kWarps; ++w)
-        v += sm[C::ACC + (((which * 2 + c % 8 / 4) * kWarps + w) * C::SETS + c / 8) * 4 + c % 4];
+      for (int w = c / 8; w < kThreads; w += VECS) v += sm[C::ACC + ((which * 2 + c % 8 / 4) * kThreads + w) * 4 + c % 4];
       a.part_d[((long long)row * 2 + which) * a.D + q.c0 + c] = v;
     }
   }
