@@ -362,30 +362,29 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns, 4) conv_bwd_kernel(ConvA
   }
 }
 
-// Sums over the rows of partials, 8 row shares to a column joined in a fixed order.
-__global__ void __launch_bounds__(256) param_sums_kernel(const float* __restrict__ partial,
-                                                         float* __restrict__ dw,
-                                                         float* __restrict__ dbias, int rows, int D,
-                                                         int W) {
-  __shared__ float red[8][32];
+// Sums over the rows of partials, 32 row shares to a column joined in a fixed order.
+__global__ void __launch_bounds__(1024) param_sums_kernel(const float* __restrict__ partial,
+                                                          float* __restrict__ dw,
+                                                          float* __restrict__ dbias, int rows, int D, int W) {
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-  const long long col = (long long)blockIdx.x * 32 + lane, cols = (long long)(W + 1) * D;
+  const long long first = (long long)blockIdx.x * 32, cols = (long long)(W + 1) * D;
   float s = 0.f;
-  if (col < cols)
+  if (first + lane < cols)
 #pragma unroll 4
-    for (int r = part; r < rows; r += 8) s += partial[(long long)r * cols + col];
+    for (int r = part; r < rows; r += 32) s += partial[(long long)r * cols + first + lane];
   red[part][lane] = s;
   __syncthreads();
-  if (part == 0 && col < cols) {
-    s = 0.f;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) s += red[q][lane];
+  const long long col = first + part;  // a warp joins one column
+  s = warp_sum(red[lane][part]);
+  if (lane == 0 && col < cols) {
     const int j = (int)(col / D);
     const long long c = col % D;
     if (j < W) {
       if (dw != nullptr) dw[c * W + j] = s;
-    } else if (dbias != nullptr)
+    } else if (dbias != nullptr) {
       dbias[c] = s;
+    }
   }
 }
 
@@ -457,7 +456,7 @@ int conv_bwd_rows(int B, int T, int) {
 
 cudaError_t launch_param_sums(const float* partial, int rows, int D, int W, float* dw, float* dbias,
                               cudaStream_t s) {
-  param_sums_kernel<<<(unsigned)(((long long)(W + 1) * D + 31) / 32), 256, 0, s>>>(partial, dw, dbias,
+  param_sums_kernel<<<(unsigned)(((long long)(W + 1) * D + 31) / 32), 1024, 0, s>>>(partial, dw, dbias,
                                                                                    rows, D, W);
   return cudaGetLastError();
 }

@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
                     (const T*)a.y.p + b * a.y.sb + q.c0,
                     GATE ? (const T*)a.z.p + b * a.z.sb + q.c0 : nullptr};
   const long long stride[4] = {a.x.st, a.dt.st, a.y.st, a.z.st};
+  const long long part_step = (long long)a.G * 2 * NP;
+  float* part = a.part_bc + (((long long)(ti % tiles) * a.B + b) * a.T * a.G + q.g) * 2 * NP;
   auto raw = [&](int tensor, int item) {
     return reinterpret_cast<Raw<T, 8>*>(sm + C::RAW) + tensor * UNITS + item;
   };
@@ -288,14 +290,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
       }
     }
     __syncthreads();
-    // the CTA's share of dB and dC
-    for (int e = tid; e < kTile * 2 * NP; e += kThreads) {
-      const int t = e / (2 * NP), r = e % (2 * NP);
+    // the CTA's share of dB and dC, four states at a time
+    for (int e = tid; e < kTile * NP / 2; e += kThreads) {
+      const int t = e / (NP / 2), r = (e % (NP / 2)) * 4;
       if (t0 + t < last) {
-        float v = 0.f;
+        const float* red = sm + C::RED + t * 2 * NP + r;
+        float2 v[2] = {};
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += sm[C::RED + (w * kTile + t) * 2 * NP + r];
-        a.part_bc[((((long long)(ti % tiles) * a.B + b) * a.T + t0 + t) * a.G + q.g) * 2 * NP + r] = v;
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 f = *reinterpret_cast<const float4*>(red + w * kTile * 2 * NP);
+          v[0] = add2(v[0], make_float2(f.x, f.y));
+          v[1] = add2(v[1], make_float2(f.z, f.w));
+        }
+        *reinterpret_cast<float4*>(part + (t0 + t) * part_step + r) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
       }
     }
 #pragma unroll
