@@ -207,20 +207,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
             s[i][e][p] = fma2(exp2_pair(mul2(dd, A2[e][p])), i == 0 ? h0[e][p] : s[i - 1][e][p], mul2(dx, Bv[p]));
           }
         }
-        if (GATE) {  // the ungated output, for dz
-          const float4 Cq = *reinterpret_cast<const float4*>(bcs + i * 2 * NP + NP);
-          float y[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 v = fma2(s[i][e][1], make_float2(Cq.z, Cq.w), mul2(s[i][e][0], make_float2(Cq.x, Cq.y)));
-            y[e] = v.x + v.y;
-          }
-          // the neighbour's first channel is this lane's second
-          y[0] += __shfl_xor_sync(0xffffffffu, y[1], 1);
-#pragma unroll
-          for (int o = 2; o < LPC; o <<= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
-          if (nl < 2) sums[(2 * UNITS + i * VECS) * kFloatUnit] = y[0];
-        }
       }
 #pragma unroll
       for (int i = kScanEvery - 1; i >= 0; --i) {
@@ -228,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
         const float4 Cq = *reinterpret_cast<const float4*>(bcs + i * 2 * NP + NP);
         const float2 Bv[2] = {make_float2(Bq.x, Bq.y), make_float2(Bq.z, Bq.w)};
         const float2 Cv[2] = {make_float2(Cq.x, Cq.y), make_float2(Cq.z, Cq.w)};
-        float2 db[2], dc[2], gb[2], ua[2];
+        float2 db[2], dc[2], gb[2], ua[2], cs[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float2 d = *reinterpret_cast<const float2*>(dxs[e] + i * VECS * kPairUnit);
@@ -240,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
             const float2 g = fma2(dy, Cv[p], G[e][p]);
             db[p] = e == 0 ? mul2(dx, g) : fma2(dx, g, db[p]);
             dc[p] = e == 0 ? mul2(dy, s[i][e][p]) : fma2(dy, s[i][e][p], dc[p]);
+            if (GATE) cs[e] = p == 0 ? mul2(s[i][e][p], Cv[p]) : fma2(s[i][e][p], Cv[p], cs[e]);
             gb[e] = p == 0 ? mul2(g, Bv[p]) : fma2(g, Bv[p], gb[e]);
             G[e][p] = mul2(exp2_pair(mul2(dd, A2[e][p])), g);
             const float2 u = mul2(G[e][p], i == 0 ? h0[e][p] : s[i - 1][e][p]);
@@ -251,6 +238,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
         float sg = gb[0].x + gb[0].y, su = ua[0].x + ua[0].y;
         sg += __shfl_xor_sync(0xffffffffu, gb[1].x + gb[1].y, 1);
         su += __shfl_xor_sync(0xffffffffu, ua[1].x + ua[1].y, 1);
+        if (GATE) {  // the ungated output, for dz
+          float sy = cs[0].x + cs[0].y;
+          sy += __shfl_xor_sync(0xffffffffu, cs[1].x + cs[1].y, 1);
+#pragma unroll
+          for (int o = 2; o < LPC; o <<= 1) sy += __shfl_xor_sync(0xffffffffu, sy, o);
+          if (nl < 2) sums[(2 * UNITS + i * VECS) * kFloatUnit] = sy;
+        }
         if constexpr (LPC == 2) {
           sums[i * VECS * kFloatUnit] = sg;
           sums[(UNITS + i * VECS) * kFloatUnit] = su;

@@ -172,6 +172,34 @@ __device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0
   }
 }
 
+// B and C of a tile in whole vectors of eight, loaded ahead of their tile: what stage_bc does for
+// a.wide_bc and N == NP, in two steps.  PAIRS 2: B and C, rows of 2 NP; 1: `b` alone, rows of NP.
+template <typename T, int NP, int TT, int PAIRS, int THREADS>
+struct RowLoads {
+  static constexpr int PER = PAIRS * NP / 8, COUNT = (TT * PER + THREADS - 1) / THREADS;
+  Raw<T, 8> r[COUNT];
+  __device__ __forceinline__ void load(const T* b, long long bst, const T* c, long long cst, int t0, int last,
+                                       int tid) {
+#pragma unroll
+    for (int m = 0; m < COUNT; ++m) {
+      const int e = tid + m * THREADS, t = t0 + e / PER, v = e % PER, n = (v % (NP / 8)) * 8;
+      zero_raw(r[m]);
+      if (e < TT * PER && t < last) load_raw<true>(v >= NP / 8 ? c + t * cst + n : b + t * bst + n, r[m], 8);
+    }
+  }
+  __device__ __forceinline__ void store(float* out, int tid) const {
+#pragma unroll
+    for (int m = 0; m < COUNT; ++m) {
+      const int e = tid + m * THREADS, t = e / PER, v = e % PER;
+      if (e < TT * PER) {
+        float2 f[4];
+        expand(r[m], f);
+        store_unit(out + t * PAIRS * NP + v * 8, f);
+      }
+    }
+  }
+};
+
 // ---- segments in turn ----
 // Work items are (segment, channel tile), all tiles of a segment before the next segment's, and a CTA
 // takes the next one from a counter when it is free.  An item waits for its tile's item of the

@@ -123,7 +123,13 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       }
     }
   };
+  // B and C come ahead too where they come in whole vectors
+  const bool vectors = a.wide_bc && a.N == NP;
+  const T* bp = (const T*)a.b.p + b * a.b.sb + q.g * a.b.sh;
+  const T* cp = (const T*)a.c.p + b * a.c.sb + q.g * a.c.sh;
+  RowLoads<T, NP, kTile, 2, kThreads> bc;
   fetch(first);
+  if (vectors) bc.load(bp, a.b.st, cp, a.c.st, first, last, tid);
   __syncthreads();
   for (int t0 = first; t0 < last; t0 += kTile) {
     const TileLoads<T, ITEMS> now = next;
@@ -134,7 +140,12 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       if (item < kTile * VECS)
         stage_delta<T>(a, now.x[m], now.dt[m], sbias + cv, t0 + t < last, q.n - cv, sd + item * kPairUnit);
     }
-    stage_bc<T, NP, kTile>(a, b, q.g, t0, last, &sbc[0][0], tid, kThreads);
+    if (vectors) {
+      bc.store(&sbc[0][0], tid);
+      bc.load(bp, a.b.st, cp, a.c.st, t0 + kTile, last, tid);
+    } else {
+      stage_bc<T, NP, kTile>(a, b, q.g, t0, last, &sbc[0][0], tid, kThreads);
+    }
     if (t0 + kTile < last) fetch(t0 + kTile);
     if (GATE) {
 #pragma unroll
@@ -305,7 +316,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_segment_kernel(ScanArgs 
     }
   };
   auto origin = [&](int i) { return first + (REVERSE ? count - 1 - i : i) * kTile; };
+  const bool vectors = a.wide_bc && a.N == NP;
+  RowLoads<T, NP, kTile, 1, kThreads> rows;
   fetch(origin(0));
+  if (vectors) rows.load(vp, vr.st, nullptr, 0, origin(0), last, tid);
   __syncthreads();
   for (int i = 0; i < count; ++i) {
     const int t0 = origin(i);
@@ -332,9 +346,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_segment_kernel(ScanArgs 
         }
       }
     }
-    for (int e = tid; e < kTile * NP; e += kThreads) {
-      const int t = t0 + e / NP, n = e % NP;
-      sv[e / NP][n] = t < last && n < a.N ? to_f32(vp[t * vr.st + n]) : 0.f;
+    if (vectors) {
+      rows.store(&sv[0][0], tid);
+      if (i + 1 < count) rows.load(vp, vr.st, nullptr, 0, origin(i + 1), last, tid);
+    } else {
+      for (int e = tid; e < kTile * NP; e += kThreads) {
+        const int t = t0 + e / NP, n = e % NP;
+        sv[e / NP][n] = t < last && n < a.N ? to_f32(vp[t * vr.st + n]) : 0.f;
+      }
     }
     if (i + 1 < count) fetch(origin(i + 1));
     __syncthreads();
