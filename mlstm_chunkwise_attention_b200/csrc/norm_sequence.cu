@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
       const float2 ms = reinterpret_cast<const float2*>(a.stats)[q.group], r = result[i & 1];
       const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
       const float2 n1 = make_float2(-r.x, -r.x), n2 = make_float2(-r.y, -r.y);
-      float2 wt[4], bias[4], s1 = make_float2(0.f, 0.f), s2 = s1, dw[4], db[4];
+      float2 wt[4], bias[4], dw[4], db[4];
       load_affine<WIDE>(a, q.head * a.d + q.c0 + lane * 8, n, wt, bias);
 #pragma unroll
       for (int k = 0; k < 4; ++k) dw[k] = db[k] = make_float2(0.f, 0.f);
@@ -438,9 +438,7 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
             // -- backward, first reading.  Absent channels have dy = 0 and so add nothing.
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 dn = mul2(g[k], GATED ? f[k] : slope[k]), h = mul2(dn, wt[k]);
-              s1 = add2(s1, h);
-              s2 = fma2(h, v[k], s2);
+              const float2 dn = mul2(g[k], GATED ? f[k] : slope[k]);
               dw[k] = fma2(dn, v[k], dw[k]);
               db[k] = add2(db[k], dn);
             }
@@ -463,6 +461,13 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
       copies_wait<0>();
       begin(behind);
       if (!q.output) {
+        // the sums of dn w and dn w xhat are those of dn and dn xhat, each channel's times its weight
+        float2 s1 = mul2(wt[0], db[0]), s2 = mul2(wt[0], dw[0]);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) {
+          s1 = fma2(wt[k], db[k], s1);
+          s2 = fma2(wt[k], dw[k], s2);
+        }
         const float w1 = warp_sum(s1.x + s1.y), w2 = warp_sum(s2.x + s2.y);
         if ((tid & 31) == 0) {
           red[i & 1][warp][0] = w1;
