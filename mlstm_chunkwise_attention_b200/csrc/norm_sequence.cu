@@ -289,28 +289,40 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
 
   // ---- the eight warps ---------------------------------------------------------------------
   const int row = tid / p.lanes, lane = tid % p.lanes;
-  // All tokens of an item, a commit group each.
-  auto begin = [&](const Item& q) {
-    if (q.output < 0) return;
-    const int n = min(8, a.d - q.c0 - lane * 8), end = q.group >= 0 && n > 0 ? q.t1 : 0;
-    const T* x = q.template at<const T>(a.x, row, lane);
-    const T* dy = BWD ? q.template at<const T>(a.y, row, lane) : nullptr;
-    const T* gate = GATED ? q.template at<const T>(a.gate, row, lane) : nullptr;
-    const long long sx = p.rows * a.x.st, sy = p.rows * a.y.st, sg = p.rows * a.gate.st;
-    int t = q.t0 + row;
-#pragma unroll
-    for (int u = 0; u < EACH; ++u) {
-      if (t < end) {
-        fetch_raw<WIDE>(&slots[u][0][tid], x, n);
-        if (BWD) fetch_raw<WIDE>(&slots[u][BWD][tid], dy, n);
-        if (GATED && (BWD || q.output)) fetch_raw<WIDE>(&slots[u][TENSORS - 1][tid], gate, n);
-      }
-      copies_commit();
-      t += p.rows;
-      x += sx;
-      if (BWD) dy += sy;
-      if (GATED) gate += sg;
+  // The tokens of an item on their way, a commit group each.  A slot is filled for the next item as soon
+  // as this one's token has been taken from it, so the loads go on through the sums and the barrier.
+  const T *x = nullptr, *dy = nullptr, *gate = nullptr;
+  const long long sx = p.rows * a.x.st, sy = p.rows * a.y.st, sg = p.rows * a.gate.st;
+  int ahead = 0, until = 0, width = 0;
+  bool with_gate = false;
+  auto aim = [&](const Item& q) {
+    until = 0;
+    if (q.output < 0 || q.group < 0) return;
+    width = min(8, a.d - q.c0 - lane * 8);
+    if (width <= 0) return;
+    until = q.t1;
+    ahead = q.t0 + row;
+    with_gate = GATED && (BWD || q.output);
+    x = q.template at<const T>(a.x, row, lane);
+    if (BWD) dy = q.template at<const T>(a.y, row, lane);
+    if (GATED) gate = q.template at<const T>(a.gate, row, lane);
+  };
+  auto fetch = [&](int u) {
+    if (ahead < until) {
+      fetch_raw<WIDE>(&slots[u][0][tid], x, width);
+      if (BWD) fetch_raw<WIDE>(&slots[u][BWD][tid], dy, width);
+      if (with_gate) fetch_raw<WIDE>(&slots[u][TENSORS - 1][tid], gate, width);
     }
+    copies_commit();
+    ahead += p.rows;
+    x += sx;
+    if (BWD) dy += sy;
+    if (GATED) gate += sg;
+  };
+  auto begin = [&](const Item& q) {
+    aim(q);
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) fetch(u);
   };
   named_barrier(0, ALL);
   begin(items[0]);
@@ -333,6 +345,7 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
     const int n = max(0, min(8, a.d - q.c0 - lane * 8));
     const int end = n > 0 ? q.t1 : 0;  // threads without channels have no tokens
     int t = q.t0 + row;
+    aim(behind);
     if (!BWD && !q.output) {
       // -- forward, first reading: a warp sums its distances from the mean of one of its vectors.  Were
       // that vector far from the rest, its own distances would make m2 as large: m2 loses at most a
@@ -342,10 +355,10 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
       int tokens = 0;
 #pragma unroll
       for (int u = 0; u < EACH; ++u) {
-        copies_wait<EACH - 1>();
-        copies_commit();  // keeps EACH groups behind this token's, so that the count above is right
+        copies_wait<EACH - 1>();  // the oldest of EACH groups
         float2 v[4];
         if (t < end) expand(slots[u][0][tid], v);
+        fetch(u);
         if (u == 0) {
           float m = 0.f;
           if (t < end) {
@@ -368,8 +381,6 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
         }
         t += p.rows;
       }
-      copies_wait<0>();
-      begin(behind);
       const float cnt = (float)__reduce_add_sync(0xffffffffu, tokens * n);
       const float sum = warp_sum(s.x + s.y), sq = warp_sum(e.x + e.y);
       if ((tid & 31) == 0) {
@@ -388,11 +399,13 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
 #pragma unroll
       for (int u = 0; u < EACH; ++u) {
         copies_wait<EACH - 1>();
-        copies_commit();
+        float2 v[4], g[4];
         if (t < end) {
-          float2 v[4], g[4];
           expand(slots[u][0][tid], v);
           if (GATED) expand(slots[u][TENSORS - 1][tid], g);
+        }
+        fetch(u);
+        if (t < end) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = fma2(mul2(add2(v[k], neg), rs), wt[k], bias[k]);
           if (GATED) {
@@ -407,7 +420,6 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
         t += p.rows;
         y += p.rows * a.y.st;
       }
-      begin(behind);
     } else {
       const float2 ms = reinterpret_cast<const float2*>(a.stats)[q.group], r = result[i & 1];
       const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
@@ -421,12 +433,14 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
 #pragma unroll 2
       for (int u = 0; u < EACH; ++u) {
         copies_wait<EACH - 1>();
-        copies_commit();
+        float2 v[4], g[4], f[4], slope[4], nn[4];  // f: the activation's argument, then its value
         if (t < end) {
-          float2 v[4], g[4], f[4], slope[4], nn[4];  // f: the activation's argument, then its value
           expand(slots[u][0][tid], v);
           expand(slots[u][BWD][tid], g);
           if (GATED) expand(slots[u][TENSORS - 1][tid], f);
+        }
+        fetch(u);
+        if (t < end) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             v[k] = mul2(add2(v[k], neg), rs);
@@ -458,8 +472,6 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
         dx += p.rows * a.dx.st;
         if (GATED) dgate += p.rows * a.dgate.st;
       }
-      copies_wait<0>();
-      begin(behind);
       if (!q.output) {
         // the sums of dn w and dn w xhat are those of dn and dn xhat, each channel's times its weight
         float2 s1 = mul2(wt[0], db[0]), s2 = mul2(wt[0], dw[0]);
