@@ -317,8 +317,9 @@ int mlstm_dstate_chain(const void* dstate_local, const void* dstate_out, const v
 
 
 /* Synchronise `stream` and report what the kernels of this device found:
- * MLSTM_ERR_TIMEOUT if a tensor-core kernel launched on the current device
- * gave up a bounded wait (2 s) since the previous mlstm_device_status call on
+ * MLSTM_ERR_TIMEOUT if a tensor-core kernel, or a kernel of mlstm_block.h
+ * whose CTAs wait for one another, launched on the current device gave up a
+ * bounded wait (2 s) since the previous mlstm_device_status call on
  * that device (the outputs of that launch are invalid), MLSTM_ERR_CUDA on a
  * CUDA error, else MLSTM_OK.  Each failure is reported once.  A failure stays
  * within its own launch: each launch carries its own abort epoch, so the

@@ -11,7 +11,12 @@
  * failed launch is MLSTM_ERR_CUDA.  The calls run on the current device, may
  * be captured into graphs, and may run at the same time on several streams if
  * each has its own workspace.  Results do not depend on scheduling: sums over
- * tokens, channels and batches are taken in a fixed order without atomics.
+ * tokens, channels and batches are taken in a fixed order, and atomics only
+ * hand out work.  Some kernels wait, bounded, for another CTA's part of the
+ * same launch; a wait that was given up is reported by mlstm_device_status.
+ *
+ * Sizes.  B T < 2^30, NH d <= 2^24, B NH d < 2^31, B T NH d < 2^40, and what the
+ * operators say; other values return MLSTM_ERR_UNSUPPORTED.
  *
  * Types.  Activations and their gradients are in the one I/O dtype
  * (MLSTM_BF16 or MLSTM_FP32); parameters, their gradients and the scan's

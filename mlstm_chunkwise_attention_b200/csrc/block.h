@@ -113,6 +113,8 @@ size_t norm_workspace(int B, int T, int NH, int d, int scope, int dtype, bool ba
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s);
 // the sequence scope's part (norm_sequence.cu)
+// items of its queue, which must stay below 2^31
+long long norm_sequence_items(int B, int T, int NH, int d);
 size_t norm_sequence_workspace(int B, int T, int NH, int d, int dtype, bool backward);
 cudaError_t launch_norm_sequence(const NormArgs& a, bool backward, cudaStream_t s);
 cudaError_t fetch_norm_error(unsigned int* flag);

@@ -45,21 +45,22 @@ int check_common(int B, int T, int dtype) {
   if ((long long)B * T >= (1LL << 30)) return MLSTM_ERR_UNSUPPORTED;
   return MLSTM_OK;
 }
-int check_channels(int B, int NH, int d) {
+int check_channels(int B, int T, int NH, int d) {
   if (NH <= 0 || d <= 0) return MLSTM_ERR_INVALID;
-  if ((long long)NH * d > (1 << 24) || (long long)B * NH * d >= (1LL << 31)) return MLSTM_ERR_UNSUPPORTED;
+  const long long D = (long long)NH * d;
+  if (D > (1 << 24) || B * D >= (1LL << 31) || B * D * T >= (1LL << 40)) return MLSTM_ERR_UNSUPPORTED;
   return MLSTM_OK;
 }
 int check_conv(int B, int T, int NH, int d, int W, int dtype) {
   int st = check_common(B, T, dtype);
-  if (st == MLSTM_OK) st = check_channels(B, NH, d);
+  if (st == MLSTM_OK) st = check_channels(B, T, NH, d);
   if (st != MLSTM_OK) return st;
   if (W <= 0) return MLSTM_ERR_INVALID;
   return W >= 2 && W <= 4 ? MLSTM_OK : MLSTM_ERR_UNSUPPORTED;
 }
 int check_scan(int B, int T, int D, int G, int N, int dtype) {
   int st = check_common(B, T, dtype);
-  if (st == MLSTM_OK) st = check_channels(B, 1, D);
+  if (st == MLSTM_OK) st = check_channels(B, T, 1, D);
   if (st != MLSTM_OK) return st;
   if (G <= 0 || N <= 0 || D % G != 0) return MLSTM_ERR_INVALID;
   if (N > 64 || (long long)B * T * G >= (1LL << 31)) return MLSTM_ERR_UNSUPPORTED;
@@ -67,10 +68,14 @@ int check_scan(int B, int T, int D, int G, int N, int dtype) {
 }
 int check_norm(int B, int T, int NH, int d, int scope, int dtype) {
   int st = check_common(B, T, dtype);
-  if (st == MLSTM_OK) st = check_channels(B, NH, d);
+  if (st == MLSTM_OK) st = check_channels(B, T, NH, d);
   if (st != MLSTM_OK) return st;
   if (scope != MLSTM_SCOPE_TOKEN && scope != MLSTM_SCOPE_SEQUENCE) return MLSTM_ERR_INVALID;
-  return scope == MLSTM_SCOPE_TOKEN && d > 512 ? MLSTM_ERR_UNSUPPORTED : MLSTM_OK;
+  if (scope == MLSTM_SCOPE_TOKEN) return d > 512 ? MLSTM_ERR_UNSUPPORTED : MLSTM_OK;
+  if ((long long)B * T == 0) return MLSTM_OK;
+  return (long long)B * NH >= (1 << 28) || mlstm::norm_sequence_items(B, T, NH, d) >= (1LL << 31)
+             ? MLSTM_ERR_UNSUPPORTED
+             : MLSTM_OK;
 }
 
 int pending_error(const char* where) { return cuda_result(cudaPeekAtLastError(), where); }

@@ -547,6 +547,15 @@ cudaError_t by_kind(const NormArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+long long norm_sequence_items(int B, int T, int NH, int d) {
+  long long most = 0;
+  for (int kind = 0; kind < 8; ++kind) {
+    const Plan p = plan_for(B, T, NH, d, kind & 1 ? 2 : 4, (kind & 2) != 0, (kind & 4) != 0);
+    if (p.items() > most) most = p.items();
+  }
+  return most;
+}
+
 size_t norm_sequence_workspace(int B, int T, int NH, int d, int dtype, bool backward) {
   size_t most = 0;  // with a gate or without
   for (int gated = 0; gated < 2; ++gated) {

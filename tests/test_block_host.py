@@ -208,6 +208,7 @@ def norm_fwd(lib, x=rows(), w=None, bias=None, gate=None, y=rows(), stats=None, 
     (dict(Bn=-1), 1), (dict(NH=0), 1), (dict(d=0), 1), (dict(scope=2), 1), (dict(act=3), 1),
     (dict(eps=0.0), 1), (dict(eps=float("nan")), 1), (dict(dtype=9), 1), (dict(d=513), 2),
     (dict(x=rows(None)), 1), (dict(y=rows(None)), 1), (dict(gate=rows(FAKE + 1)), 1),
+    (dict(Bn=1 << 14, T=1 << 14, NH=1 << 6, d=1 << 8), 2), (dict(Bn=1 << 14, NH=1 << 14, d=1, scope=1), 2),
     (dict(w=FAKE + 1), 1), (dict(stats=FAKE + 4), 1), (dict(scope=1), 3), (dict(scope=1, ws=FAKE, nbytes=4), 3),
     (dict(Bn=0), 0), (dict(T=0), 0),
 ])
