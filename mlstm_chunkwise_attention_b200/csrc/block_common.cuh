@@ -158,28 +158,38 @@ __device__ __forceinline__ void store_pairs(float* p, const float2* v, int n) {
   }
 }
 
-// A copy of 8 or 16 bytes into shared memory that completes in the background.
+// A copy of 4, 8 or 16 bytes into shared memory that completes in the background.
 template <int BYTES = 16>
 __device__ __forceinline__ void copy_async(void* smem, const void* gmem) {
   const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
   if (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(gmem) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(gmem) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(gmem), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
 __device__ __forceinline__ void copies_wait() {  // all but the newest LEFT groups are done
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
-// Brings a thread's channels into its own slot of shared memory, in the background where the
-// accesses are wide.  The thread reads them after its own wait; no barrier is needed.
+// Brings a thread's channels into its own slot of shared memory, in the background unless they are
+// single bf16 values (there is no such copy of two bytes).  The thread reads them after its own
+// wait; no barrier is needed.
 template <bool WIDE, typename T, int C>
 __device__ __forceinline__ void fetch_raw(Raw<T, C>* to, const T* from, int n) {
   if (WIDE) {
     constexpr int size = (int)sizeof(Raw<T, C>), piece = size < 16 ? 8 : 16;
 #pragma unroll
     for (int i = 0; i < size; i += piece) copy_async<piece>((char*)to + i, (const char*)from + i);
+  } else if (sizeof(T) == 4) {
+    float* slot = reinterpret_cast<float*>(to);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      if (i < n)
+        copy_async<4>(slot + i, from + i);
+      else
+        slot[i] = 0.f;
+    }
   } else {
     Raw<T, C> r;
     load_raw<false>(from, r, n);

@@ -92,6 +92,25 @@ __device__ __forceinline__ void conv_token(const float2 (*w)[kPairs], const floa
 template <typename T> constexpr int kRing = sizeof(T) == 2 ? 16 : 8;
 constexpr int kBatch = 4;
 
+// A batch of tokens into slots that lie `apart` from each other; `left` tokens exist.
+template <bool WIDE, typename T>
+__device__ __forceinline__ void fetch_batch(Raw<T, kC>* to, int apart, const T* from, long long step, int n,
+                                            int left) {
+  if (WIDE || sizeof(T) == 4) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (u < left) fetch_raw<WIDE>(to + u * apart, from + u * step, n);
+  } else {  // all loads before the first store, which might be to where they read from
+    Raw<T, kC> r[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (u < left) load_raw<false>(from + u * step, r[u], n);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (u < left) to[u * apart] = r[u];
+  }
+}
+
 template <typename T, int W, int ACT, bool WIDE>
 __global__ void __launch_bounds__(128, 7) conv_fwd_kernel(ConvArgs a, int run, int runs, int vecs) {
   constexpr int RING = kRing<T>;
@@ -110,12 +129,9 @@ __global__ void __launch_bounds__(128, 7) conv_fwd_kernel(ConvArgs a, int run, i
   const T* src = x + t0 * a.x.st;  // of the next token to fetch
   int ahead = t0;
   auto fetch = [&](int slot) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (ahead < t1) fetch_raw<WIDE>(&ring[slot + u][threadIdx.x], src, n);
-      src += a.x.st;
-      ++ahead;
-    }
+    fetch_batch<WIDE>(&ring[slot][threadIdx.x], 128, src, a.x.st, n, t1 - ahead);
+    src += kBatch * a.x.st;
+    ahead += kBatch;
     copies_commit();
   };
 #pragma unroll
@@ -170,9 +186,18 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, int vecs) {
   for (int j = 0; j < W - 1; ++j) store_pairs<WIDE, kC>(so + (long long)j * D, win[j], n);
 }
 
-constexpr int kBwdRun = 64;    // tokens of one thread's run
 constexpr int kBwdLanes = 32;  // channel vectors of a CTA
 constexpr int kBwdRuns = 4;    // runs of a CTA, joined in shared memory
+
+// Tokens of one thread's run: 64 (3 of 67 loads are the halo), fewer while that leaves under two CTAs
+// an SM.
+int bwd_run(int B, int T, int D) {
+  const long long cblocks = (D + kC * kBwdLanes - 1) / (kC * kBwdLanes);
+  int run = 64;
+  while (run > 8 && cblocks * (((long long)B * ((T + run - 1) / run) + kBwdRuns - 1) / kBwdRuns) < 2 * 148)
+    run /= 2;
+  return run;
+}
 
 // One thread's walk through its run: windows of W inputs and W values of dp, sums for the taps.
 template <typename T, int W, int ACT, bool WIDE>
@@ -256,31 +281,35 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns, 4) conv_bwd_kernel(ConvA
     load_taps<W, WIDE>(a, c0, n, k.w, k.bias);
     const int end = min(t1 + W - 1, a.T);  // tokens read: dx of t1 - 1 is complete at t1 + W - 2
     const T *sx = x + t0 * a.x.st, *sg = dy + t0 * a.y.st + off;
+    long long place[kC];  // of each channel in a row of dy, where they are taken one by one
+    if (!WIDE)
+#pragma unroll
+      for (int i = 0; i < kC; ++i) place[i] = ((c0 + i) / a.d) * a.y.sh + (c0 + i) % a.d;
     int ahead = t0;
     auto fetch = [&](int slot) {
+      fetch_batch<WIDE>(&ring[0][slot][tid], kBwdLanes * kBwdRuns, sx, a.x.st, n, end - ahead);
+      if (WIDE) {
+        fetch_batch<true>(&ring[1][slot][tid], kBwdLanes * kBwdRuns, sg, a.y.st, n, end - ahead);
+      } else {  // the channels may lie in several heads
+        float2 v[kBatch][kPairs];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (ahead < end) {
-          fetch_raw<WIDE>(&ring[0][slot + u][tid], sx, n);
-          if (WIDE) {
-            fetch_raw<true>(&ring[1][slot + u][tid], sg, n);
-          } else {  // the channels may lie in several heads
-            float2 v[kPairs];
+        for (int u = 0; u < kBatch; ++u) {
+          if (ahead + u < end) {
+            const T* row = sg - off + u * a.y.st;
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) {
-              const int c = c0 + 2 * p;
-              const T* row = sg - off;
-              v[p].x = 2 * p < n ? to_f32(row[(c / a.d) * a.y.sh + c % a.d]) : 0.f;
-              v[p].y = 2 * p + 1 < n ? to_f32(row[((c + 1) / a.d) * a.y.sh + (c + 1) % a.d]) : 0.f;
+              v[u][p].x = 2 * p < n ? to_f32(row[place[2 * p]]) : 0.f;
+              v[u][p].y = 2 * p + 1 < n ? to_f32(row[place[2 * p + 1]]) : 0.f;
             }
-            // exact: the values come from T
-            store_pairs<true, kC>(reinterpret_cast<T*>(&ring[1][slot + u][tid]), v, kC);
           }
         }
-        sx += a.x.st;
-        sg += a.y.st;
-        ++ahead;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)  // exact: the values come from T
+          if (ahead + u < end) store_pairs<true, kC>(reinterpret_cast<T*>(&ring[1][slot + u][tid]), v[u], kC);
       }
+      sx += kBatch * a.x.st;
+      sg += kBatch * a.y.st;
+      ahead += kBatch;
       copies_commit();
     };
 #pragma unroll
@@ -388,8 +417,6 @@ __global__ void __launch_bounds__(1024) param_sums_kernel(const float* __restric
   }
 }
 
-int bwd_runs(int T) { return (T + kBwdRun - 1) / kBwdRun; }
-
 template <typename T, int W, int ACT, bool WIDE>
 cudaError_t fwd(const ConvArgs& a, cudaStream_t s) {
   const int vecs = (a.D() + kC - 1) / kC;
@@ -414,10 +441,10 @@ cudaError_t step(const ConvArgs& a, cudaStream_t s) {
 template <typename T, int W, int ACT, bool WIDE>
 cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
   const int D = a.D(), vecs = (D + kC - 1) / kC, cblocks = (vecs + kBwdLanes - 1) / kBwdLanes;
-  const int rows = conv_bwd_rows(a.B, a.T, D);
+  const int rows = conv_bwd_rows(a.B, a.T, D), run = bwd_run(a.B, a.T, D);
   conv_bwd_kernel<T, W, ACT, WIDE>
       <<<(unsigned)((long long)rows * cblocks), dim3(kBwdLanes, kBwdRuns), 0, s>>>(
-          a, kBwdRun, bwd_runs(a.T), vecs, cblocks);
+          a, run, (a.T + run - 1) / run, vecs, cblocks);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_param_sums(a.partial, rows, D, W, a.dw, a.dbias, s);
@@ -450,8 +477,9 @@ cudaError_t by_type(const ConvArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int conv_bwd_rows(int B, int T, int) {
-  return (int)(((long long)B * bwd_runs(T) + kBwdRuns - 1) / kBwdRuns);
+int conv_bwd_rows(int B, int T, int D) {
+  const int run = bwd_run(B, T, D);
+  return (int)(((long long)B * ((T + run - 1) / run) + kBwdRuns - 1) / kBwdRuns);
 }
 
 cudaError_t launch_param_sums(const float* partial, int rows, int D, int W, float* dw, float* dbias,

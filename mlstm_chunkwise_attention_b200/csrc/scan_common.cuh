@@ -161,13 +161,24 @@ __device__ __forceinline__ void stage_bc(const ScanArgs& a, int b, int g, int t0
       }
     }
   } else {
-    for (int e = tid; e < TT * 2 * NP; e += threads) {
-      const int t = e / (2 * NP), r = e % (2 * NP), n = r % NP;
-      float v = 0.f;
-      if (t0 + t < last && n < a.N)
-        v = r >= NP ? to_f32(cp[(t0 + t) * a.c.st + n]) : to_f32(bp[(t0 + t) * a.b.st + n]);
+    // eight loads before their stores, which the compiler must take to be where the loads read
+    constexpr int BATCH = 8;
+    for (int e0 = tid; e0 < TT * 2 * NP; e0 += BATCH * threads) {
+      float v[BATCH];
 #pragma unroll
-      for (int p = 0; p < COPIES; ++p) out[p * STRIDE + (e ^ p)] = v;
+      for (int i = 0; i < BATCH; ++i) {
+        const int e = e0 + i * threads, t = e / (2 * NP), r = e % (2 * NP), n = r % NP;
+        v[i] = 0.f;
+        if (e < TT * 2 * NP && t0 + t < last && n < a.N)
+          v[i] = r >= NP ? to_f32(cp[(t0 + t) * a.c.st + n]) : to_f32(bp[(t0 + t) * a.b.st + n]);
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int e = e0 + i * threads;
+        if (e < TT * 2 * NP)
+#pragma unroll
+          for (int p = 0; p < COPIES; ++p) out[p * STRIDE + (e ^ p)] = v[i];
+      }
     }
   }
 }

@@ -350,9 +350,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_segment_kernel(ScanArgs 
       rows.store(&sv[0][0], tid);
       if (i + 1 < count) rows.load(vp, vr.st, nullptr, 0, origin(i + 1), last, tid);
     } else {
-      for (int e = tid; e < kTile * NP; e += kThreads) {
-        const int t = t0 + e / NP, n = e % NP;
-        sv[e / NP][n] = t < last && n < a.N ? to_f32(vp[t * vr.st + n]) : 0.f;
+      for (int e0 = tid; e0 < kTile * NP; e0 += 8 * kThreads) {  // eight loads before their stores
+        float v[8];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          const int e = e0 + m * kThreads, t = t0 + e / NP, n = e % NP;
+          v[m] = e < kTile * NP && t < last && n < a.N ? to_f32(vp[t * vr.st + n]) : 0.f;
+        }
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          const int e = e0 + m * kThreads;
+          if (e < kTile * NP) sv[e / NP][e % NP] = v[m];
+        }
       }
     }
     if (i + 1 < count) fetch(origin(i + 1));
@@ -510,7 +519,7 @@ cudaError_t by_type(const ScanArgs& a, cudaStream_t s) {
 }  // namespace
 
 ScanSegments scan_cut(int T, long long ctas, int slots) {
-  constexpr int most = 256, least = 4 * kTile;  // tokens of a segment in turn / at once, at least
+  constexpr int most = 256, least = 2 * kTile;  // tokens of a segment in turn / at once, at least
   ScanSegments z = {T, 1, false, (int)ctas};
   long long segs = 1;
   if (ctas > slots) {

@@ -139,8 +139,8 @@ SCAN = [
     (2, 130, 136, 16, 1, True, True, True, True, False, BF, False),  # ragged channel tiles
     (1, 65, 48, 32, 2, True, True, False, True, True, F32, False),
     (1, 70, 20, 64, 1, False, True, True, False, True, F32, False),
-    (1, 1111, 24, 16, 1, True, True, True, True, True, F32, False),  # eight segments, the last ragged
-    (2, 530, 40, 6, 2, True, True, True, True, True, BF, False),     # four segments
+    (1, 1111, 24, 16, 1, True, True, True, True, True, F32, False),  # many segments, the last ragged
+    (2, 530, 40, 6, 2, True, True, True, True, True, BF, False),     # several segments
     (2, 600, 256, 16, 256, False, True, True, True, True, F32, False),  # many tiles: segments in turn
     (5, 530, 256, 4, 256, True, False, True, True, True, BF, False),    # in turn in both directions
     (2, 64, 64, 20, 64, True, True, True, True, True, F32, False),   # a group per channel
