@@ -260,6 +260,8 @@ NORM = [
     (1, 50, 2, 2056, "sequence", "none", False, True, F32, False, False),  # two channel blocks
     (2, 70, 3, 40, "sequence", "sigmoid", True, False, BF, True, False),
     (1, 3000, 1, 8, "sequence", "silu", True, True, F32, True, False),
+    (8, 256, 128, 32, "sequence", "silu", False, True, BF, False, False),  # several chunks of groups
+    (4, 200, 64, 64, "sequence", "sigmoid", True, True, F32, True, False),
 ]
 
 
@@ -408,6 +410,89 @@ def test_captured_calls_replay_on_new_inputs():
     torch.cuda.synchronize()
     for a, b in zip(outs, want):
         same(a, b)
+
+
+def in_turn_inputs(seed):
+    """Many channel tiles and several segments: both directions of the scan take work in turn."""
+    case = (5, 530, 256, 4, 256, True, False, True, True, True, BF, False)
+    g = torch.Generator().manual_seed(seed)
+    c = scan_case(*case)
+    for name in ("x", "z", "dy"):
+        c[name] = rand(g, *c[name].shape, dtype=BF)
+    return scan_dev(c)
+
+
+def run_in_turn(t, stream=None):
+    kw = dict(**scan_kw(t, True), stream=stream)
+    y, saved, end = block.selective_scan_forward(*scan_args(t), **kw, want_state=True)
+    got = block.selective_scan_backward(*scan_args(t), t["dy"], saved, **kw, dstate_out=t["dso"],
+                                        want_dstate=True)
+    return {"y": y, "end": end, **{k: v for k, v in got.items() if v is not None}}
+
+
+def test_scans_in_turn_at_once_and_replayed():
+    """CTAs that wait for one another within a launch: two such launches at once, and a graph of one
+    replayed (its counters start again from zero each time)."""
+    t = [in_turn_inputs(s) for s in (1, 2)]
+    want = [run_in_turn(v) for v in t]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in t]
+    got = [[run_in_turn(v, s) for v, s in zip(t, streams)] for _ in range(3)]
+    torch.cuda.synchronize()
+    for rep in got:
+        for a, b in zip(rep, want):
+            same(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run_in_turn(t[0])
+    for k in t[0]:
+        if t[0][k] is not None:
+            t[0][k].copy_(t[1][k])
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        same(out, want[1])
+    binding.check_device()
+
+
+def test_offsets_beyond_32_bits():
+    """Tensors of more than 2^31 elements: the last tokens are those of a call that starts there."""
+    T, T0, D, NH = 280000, 279900, 8192, 64
+    x = torch.empty(1, T, D, dtype=BF, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    assert x.numel() > 2 ** 31
+    w, b = torch.randn(D, 4, device="cuda"), torch.randn(D, device="cuda")
+    y, end = block.causal_conv_forward(x, w, b, want_state=True)
+    _, st = block.causal_conv_forward(x[:, T0 - 3:T0], w, b, want_state=True)
+    tail, end2 = block.causal_conv_forward(x[:, T0:], w, b, state_in=st, want_state=True)
+    assert torch.equal(y[:, T0:], tail) and torch.equal(end, end2)
+    got = block.causal_conv_backward(x, w, b, x)
+    part = block.causal_conv_backward(x[:, T0:], w, b, x[:, T0:], state_in=st)
+    assert torch.equal(got["dx"][:, T0:], part["dx"])
+    del got, part
+    for act in (block.ACT_NONE, block.ACT_SILU):
+        y, stats = block.group_norm_forward(x, b, b, groups=NH, act=act)
+        part, stats2 = block.group_norm_forward(x[:, T0:], b, b, groups=NH, act=act)
+        assert torch.equal(y[:, T0:], part) and torch.equal(stats[:, T0:], stats2)
+    got = block.group_norm_backward(x, b, b, x, stats, groups=NH, act=block.ACT_SILU)
+    part = block.group_norm_backward(x[:, T0:], b, b, x[:, T0:], stats2, groups=NH, act=block.ACT_SILU)
+    assert torch.equal(got["dx"][:, T0:], part["dx"])
+    del got, part
+    y, stats = block.group_norm_forward(x, b, b, groups=NH, scope=block.SCOPE_SEQUENCE)
+    mean, rstd = stats[0, :, 0].repeat_interleave(D // NH), stats[0, :, 1].repeat_interleave(D // NH)
+    want = (x[0, T0:].float() - mean) * rstd * b + b
+    assert float((y[0, T0:].float() - want).abs().max()) <= 2.0 ** -8 * float(want.abs().max()) * 1.01
+    del y
+    A, Bm = -torch.ones(D, 1, device="cuda"), torch.ones(1, T, 1, dtype=BF, device="cuda")
+    y, _, end = block.selective_scan_forward(x, x, A, Bm, Bm, keep_saved=False, want_state=True)
+    # a step of softplus(x) on average forgets e^-0.8 a token: 400 tokens before T0 decide the state there
+    _, _, st = block.selective_scan_forward(x[:, T0 - 400:T0], x[:, T0 - 400:T0], A, Bm[:, :400], Bm[:, :400],
+                                            keep_saved=False, want_state=True)
+    tail, _, end2 = block.selective_scan_forward(x[:, T0:], x[:, T0:], A, Bm[:, T0:], Bm[:, T0:], state_in=st,
+                                                 keep_saved=False, want_state=True)
+    # the same operations in other segments: fp32 states to 1e-5 of the largest, outputs to a bf16 step
+    assert float((end - end2).abs().max()) <= 1e-5 * float(end.abs().max())
+    assert float((y[:, T0:].float() - tail.float()).abs().max()) <= 2.0 ** -7 * float(tail.float().abs().max())
+    binding.check_device()
 
 
 def test_a_bad_batch_stays_alone():
