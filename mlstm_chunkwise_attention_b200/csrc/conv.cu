@@ -189,12 +189,12 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, int vecs) {
 constexpr int kBwdLanes = 32;  // channel vectors of a CTA
 constexpr int kBwdRuns = 4;    // runs of a CTA, joined in shared memory
 
-// Tokens of one thread's run: 64 (3 of 67 loads are the halo), fewer while that leaves under two CTAs
-// an SM.
+// Tokens of one thread's run: 256 (a run's first and last batches cost twice the others, and the halo
+// is read twice), fewer while that leaves under eight CTAs an SM, but 8 at least.
 int bwd_run(int B, int T, int D) {
   const long long cblocks = (D + kC * kBwdLanes - 1) / (kC * kBwdLanes);
-  int run = 64;
-  while (run > 8 && cblocks * (((long long)B * ((T + run - 1) / run) + kBwdRuns - 1) / kBwdRuns) < 2 * 148)
+  int run = 256;
+  while (run > 8 && cblocks * (((long long)B * ((T + run - 1) / run) + kBwdRuns - 1) / kBwdRuns) < 8 * 148)
     run /= 2;
   return run;
 }
@@ -420,10 +420,10 @@ __global__ void __launch_bounds__(1024) param_sums_kernel(const float* __restric
 template <typename T, int W, int ACT, bool WIDE>
 cudaError_t fwd(const ConvArgs& a, cudaStream_t s) {
   const int vecs = (a.D() + kC - 1) / kC;
-  // Runs of 64 tokens (3 of 67 loads are the halo), shorter while that leaves under two
-  // thousand warps: few rows then spread over the GPU.
-  int run = 64;
-  while (run > 4 && (long long)vecs * a.B * ((a.T + run - 1) / run) < 65536) run /= 2;
+  // Runs of 256 tokens, shorter while that leaves under eight thousand warps (the GPU holds half of
+  // them): few rows then spread over the GPU.
+  int run = 256;
+  while (run > 4 && (long long)vecs * a.B * ((a.T + run - 1) / run) < 8192 * 32) run /= 2;
   const int runs = (a.T + run - 1) / run;
   const long long items = (long long)vecs * runs * a.B;
   conv_fwd_kernel<T, W, ACT, WIDE><<<(unsigned)((items + 127) / 128), 128, 0, s>>>(a, run, runs, vecs);
