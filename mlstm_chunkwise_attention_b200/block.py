@@ -39,8 +39,11 @@ def _dtype_code(t):
     raise TypeError(f"unsupported dtype {t.dtype}: use bfloat16 or float32")
 
 
-# The checks run on every call, of which a small one takes 15 us: each asks the tensor for as
-# little as it can (get_device() is -1 off the GPU) and leaves the wording to _refuse.
+# The checks run on every call, of which a small one takes 15 us.  So they ask each tensor for as
+# little as they can (get_device() is -1 off the GPU), in line where a call has many tensors, and
+# leave what is not plainly right to _activation and _fp32, and the wording to _refuse.
+_FP32 = torch.float32
+
 
 def _activation(name, t, shape, like):
     """An activation of `like`'s dtype and device, last dimension contiguous, of this shape."""
@@ -51,9 +54,9 @@ def _activation(name, t, shape, like):
 
 def _fp32(name, t, shape, like):
     """A contiguous float32 parameter or state (None passes)."""
-    if t is not None and not (t.shape == shape and t.dtype == torch.float32 and t.is_contiguous()
+    if t is not None and not (t.shape == shape and t.dtype == _FP32 and t.is_contiguous()
                               and t.get_device() == like.get_device()):
-        _refuse(name, t, shape, like, torch.float32, "contiguous")
+        _refuse(name, t, shape, like, _FP32, "contiguous")
 
 
 def _refuse(name, t, shape, like, dtype, layout):
@@ -178,7 +181,9 @@ def causal_conv_forward(x, weight, bias=None, *, act=ACT_SILU, state_in=None, wa
 
     def launch(s):
         y = _like(x) if heads is None else x.new_empty((B, NH, T, d))
-        state_out = x.new_empty((B, W - 1, D)) if want_state else None
+        state_out = None
+        if want_state:
+            state_out = _like(state_in) if state_in is not None else x.new_empty((B, W - 1, D))
         _check(load().mlstm_conv_fwd(_rows(x), weight.data_ptr(), _ptr(bias), _ptr(state_in),
                                      _head_rows(y, "last" if heads is None else "heads", d),
                                      _ptr(state_out), B, T, NH, d, W, act, dt, s), "mlstm_conv_fwd")
@@ -246,36 +251,46 @@ _SCAN_PROBLEM = struct.Struct("@20q4q7i4x")
 
 def _scan_problem(x, dt, A, Bm, Cm, skip, z, dt_bias, softplus, state):
     """mlstm_scan_t of a call on [B, T, D] tensors (or [B, D]: one token)."""
-    shape = x.shape
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
     _activation("x", x, shape, x)
     D = shape[-1]
-    _activation("dt", dt, shape, x)
-    if z is not None:
+    if dt.shape != shape or dt.dtype != dtype or dt.get_device() != dev or not dt.is_contiguous():
+        _activation("dt", dt, shape, x)
+    if z is not None and (z.shape != shape or z.dtype != dtype or z.get_device() != dev
+                          or not z.is_contiguous()):
         _activation("z", z, shape, x)
-    _dims("A", A, 2)
+    if A.dim() != 2:
+        _dims("A", A, 2)
     N = A.shape[1]
     _fp32("A", A, (D, N), x)
-    _fp32("skip", skip, (D,), x)
-    _fp32("dt_bias", dt_bias, (D,), x)
-    G = Bm.shape[-2] if Bm.dim() > len(shape) else 1
-    shape = (*shape[:-1], G, N) if Bm.dim() > len(shape) else (*shape[:-1], N)
-    _activation("B", Bm, shape, x)
-    _activation("C", Cm, shape, x)
-    if G <= 0 or D % G:
-        raise ValueError(f"{G} groups do not divide {D} channels")
-    _fp32("state", state, (x.shape[0], D, N), x)
-    xs, ds, bs, cs = x.stride(), dt.stride(), Bm.stride(), Cm.stride()
+    for name, t in (("skip", skip), ("dt_bias", dt_bias)):
+        if t is not None and (t.shape != (D,) or t.dtype != _FP32 or t.get_device() != dev
+                              or not t.is_contiguous()):
+            _fp32(name, t, (D,), x)
+    G, grouped = 1, Bm.dim() > len(shape)
+    if grouped:
+        G = Bm.shape[-2]
+        if G <= 0 or D % G:
+            raise ValueError(f"{G} groups do not divide {D} channels")
+    per = (*shape[:-1], G, N) if grouped else (*shape[:-1], N)
+    bs, cs = Bm.stride(), Cm.stride()
+    if Bm.shape != per or Bm.dtype != dtype or Bm.get_device() != dev or bs[-1] != 1:
+        _activation("B", Bm, per, x)
+    if Cm.shape != per or Cm.dtype != dtype or Cm.get_device() != dev or cs[-1] != 1:
+        _activation("C", Cm, per, x)
+    _fp32("state", state, (shape[0], D, N), x)
+    xs, ds = x.stride(), dt.stride()
     zp, zs = (0, xs) if z is None else (z.data_ptr(), z.stride())
     if len(xs) == 3:
-        T, xt, dtt, zt, bt, ct = x.shape[1], xs[1], ds[1], zs[1], bs[1], cs[1]
+        T, xt, dtt, zt, bt, ct = shape[1], xs[1], ds[1], zs[1], bs[1], cs[1]
     else:
         T, xt, dtt, zt, bt, ct = 1, 0, 0, 0, 0, 0
-    bg, cg = (bs[-2], cs[-2]) if len(bs) > len(xs) else (0, 0)
+    bg, cg = (bs[-2], cs[-2]) if grouped else (0, 0)
     return ScanProblem.from_buffer_copy(_SCAN_PROBLEM.pack(
         x.data_ptr(), xs[0], xt, 0, dt.data_ptr(), ds[0], dtt, 0, zp, zs[0], zt, 0,
         Bm.data_ptr(), bs[0], bt, bg, Cm.data_ptr(), cs[0], ct, cg, A.data_ptr(),
         0 if skip is None else skip.data_ptr(), 0 if dt_bias is None else dt_bias.data_ptr(),
-        0 if state is None else state.data_ptr(), x.shape[0], T, D, G, N, 1 if softplus else 0,
+        0 if state is None else state.data_ptr(), shape[0], T, D, G, N, 1 if softplus else 0,
         _dtype_code(x)))
 
 
@@ -374,11 +389,15 @@ def _norm_args(x, weight, bias, gate, act, scope, groups):
             raise ValueError(f"{groups} groups do not divide {D} channels")
         NH, d = groups, D // groups
         layout = "last"
+    D, dev = NH * d, x.get_device()
     _activation("x", x, x.shape, x)
-    _fp32("weight", weight, (NH * d,), x)
-    _fp32("bias", bias, (NH * d,), x)
-    if gate is not None:
-        _activation("gate", gate, (B, T, NH * d), x)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None and (t.shape != (D,) or t.dtype != _FP32 or t.get_device() != dev
+                              or not t.is_contiguous()):
+            _fp32(name, t, (D,), x)
+    if gate is not None and (gate.shape != (B, T, D) or gate.dtype != x.dtype
+                             or gate.get_device() != dev or not gate.is_contiguous()):
+        _activation("gate", gate, (B, T, D), x)
     if act not in (ACT_NONE, ACT_SILU, ACT_SIGMOID):
         raise ValueError("act must be ACT_NONE, ACT_SILU or ACT_SIGMOID")
     if scope not in (SCOPE_TOKEN, SCOPE_SEQUENCE):
@@ -406,8 +425,10 @@ def group_norm_forward(x, weight=None, bias=None, *, gate=None, act=ACT_NONE, sc
         y = x.new_empty((B, T, NH * d))
         stats = (x.new_empty(_stats_shape(B, T, NH, scope), dtype=torch.float32) if keep_stats
                  else None)
-        need = load().mlstm_group_norm_workspace_size(B, T, NH, d, scope, dt, 0)
-        ws = _bytes(need, x) if need else None
+        need, ws = 0, None  # a forward per token needs none
+        if scope == SCOPE_SEQUENCE:
+            need = load().mlstm_group_norm_workspace_size(B, T, NH, d, scope, dt, 0)
+            ws = _bytes(need, x) if need else None
         _check(load().mlstm_group_norm_fwd(_head_rows(x, layout, d), _ptr(weight), _ptr(bias),
                                            _head_rows(gate, "last", d), _head_rows(y, "last", d),
                                            _ptr(stats), _ptr(ws), need, B, T, NH, d, scope, act, eps,
