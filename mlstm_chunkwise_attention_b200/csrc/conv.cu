@@ -11,6 +11,10 @@
 // so each input is loaded once per run plus W - 1 tokens of the run before it.
 // Inputs and outputs are addressed by strides: the convolved half of a wider
 // projection is read in place, and y can be written head-major.
+//
+// Measured on one B200 at B8 T4096 D4096 W4 bf16 with SiLU: forward 103 us, 5.2 TB/s or 0.80 of
+// a plain copy; backward with its parameter sums 176 us, 4.6 TB/s or 0.71: there the fp32 pipe
+// (16 multiply-adds and a sigmoid's slope an element) is the next bound.
 #include "block_common.cuh"
 
 namespace mlstm {

@@ -12,6 +12,11 @@
 // states of two channels; sums over a channel's states run along LPC lanes, sums over channels
 // along the others, both as transposing reductions, then over the CTA's warps in shared memory.
 // Each CTA writes its share of dB and dC; a second kernel adds the shares in a fixed order.
+//
+// Measured on one B200 at B8 T4096 D4096 N16 bf16 with a gate: 2.60 ms with its three small kernels
+// (50, 8 and 5 us).  Shared memory hands over 0.64 of what it can, 0.48 of the cycles issue, with 12
+// warps an SM: latency between those two.  With the decays kept in registers (two CTAs an SM) 3.43 ms;
+// without segments in turn the 512 CTAs take two waves of 444.
 #include "internal.h"
 #include "scan_common.cuh"
 
