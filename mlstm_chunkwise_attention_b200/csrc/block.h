@@ -118,5 +118,8 @@ long long norm_sequence_items(int B, int T, int NH, int d);
 size_t norm_sequence_workspace(int B, int T, int NH, int d, int dtype, bool backward);
 cudaError_t launch_norm_sequence(const NormArgs& a, bool backward, cudaStream_t s);
 cudaError_t fetch_norm_error(unsigned int* flag);
+// Groups that fit the shared memory of a cluster (norm_resident.cu); false: norm_sequence.cu takes them.
+bool norm_resident_workspace(int B, int T, int NH, int d, int dtype, bool gated, bool backward, size_t* bytes);
+bool launch_norm_resident(const NormArgs& a, bool backward, cudaStream_t s, cudaError_t* status);
 
 }  // namespace mlstm

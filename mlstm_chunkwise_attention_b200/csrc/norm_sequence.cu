@@ -1,5 +1,5 @@
 // Group norm with statistics over a whole sequence, forward and backward (the formulas are in
-// group_norm.cu).
+// group_norm.cu), for groups too large for a cluster's shared memory (norm_resident.cu).
 //
 // Bound by HBM: the statistics need every value before the first output, so x (in the backward x and
 // dy) is read twice, and a plain second pass reads it from memory again.  Here one persistent kernel
@@ -564,14 +564,17 @@ long long norm_sequence_items(int B, int T, int NH, int d) {
 size_t norm_sequence_workspace(int B, int T, int NH, int d, int dtype, bool backward) {
   size_t most = 0;  // with a gate or without
   for (int gated = 0; gated < 2; ++gated) {
-    const Plan p = plan_for(B, T, NH, d, dtype == 0 ? 2 : 4, gated != 0, backward);
-    const size_t bytes = layout_for(p, B, NH * d, backward).total;
+    size_t bytes;
+    if (!norm_resident_workspace(B, T, NH, d, dtype, gated != 0, backward, &bytes))
+      bytes = layout_for(plan_for(B, T, NH, d, dtype == 0 ? 2 : 4, gated != 0, backward), B, NH * d, backward).total;
     if (bytes > most) most = bytes;
   }
   return most;
 }
 
 cudaError_t launch_norm_sequence(const NormArgs& a, bool backward, cudaStream_t s) {
+  cudaError_t status;
+  if (launch_norm_resident(a, backward, s, &status)) return status;
   if (backward) return a.dtype == 0 ? by_kind<bf16, true>(a, s) : by_kind<float, true>(a, s);
   return a.dtype == 0 ? by_kind<bf16, false>(a, s) : by_kind<float, false>(a, s);
 }

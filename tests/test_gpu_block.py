@@ -306,6 +306,73 @@ def test_norm_against_64_bits(case):
         close(got["dbias"], *(v.flatten() for v in ref["dbias"]), K + B * T, "dbias")
 
 
+# groups too large for the shared memory of a cluster (more than 2048 channels, or long), or nearly so
+NORM_LARGE = [
+    (1, 900, 3, 1000, "sequence", "silu", False, True, BF, False, False),
+    (2, 480, 2, 1021, "sequence", "sigmoid", True, True, F32, True, False),   # element accesses
+    (12, 33, 9, 2050, "sequence", "none", False, True, F32, False, True),     # several chunks of groups
+    (2, 700, 2, 1024, "sequence", "silu", True, False, BF, True, False),
+    (1, 1, 2, 2056, "sequence", "silu", False, True, BF, False, False),       # one token
+    (5, 160, 32, 512, "sequence", "silu", False, True, F32, False, False),    # eight CTAs, two to an SM
+    (1, 400, 2, 512, "sequence", "silu", False, True, F32, True, False),      # alone on their SMs: backward
+    (1, 400, 2, 508, "sequence", "silu", True, True, F32, False, False),      # and forward
+]
+
+
+@pytest.mark.parametrize("case", NORM_LARGE, ids=[f"b{c[0]}t{c[1]}h{c[2]}d{c[3]}" for c in NORM_LARGE])
+def test_norm_of_large_groups_against_64_bits(case):
+    test_norm_against_64_bits(case)
+
+
+def large_group_inputs(seed):
+    case = (3, 40, 5, 2056, "sequence", "silu", True, True, BF, False, False)
+    g = torch.Generator().manual_seed(seed)
+    return {k: dev(rand(g, *v.shape, dtype=v.dtype)) for k, v in norm_case(*case).items()}
+
+
+def run_large_group(t, stream=None):
+    kw = dict(gate=t["gate"], act=block.ACT_SILU, scope=block.SCOPE_SEQUENCE, groups=5, stream=stream)
+    y, stats = block.group_norm_forward(t["x"], t["w"], t["b"], **kw)
+    return {"y": y, **block.group_norm_backward(t["x"], t["w"], t["b"], t["dy"], stats, **kw)}
+
+
+def test_norms_of_large_groups_at_once_and_replayed():
+    """CTAs that wait for one another's sums: two launches at once, and a graph of one replayed."""
+    t = [large_group_inputs(s) for s in (1, 2)]
+    want = [run_large_group(v) for v in t]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in t]
+    got = [[run_large_group(v, s) for v, s in zip(t, streams)] for _ in range(3)]
+    torch.cuda.synchronize()
+    for rep in got:
+        for a, b in zip(rep, want):
+            same(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run_large_group(t[0])
+    for k in t[0]:
+        t[0][k].copy_(t[1][k])
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        same(out, want[1])
+    binding.check_device()
+
+
+@pytest.mark.parametrize("d", [64, 2056])
+def test_norm_with_one_value_far_from_the_rest(d):
+    """The first vector of a group lies 2^12 off: the others' distances keep their bits beside it."""
+    g = torch.Generator().manual_seed(12)
+    B, T, NH = 1, 200, 2
+    x = rand(g, B, T, NH * d)
+    x[:, 0, :8] += 4096.0
+    x[:, :, d:] += 4096.0
+    y, _ = block.group_norm_forward(dev(x), groups=NH, scope=block.SCOPE_SEQUENCE)
+    one, zero = torch.ones(NH, d, dtype=torch.float64), torch.zeros(NH, d, dtype=torch.float64)
+    ref, mag = norm64(d64(x).view(B, T, NH, d), one, zero, None, "none", "sequence", 1e-5)["y"]
+    close(y, ref.reshape(B, T, -1), mag.reshape(B, T, -1), 64 + T + d, "y")
+
+
 @pytest.mark.parametrize("scope", ["token", "sequence"])
 def test_norm_of_values_far_from_zero(scope):
     """A common offset of 4096 leaves the statistics: squares are never subtracted.  fp32 holds the
