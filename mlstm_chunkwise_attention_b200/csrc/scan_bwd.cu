@@ -11,10 +11,11 @@
 // exponentials' pipe has room and 64 registers do not) and walked backwards.  A lane holds four
 // states of two channels; sums over a channel's states run along LPC lanes, sums over channels
 // along the others, both as transposing reductions, then over the CTA's warps in shared memory.
-// Each CTA writes its share of dB and dC; a second kernel adds the shares in a fixed order.
+// Each CTA writes its share of dB, dC and the parameters' gradients; a second kernel adds the shares in
+// a fixed order.
 //
-// Measured on one B200 at B8 T4096 D4096 N16 bf16 with a gate: 2.60 ms with its three small kernels
-// (50, 8 and 5 us).  Shared memory hands over 0.64 of what it can, 0.48 of the cycles issue, with 12
+// Measured on one B200 at B8 T4096 D4096 N16 bf16 with a gate: 2.59 ms and 0.06 for the sums
+// (268 MB of shares of dB and dC).  Shared memory hands over 0.64 of what it can, 0.48 of the cycles issue, with 12
 // warps an SM: latency between those two.  With the decays kept in registers (two CTAs an SM) 3.43 ms;
 // without segments in turn the 512 CTAs take two waves of 444.
 #include "internal.h"
@@ -392,10 +393,33 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
   }
 }
 
-// dB and dC: the sum of the channel tiles' shares.
+// The sums of all shares, in a fixed order.  The first `columns` / 32 blocks add those of dA and, behind
+// them, dskip and ddt_bias over batches and segments, eight threads to a column (one to a column waited
+// for each row of few long sequences in turn); the others those of dB and dC over the channel tiles.
 template <typename T>
-__global__ void __launch_bounds__(256) scan_bc_kernel(ScanArgs a, int tiles, int NP) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(256) scan_sums_kernel(ScanArgs a, int tiles, int NP, int rows, long long columns,
+                                                        unsigned int column_blocks) {
+  __shared__ float red[8][32];
+  if (blockIdx.x < column_blocks) {
+    const long long i = (long long)blockIdx.x * 32 + threadIdx.x % 32, all = (long long)a.D * a.N, j = i - all;
+    const int part = threadIdx.x / 32;
+    const float* from = j < 0 ? a.part_a + i : a.part_d + j;
+    const long long step = j < 0 ? all : 2LL * a.D;
+    float v = 0.f;
+    if (i < columns)
+#pragma unroll 8
+      for (int r = part; r < rows; r += 8) v += from[r * step];
+    red[part][threadIdx.x % 32] = v;
+    __syncthreads();
+    if (part == 0 && i < columns) {
+      float* to = j < 0 ? a.dA + i : j < a.D ? a.dskip : a.ddt_bias;
+#pragma unroll
+      for (int k = 1; k < 8; ++k) v += red[k][threadIdx.x];
+      if (to != nullptr) to[j < 0 ? 0 : j % a.D] = v;
+    }
+    return;
+  }
+  const long long i = (long long)(blockIdx.x - column_blocks) * 256 + threadIdx.x;
   const long long total = (long long)a.B * a.T * a.G * 2 * NP;
   if (i >= total) return;
   const int r = (int)(i % (2 * NP)), n = r % NP;
@@ -409,17 +433,6 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(ScanArgs a, int tiles, int
   const int t = (int)(bt % a.T), b = (int)(bt / a.T);
   const Rows& o = r >= NP ? a.dc : a.db;
   ((T*)o.p)[b * o.sb + t * o.st + g * o.sh + n] = from_f32<T>(v);
-}
-
-// dA: the sum of the batches' and segments' shares.
-__global__ void __launch_bounds__(256) scan_da_kernel(const float* __restrict__ part, float* __restrict__ dA,
-                                                      int rows, long long count) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= count) return;
-  float v = 0.f;
-#pragma unroll 8
-  for (int r = 0; r < rows; ++r) v += part[r * count + i];
-  dA[i] = v;
 }
 
 template <typename T, int LPC, bool GATE, bool WIDE>
@@ -445,13 +458,11 @@ cudaError_t bwd(const ScanArgs& a, cudaStream_t s) {
     e = a.wide ? bwd_kernel<T, LPC, false, true>(a, tiles, s) : bwd_kernel<T, LPC, false, false>(a, tiles, s);
   if (e != cudaSuccess) return e;
   const long long total = (long long)a.B * a.T * a.G * 2 * Cfg<T, LPC>::NP;
-  scan_bc_kernel<T><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, tiles, Cfg<T, LPC>::NP);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long count = (long long)a.D * a.N;
-  scan_da_kernel<<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a.part_a, a.dA, a.B * a.segs, count);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.dskip == nullptr && a.ddt_bias == nullptr) return cudaSuccess;
-  return launch_param_sums(a.part_d, a.B * a.segs, a.D, 1, a.dskip, a.ddt_bias, s);
+  const long long columns = (long long)a.D * (a.N + (a.dskip != nullptr || a.ddt_bias != nullptr ? 2 : 0));
+  const unsigned column_blocks = (unsigned)((columns + 31) / 32);
+  scan_sums_kernel<T><<<column_blocks + (unsigned)((total + 255) / 256), 256, 0, s>>>(
+      a, tiles, Cfg<T, LPC>::NP, a.B * a.segs, columns, column_blocks);
+  return cudaGetLastError();
 }
 
 template <typename T>
