@@ -82,8 +82,9 @@ struct ScanSegments {
 };
 ScanSegments scan_fwd_segments(int B, int T, int D, int G, int N);
 ScanSegments scan_bwd_segments(int B, int T, int D, int G, int N);
-// ctas: those of an undivided scan; slots: CTAs that the GPU holds at once.
-ScanSegments scan_cut(int T, long long ctas, int slots);
+// tile: tokens that segments are multiples of; ctas: those of an undivided scan; slots: CTAs that the GPU
+// holds at once.
+ScanSegments scan_cut(int T, int tile, long long ctas, int slots);
 struct ScanBwdSizes {
   int tiles;                    // channel tiles of one group
   size_t part_bc, part_a, part_d;  // floats

@@ -479,7 +479,7 @@ cudaError_t by_states(const ScanArgs& a, cudaStream_t s) {
 
 ScanSegments scan_bwd_segments(int B, int T, int D, int G, int N) {
   const int CT = kWarps * 2 * 32 * 4 / scan_pad(N);
-  return scan_cut(T, (long long)B * G * ((D / G + CT - 1) / CT), kSlots);
+  return scan_cut(T, kTile, (long long)B * G * ((D / G + CT - 1) / CT), kSlots);
 }
 
 cudaError_t fetch_scan_bwd_error(unsigned int* flag) {

@@ -122,16 +122,33 @@ __device__ __forceinline__ float4 permuted(float4 v, int perm) {
 template <int NP, bool REVERSE>
 __device__ __forceinline__ void enter_segment(const ScanArgs& a, int b, int c, int nl, int seg,
                                               const float2* A2, float2* h, int perm = 0) {
-  for (int i = REVERSE ? a.segs - 1 : 0; REVERSE ? i > seg : i < seg; i += REVERSE ? -1 : 1) {
-    const long long row = ((long long)i * a.B + b) * a.D + c;
-    const float4 s = permuted(*reinterpret_cast<const float4*>(a.seg_state + row * NP + nl * 4), perm);
-    const float2 sum = make_float2(a.seg_sum[row], a.seg_sum[row]);
-    const float2 e0 = exp2_pair(mul2(sum, A2[0])), e1 = exp2_pair(mul2(sum, A2[1]));
-    // a state of zero stays zero, however far a growing mode (A > 0) would have grown
-    h[0].x = (h[0].x == 0.f ? 0.f : e0.x * h[0].x) + s.x;
-    h[0].y = (h[0].y == 0.f ? 0.f : e0.y * h[0].y) + s.y;
-    h[1].x = (h[1].x == 0.f ? 0.f : e1.x * h[1].x) + s.z;
-    h[1].y = (h[1].y == 0.f ? 0.f : e1.y * h[1].y) + s.w;
+  constexpr int BATCH = 6;  // segments whose loads are in flight together
+  const int count = REVERSE ? a.segs - 1 - seg : seg;
+  for (int i0 = 0; i0 < count; i0 += BATCH) {
+    float4 s[BATCH];
+    float sum[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      s[k] = make_float4(0.f, 0.f, 0.f, 0.f);  // behind the last one: a step of 0, which leaves h
+      sum[k] = 0.f;
+      if (i0 + k < count) {
+        const int i = REVERSE ? a.segs - 1 - i0 - k : i0 + k;
+        const long long row = ((long long)i * a.B + b) * a.D + c;
+        s[k] = *reinterpret_cast<const float4*>(a.seg_state + row * NP + nl * 4);
+        sum[k] = a.seg_sum[row];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const float4 v = permuted(s[k], perm);
+      const float2 by = make_float2(sum[k], sum[k]);
+      const float2 e0 = exp2_pair(mul2(by, A2[0])), e1 = exp2_pair(mul2(by, A2[1]));
+      // a state of zero stays zero, however far a growing mode (A > 0) would have grown
+      h[0].x = (h[0].x == 0.f ? 0.f : e0.x * h[0].x) + v.x;
+      h[0].y = (h[0].y == 0.f ? 0.f : e0.y * h[0].y) + v.y;
+      h[1].x = (h[1].x == 0.f ? 0.f : e1.x * h[1].x) + v.z;
+      h[1].y = (h[1].y == 0.f ? 0.f : e1.y * h[1].y) + v.w;
+    }
   }
 }
 
