@@ -1,5 +1,5 @@
 // Internal interfaces of the operators around the recurrence (block_api.cu to
-// conv.cu, scan_fwd.cu, scan_bwd.cu, group_norm.cu).
+// conv.cu, scan_fwd.cu, scan_bwd.cu, group_norm.cu, norm_sequence.cu, norm_resident.cu).
 #pragma once
 
 #include <cuda_runtime.h>

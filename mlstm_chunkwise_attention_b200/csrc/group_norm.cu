@@ -1,6 +1,6 @@
 // Group norm of channels-last (or head-major) activations with an activation or
 // an output gate, forward and backward; here the statistics of single tokens, in
-// norm_sequence.cu those of whole sequences.  With n = xhat w + bias over groups of d
+// norm_resident.cu and norm_sequence.cu those of whole sequences.  With n = xhat w + bias over groups of d
 // channels, xhat = (x - mean) rstd:
 //
 //   y = act(n)  or  y = n act(gate)

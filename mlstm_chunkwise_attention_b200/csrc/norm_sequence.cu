@@ -12,7 +12,7 @@
 // Means and variances are joined as (count, mean, sum of squared distances), never as a difference of
 // squares, and in a fixed order whoever comes last.
 //
-// Measured on one B200 at B4 T8192 NH16 d256 bf16 with SiLU: forward 155 us, backward 307 us (0.53 and
+// Measured on one B200 at B4 T8192 NH16 d256 bf16 with SiLU: forward 150 us, backward 304 us (0.55 and
 // 0.41 of a plain copy of the tensors moved once).  A second pass over memory took 165 and 324 us at
 // its best; a chunk of half or twice as many items as CTAs 206 / 349 and 175 / 327 us (waits; L2).
 // What bounds it now is the issue of instructions between the barriers (0.5 to 0.6 of the cycles).

@@ -14,9 +14,9 @@
 // Each CTA writes its share of dB, dC and the parameters' gradients; a second kernel adds the shares in
 // a fixed order.
 //
-// Measured on one B200 at B8 T4096 D4096 N16 bf16 with a gate: 2.59 ms and 0.06 for the sums
-// (268 MB of shares of dB and dC).  Shared memory hands over 0.64 of what it can, 0.48 of the cycles issue, with 12
-// warps an SM: latency between those two.  With the decays kept in registers (two CTAs an SM) 3.43 ms;
+// Measured on one B200 at B8 T4096 D4096 N16 bf16 with a gate: 2.59 ms, and 0.06 for the sums (268 MB
+// of shares of dB and dC).  Shared memory hands over 0.64 of what it can, 0.48 of the cycles issue, with
+// 12 warps an SM: latency between those two.  With the decays kept in registers (two CTAs an SM) 3.43 ms;
 // without segments in turn the 512 CTAs take two waves of 444.
 #include "internal.h"
 #include "scan_common.cuh"
