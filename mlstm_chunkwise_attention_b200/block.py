@@ -331,8 +331,9 @@ def selective_scan_backward(x, dt, A, B, C, dy, saved, *, skip=None, z=None, dt_
     _activation("dy", dy, x.shape, x)
     _fp32("dstate_out", dstate_out, (p.B, p.D, p.N), x)
     need = load().mlstm_scan_saved_size(p.B, p.T, p.D, p.G, p.N, p.dtype)
-    if saved is None or saved.device != x.device or saved.numel() * saved.element_size() < need:
-        raise ValueError(f"saved must hold the {need} bytes of the forward of the same inputs")
+    if (saved is None or saved.device != x.device or not saved.is_contiguous()
+            or saved.numel() * saved.element_size() < need):
+        raise ValueError(f"saved must hold the {need} bytes of the forward of the same inputs, contiguous")
 
     def launch(s):
         out = {"dx": _like(x), "ddt": _like(x), "dA": _like(A), "dB": _like(B), "dC": _like(C),

@@ -28,7 +28,7 @@ constexpr int kSms = 148;
 // Dynamic shared memory of each of `ctas` CTAs on an SM: of its 228 KB, each takes one for the system and
 // one for `sums`.
 constexpr int share_of(int ctas) { return (228 / ctas - 2) * 1024; }
-constexpr int kEach = 64;  // tokens of a thread: few enough that sums of them in fp32 lose little
+constexpr int kEach = 64;  // more tokens of a thread than ever fit: bounds the arithmetic below
 
 // A CTA takes `slab` tokens of one group, `each` of them to a thread: lanes along the channels, eight to
 // a lane, and its other threads along tokens.
@@ -91,7 +91,8 @@ __device__ __forceinline__ double warp_sum64(double v) {
 }
 
 template <typename T, bool GATED, bool WIDE, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) norm_resident_kernel(NormArgs a, Slabs p, float* param) {
+__global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas)
+    norm_resident_kernel(NormArgs a, Slabs p, float* param) {
   constexpr int TENSORS = 1 + BWD + GATED;
   constexpr bool LATE = GATED && !BWD;  // the gate is not needed before the outputs
   extern __shared__ __align__(16) unsigned char dynamic[];
@@ -250,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, BWD ? kBwdCtas : kFwdCtas) norm_resi
       y += p.rows * a.y.st;
     }
   } else {
-    const float m1 = (float)(warp_sum64((double)q0.x + q1.x) * inv), m2 = (float)(warp_sum64((double)q0.y + q1.y) * inv);
+    const float m1 = (float)(warp_sum64((double)q0.x + q1.x) * inv);
+    const float m2 = (float)(warp_sum64((double)q0.y + q1.y) * inv);
     const float2 ms = reinterpret_cast<const float2*>(a.stats)[group];
     const float2 neg = make_float2(-ms.x, -ms.x), rs = make_float2(ms.y, ms.y);
     const float2 n1 = make_float2(-m1, -m1), n2 = make_float2(-m2, -m2);

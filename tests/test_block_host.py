@@ -209,7 +209,9 @@ def norm_fwd(lib, x=rows(), w=None, bias=None, gate=None, y=rows(), stats=None, 
     (dict(eps=0.0), 1), (dict(eps=float("nan")), 1), (dict(dtype=9), 1), (dict(d=513), 2),
     (dict(x=rows(None)), 1), (dict(y=rows(None)), 1), (dict(gate=rows(FAKE + 1)), 1),
     (dict(Bn=1 << 14, T=1 << 14, NH=1 << 6, d=1 << 8), 2), (dict(Bn=1 << 14, NH=1 << 14, d=1, scope=1), 2),
-    (dict(w=FAKE + 1), 1), (dict(stats=FAKE + 4), 1), (dict(scope=1), 3), (dict(scope=1, ws=FAKE, nbytes=4), 3),
+    (dict(w=FAKE + 1), 1), (dict(stats=FAKE + 4), 1),
+    # a group too large for a cluster's shared memory needs a workspace
+    (dict(d=4096, scope=1), 3), (dict(d=4096, scope=1, ws=FAKE, nbytes=4), 3),
     (dict(Bn=0), 0), (dict(T=0), 0),
 ])
 def test_norm_argument_errors(lib, kw, status):
@@ -226,6 +228,10 @@ def test_norm_backward_argument_errors(lib):
 
     assert bwd(stats=None) == 1 and bwd(dx=rows(None)) == 1 and bwd(gate=rows()) == 1
     assert bwd(ws=None) == 3 and bwd(nbytes=need - 4) == 3 and bwd(ws=FAKE + 8) == 1
+    # over a sequence: none in the forward where a cluster holds a group, else for what CTAs hand on
+    assert lib.mlstm_group_norm_workspace_size(2, 5, 4, 16, 1, B.BF16, 0) == 0
+    assert lib.mlstm_group_norm_workspace_size(2, 5, 4, 16, 1, B.BF16, 1) >= 2 * 2 * 4 * 16 * 4
+    assert lib.mlstm_group_norm_workspace_size(2, 5, 4, 4096, 1, B.BF16, 0) > 0
     assert lib.mlstm_group_norm_stats_size(2, 5, 4, 16, 0) == 2 * 5 * 4 * 8
     assert lib.mlstm_group_norm_stats_size(2, 5, 4, 16, 1) == 2 * 4 * 8
 

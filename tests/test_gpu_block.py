@@ -672,6 +672,14 @@ def test_refusals_on_the_device():
         block.group_norm_backward(x, None, None, x, None, groups=2)
 
 
+def test_saved_states_are_refused_unless_contiguous():
+    x = torch.zeros(2, 5, 16, dtype=BF, device="cuda")
+    A, Bm = torch.zeros(16, 4, device="cuda"), torch.zeros(2, 5, 4, dtype=BF, device="cuda")
+    _, saved, _ = block.selective_scan_forward(x, x, A, Bm, Bm)
+    with pytest.raises(ValueError, match="contiguous"):
+        block.selective_scan_backward(x, x, A, Bm, Bm, x, saved.repeat(2)[::2])
+
+
 # ---- together, as a block uses them --------------------------------------------------------------
 
 @pytest.mark.parametrize("variant", [binding.SIG, binding.EXP], ids=["sig", "exp"])
