@@ -88,15 +88,18 @@ def scan64(x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, softplus=True, sta
         delta, deltam, dslope = raw, rawm, torch.ones_like(raw)
     wide = lambda m, t: m[:, t].repeat_interleave(P, 1)  # [B, D, N]
     s = state if state is not None else x.new_zeros(B, D, N)
-    sm = s.abs()
-    trail, mags, ys, ym = [s], [sm], [], []
+    sa = sm = s.abs()
+    trail, sizes, mags, ys, ym = [s], [sa], [sm], [], []
     for t in range(T):
         e = torch.exp(delta[:, t, :, None] * A)
-        # the decay's exponent carries deltam |A| roundings
-        em = e * (1 + deltam[:, t, :, None] * A.abs())
+        # To first order an error of the state decays as the state does, and each step adds its own
+        # roundings and the decay's: deltam |A| of its exponent, on a state of at most sa.
         s = e * s + (delta[:, t] * x[:, t])[..., None] * wide(Bm, t)
-        sm = em * sm + (deltam[:, t] * x[:, t].abs())[..., None] * wide(Bm, t).abs()
+        sm = (e * (sm + (1 + deltam[:, t, :, None] * A.abs()) * sa)
+              + (deltam[:, t] * x[:, t].abs())[..., None] * wide(Bm, t).abs())
+        sa = e * sa + ((delta[:, t] * x[:, t])[..., None] * wide(Bm, t)).abs()
         trail.append(s)
+        sizes.append(sa)
         mags.append(sm)
         ys.append((s * wide(Cm, t)).sum(-1))
         ym.append((sm * wide(Cm, t).abs()).sum(-1))
@@ -116,20 +119,21 @@ def scan64(x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, softplus=True, sta
         out["dz"] = (dy * y * zsl, dy.abs() * (ym + y.abs()) * zslm)
         dy, dym = dy * zs, dy.abs() * zm
     g = dstate_out if dstate_out is not None else x.new_zeros(B, D, N)
-    gm = g.abs()
+    ga = gm = g.abs()
     dx, ddt, dB, dC = (torch.zeros_like(v) for v in (x, x, Bm, Cm))
     dxm, ddtm, dBm, dCm = (torch.zeros_like(v) for v in (x, x, Bm, Cm))
     dA, dAm = torch.zeros_like(A), torch.zeros_like(A)
     for t in range(T - 1, -1, -1):
         g = g + dy[:, t, :, None] * wide(Cm, t)
         gm = gm + dym[:, t, :, None] * wide(Cm, t).abs()
+        ga = ga + dy[:, t, :, None].abs() * wide(Cm, t).abs()
         dC[:, t] = (dy[:, t, :, None] * trail[t + 1]).view(B, G, P, N).sum(2)
         dCm[:, t] = (dym[:, t, :, None] * mags[t + 1]).view(B, G, P, N).sum(2)
         dB[:, t] = ((delta[:, t] * x[:, t])[..., None] * g).view(B, G, P, N).sum(2)
         dBm[:, t] = ((deltam[:, t] * x[:, t].abs())[..., None] * gm).view(B, G, P, N).sum(2)
         e = torch.exp(delta[:, t, :, None] * A)
-        em = e * (1 + deltam[:, t, :, None] * A.abs())
-        u, um = g * e * trail[t], gm * em * mags[t]
+        power = 1 + deltam[:, t, :, None] * A.abs()
+        u, um = g * e * trail[t], e * (gm * sizes[t] + ga * mags[t] + power * ga * sizes[t])
         gB, gBm = (g * wide(Bm, t)).sum(-1), (gm * wide(Bm, t).abs()).sum(-1)
         dA += (u * delta[:, t, :, None]).sum(0)
         dAm += (um * deltam[:, t, :, None]).sum(0)
@@ -137,7 +141,7 @@ def scan64(x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, softplus=True, sta
         dxm[:, t] = gBm * deltam[:, t]
         ddt[:, t] = gB * x[:, t] + (u * A).sum(-1)
         ddtm[:, t] = gBm * x[:, t].abs() + (um * A.abs()).sum(-1)
-        g, gm = g * e, gm * em
+        g, gm, ga = g * e, e * (gm + power * ga), e * ga
     if skip is not None:
         dx, dxm = dx + skip * dy, dxm + (skip * dy).abs() + skip.abs() * dym
     ddt, ddtm = ddt * dslope, ddtm * dslope * (1 + rawm)

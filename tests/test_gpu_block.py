@@ -144,6 +144,7 @@ SCAN = [
     (2, 600, 256, 16, 256, False, True, True, True, True, F32, False),  # many tiles: segments in turn
     (5, 530, 256, 4, 256, True, False, True, True, True, BF, False),    # in turn in both directions
     (2, 64, 64, 20, 64, True, True, True, True, True, F32, False),   # a group per channel
+    (1, 2943, 44, 12, 2, True, False, True, True, True, F32, False),  # long, and as many segments as fit
 ]
 
 
@@ -186,7 +187,7 @@ def test_scan_against_64_bits(case):
     assert none is None and torch.equal(alone, y)
     ref = scan64(*(d64(c[k]) for k in ("x", "dt", "A", "Bm", "Cm", "skip", "z", "dt_bias")), softplus,
                  d64(c["state"]), d64(c["dy"]), d64(c["dso"]))
-    K = 64 + 16 * T + N
+    K = 64 + T + N  # T: where the scan is cut, the steps of a segment are summed before their exponential
     close(y, *ref["y"], K, "y")
     close(end, *ref["state"], K, "state")
     for name in ("dx", "ddt", "dstate_in", "dz"):
@@ -221,8 +222,8 @@ def test_scan_pieces_and_steps_continue_a_sequence(dtype, D, N):
     binding.check_device()
     ref = scan64(*(d64(c[k]) for k in ("x", "dt", "A", "Bm", "Cm", "skip", "z", "dt_bias")), True,
                  d64(c["state"]))
-    close(torch.cat(parts, 1), *ref["y"], 64 + 16 * T + N, "y")
-    close(st, *ref["state"], 64 + 16 * T + N, "state")
+    close(torch.cat(parts, 1), *ref["y"], 64 + T + N, "y")
+    close(st, *ref["state"], 64 + T + N, "state")
 
 
 def test_scan_closed_decay_and_large_steps():
