@@ -14,6 +14,9 @@
  * tokens, channels and batches are taken in a fixed order, and atomics only
  * hand out work.  Some kernels wait, bounded, for another CTA's part of the
  * same launch; a wait that was given up is reported by mlstm_device_status.
+ * A launch behind a failed one runs normally, and so does every replay of a
+ * captured one: what a failure leaves for its own launch to see lies in the
+ * workspace and is cleared when the launch starts, and each failure is counted.
  *
  * Sizes.  B T < 2^30, NH d <= 2^24, B NH d < 2^31, B T NH d < 2^40, and what the
  * operators say; other values return MLSTM_ERR_UNSUPPORTED.
@@ -181,6 +184,17 @@ int mlstm_group_norm_bwd(const mlstm_rows_t* x, const float* weight, const float
                          const mlstm_rows_t* dx, const mlstm_rows_t* dgate, float* dweight,
                          float* dbias, void* workspace, size_t workspace_bytes, int B, int T,
                          int NH, int d, int scope, int act, int dtype, void* stream);
+
+/* Self-test of the failure report, as mlstm_selftest_timeout: enqueue one tiny
+ * kernel that waits as the kernels of `family` do, on a word that nothing
+ * raises, gives up after 2 s and returns.  The next mlstm_device_status
+ * returns MLSTM_ERR_TIMEOUT.  workspace: 8 bytes at least. */
+typedef enum {
+  MLSTM_WAITS_SCAN_FWD = 0,
+  MLSTM_WAITS_SCAN_BWD = 1,
+  MLSTM_WAITS_NORM = 2
+} mlstm_block_waits_t;
+int mlstm_block_selftest_timeout(int family, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

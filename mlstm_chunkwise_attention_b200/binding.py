@@ -110,6 +110,7 @@ EXPORTS = {
                              [ctypes.c_float, _I, _P]),
     "mlstm_group_norm_bwd": (_I, [_ROWS, _P, _P, _ROWS, _ROWS, _P, _ROWS, _ROWS, _P, _P, _P,
                                   ctypes.c_size_t] + [_I] * 7 + [_P]),
+    "mlstm_block_selftest_timeout": (_I, [_I, _P, ctypes.c_size_t, _P]),
 }
 
 

@@ -59,8 +59,9 @@ struct ScanArgs {
   float *part_bc, *part_a, *part_d;
   // the sequence's segments (one: the whole of it).  At once: seg_state and seg_sum hold each
   // segment's own state and its sum of delta, [segs, B, D, scan_pad(N)] and [segs, B, D].  In turn:
-  // seg_state is the state handed from a segment to the next, [B, D, scan_pad(N)], and `turn` a
-  // counter of taken items followed by each channel tile's finished segments, zero at the launch.
+  // seg_state is the state handed from a segment to the next, [B, D, scan_pad(N)], and `turn` the
+  // launch's abort word, a counter of taken items and each channel tile's finished segments, zero at the
+  // launch.
   float *seg_state, *seg_sum;
   unsigned int* turn;
   int seg_len, segs;
@@ -69,6 +70,7 @@ struct ScanArgs {
   bool wide, wide_bc;           // 16-byte accesses of the [B, T, D] tensors / of B and C
 };
 constexpr int kScanEvery = 8;  // tokens between two saved states
+constexpr int kTurnAbort = 0, kTurnNext = 1, kTurnTiles = 2;  // words of ScanArgs::turn
 // States per channel as the kernels hold them: four to a lane, 2, 4, 8 or 16 lanes to a channel.
 inline int scan_pad(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 // How a pass cuts the sequence: into `count` segments of `len` tokens (a multiple of the kernels'
@@ -94,9 +96,11 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_reverse_segments(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t s);
-// Epochs of the scan kernels' last launches that gave up a wait (see tc::Abort).
+// How many launches of a family gave up a wait (see LaunchAbort), and one that does: `words` are two, zero.
 cudaError_t fetch_scan_fwd_error(unsigned int* flag);
 cudaError_t fetch_scan_bwd_error(unsigned int* flag);
+cudaError_t launch_scan_fwd_selftest(unsigned int* words, cudaStream_t s);
+cudaError_t launch_scan_bwd_selftest(unsigned int* words, cudaStream_t s);
 
 // ---- group norm --------------------------------------------------------------
 struct NormArgs {
@@ -119,6 +123,7 @@ long long norm_sequence_items(int B, int T, int NH, int d);
 size_t norm_sequence_workspace(int B, int T, int NH, int d, int dtype, bool backward);
 cudaError_t launch_norm_sequence(const NormArgs& a, bool backward, cudaStream_t s);
 cudaError_t fetch_norm_error(unsigned int* flag);
+cudaError_t launch_norm_selftest(unsigned int* words, cudaStream_t s);
 // Groups that fit the shared memory of a cluster (norm_resident.cu); false: norm_sequence.cu takes them.
 bool norm_resident_workspace(int B, int T, int NH, int d, int dtype, bool gated, bool backward, size_t* bytes);
 bool launch_norm_resident(const NormArgs& a, bool backward, cudaStream_t s, cudaError_t* status);

@@ -102,7 +102,7 @@ ScanWorkspace scan_workspace(int B, int T, int D, int G, int N, bool backward) {
   if (w.cut.count > 1) rows = (size_t)(w.cut.in_turn ? 1 : w.cut.count) * B * D;
   w.seg_sum = align256(rows * mlstm::scan_pad(N) * 4);
   w.turn = align256(w.seg_sum + (w.cut.in_turn ? 0 : rows * 4));
-  w.bc = align256(w.turn + (w.cut.in_turn ? ((size_t)w.cut.tiles + 1) * 4 : 0));
+  w.bc = align256(w.turn + (w.cut.in_turn ? ((size_t)w.cut.tiles + mlstm::kTurnTiles) * 4 : 0));
   w.total = w.bc;
   if (backward) {
     const mlstm::ScanBwdSizes z = mlstm::scan_bwd_sizes(B, T, D, G, N);
@@ -120,7 +120,7 @@ int use_segments(mlstm::ScanArgs* a, char* ws, const ScanWorkspace& w, void* str
   a->seg_sum = (float*)(ws + w.seg_sum);
   a->turn = (unsigned int*)(ws + w.turn);
   if (!a->in_turn) return MLSTM_OK;
-  return fill(a->turn, nullptr, ((size_t)w.cut.tiles + 1) * 4, stream, "scan turns");
+  return fill(a->turn, nullptr, ((size_t)w.cut.tiles + mlstm::kTurnTiles) * 4, stream, "scan turns");
 }
 
 // The inputs of a scan call; T is that of the call (1 for a step).
@@ -437,6 +437,18 @@ int mlstm_group_norm_bwd(const mlstm_rows_t* x, const float* weight, const float
            !off16(bias);
   if ((st = pending_error("before mlstm_group_norm_bwd")) != MLSTM_OK) return st;
   return cuda_result(mlstm::launch_norm_bwd(a, (cudaStream_t)stream), "group_norm_bwd");
+}
+
+int mlstm_block_selftest_timeout(int family, void* workspace, size_t workspace_bytes, void* stream) {
+  if (family < MLSTM_WAITS_SCAN_FWD || family > MLSTM_WAITS_NORM || off4(workspace)) return MLSTM_ERR_INVALID;
+  if (workspace == nullptr || workspace_bytes < 8) return MLSTM_ERR_WORKSPACE;
+  int st = pending_error("before mlstm_block_selftest_timeout");
+  if (st == MLSTM_OK) st = fill(workspace, nullptr, 8, stream, "selftest words");
+  if (st != MLSTM_OK) return st;
+  auto launch = family == MLSTM_WAITS_SCAN_FWD   ? mlstm::launch_scan_fwd_selftest
+                : family == MLSTM_WAITS_SCAN_BWD ? mlstm::launch_scan_bwd_selftest
+                                                 : mlstm::launch_norm_selftest;
+  return cuda_result(launch((unsigned int*)workspace, (cudaStream_t)stream), "block selftest_timeout");
 }
 
 }  // extern "C"

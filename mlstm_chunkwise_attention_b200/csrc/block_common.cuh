@@ -4,6 +4,7 @@
 
 #include "block.h"
 #include "common.cuh"
+#include "tc_common.cuh"
 
 namespace mlstm {
 
@@ -216,6 +217,41 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   unsigned long long d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
   return as_f2(d);
+}
+
+// The abort state of one launch whose CTAs wait for one another.  `word` lies in the launch's workspace
+// and is zeroed with its counters, by a memset that a graph captures too, so a replayed launch starts
+// clean whatever became of the ones before it.  `failures` is the kernel family's count of launches that
+// gave up; it only grows, so a second failure of the same graph is news as well.
+struct LaunchAbort {
+  unsigned int *word, *failures;
+  __device__ __forceinline__ bool raised() const { return *reinterpret_cast<volatile unsigned int*>(word) != 0; }
+  __device__ __forceinline__ void raise() const {
+    if (atomicExch(word, 1u) == 0) atomicAdd(failures, 1u);
+  }
+};
+__device__ __forceinline__ unsigned int load_acquire(const unsigned int* at) {
+  unsigned int v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+  return v;
+}
+// One thread waits until *at >= least; false if it gave up, after the 2 s of the tensor-core kernels' waits
+// or because another CTA of the launch did.
+__device__ __forceinline__ bool wait_at_least(const unsigned int* at, unsigned int least,
+                                              const LaunchAbort& abort, unsigned int nap_ns) {
+  const uint64_t began = tc::global_timer_ns();
+  for (unsigned int i = 1; load_acquire(at) < least; ++i) {
+    if ((i & 63) == 0 && (abort.raised() || tc::global_timer_ns() - began > tc::kWaitTimeoutNs)) {
+      abort.raise();
+      return false;
+    }
+    __nanosleep(nap_ns);
+  }
+  return true;
+}
+// A launch whose wait runs out: word 0 is its abort word, word 1 what nothing raises.
+__device__ __forceinline__ void selftest_wait(unsigned int* words, unsigned int* failures) {
+  wait_at_least(words + 1, 1, LaunchAbort{words, failures}, 200);
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;

@@ -755,9 +755,10 @@ const char* mlstm_last_error(void) { return g_last_error; }
 
 namespace {
 // Failures already reported, per device and kernel family: the flag values
-// mlstm_device_status saw last.  A flag holds the epoch of the last launch of
-// its family that gave up, so a value that differs from the last one seen is a
-// failure not yet reported.
+// mlstm_device_status saw last.  A tensor-core family's flag holds the epoch of
+// its last launch that gave up, a family's of mlstm_block.h the number of those
+// launches, so a value that differs from the last one seen is a failure not yet
+// reported.
 constexpr int kFlagDevices = 64, kFlagFamilies = 10;
 std::mutex g_flag_mu;
 unsigned int g_flag_seen[kFlagDevices][kFlagFamilies] = {};

@@ -16,9 +16,7 @@
 // 0.41 of a plain copy of the tensors moved once).  A second pass over memory took 165 and 324 us at
 // its best; a chunk of half or twice as many items as CTAs 206 / 349 and 175 / 327 us (waits; L2).
 // What bounds it now is the issue of instructions between the barriers (0.5 to 0.6 of the cycles).
-#include "internal.h"
 #include "norm_common.cuh"
-#include "tc_common.cuh"
 
 namespace mlstm {
 
@@ -26,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int slots_of(bool backward) { return 148 * (backward ? 2 : 3); }  // CTAs of the persistent grid
-__device__ unsigned int g_norm_error = 0;  // epoch of the last launch that gave up a wait
+__device__ unsigned int g_norm_failures = 0;  // launches that gave up a wait
 
 // The problem's items.  A CTA takes a slab of tokens and a block of up to 2048 channels of a (batch,
 // group): lanes along the channels, eight to a lane, and its other threads along tokens.
@@ -40,10 +38,10 @@ struct Plan {
   __host__ __device__ long long items() const { return 2LL * chunks * chunk * parts(); }
 };
 
-// Workspace: counters (next item; finished sums and readiness of each group, zero at the launch), each
-// group's pair of results, each item's sums, and in the backward rows of parameter sums.
+// Workspace: words that are zero at the launch (its abort word; the next item; finished sums and readiness
+// of each group), each group's pair of results, each item's sums, and in the backward rows of parameter sums.
 struct Layout {
-  size_t zeroed, pair, part, param, total;  // bytes; the counters lie at 0
+  size_t zeroed, pair, part, param, total;  // bytes; the zeroed words lie at 0
 };
 
 // Tokens of an item that a thread takes, all of them on their way from memory at once: as many as 64 KB
@@ -77,7 +75,7 @@ Plan plan_for(int B, int T, int NH, int d, int elem, bool gated, bool backward) 
 Layout layout_for(const Plan& p, int B, int D, bool backward) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   Layout l;
-  l.zeroed = ((size_t)p.groups * 2 + 1) * 4;
+  l.zeroed = ((size_t)p.groups * 2 + 2) * 4;
   l.pair = up(l.zeroed);
   l.part = up(l.pair + (size_t)p.groups * 8);
   l.param = up(l.part + (size_t)p.groups * p.parts() * 3 * 4);
@@ -86,7 +84,7 @@ Layout layout_for(const Plan& p, int B, int D, bool backward) {
 }
 
 struct Work {
-  unsigned int *next, *done, *ready;
+  unsigned int *abort, *next, *done, *ready;
   float2* pair;  // [groups]: mean and 1 / deviation, or the two means of the backward
   float* part;   // [groups, parts, 3]
   float* param;  // [B, slabs, 2, NH d], or null
@@ -145,7 +143,7 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 // item.
 template <typename T, bool GATED, bool WIDE, bool BWD>
 __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
-    norm_sequence_kernel(NormArgs a, Plan p, Work w, unsigned int epoch) {
+    norm_sequence_kernel(NormArgs a, Plan p, Work w) {
   constexpr int TENSORS = 1 + BWD + GATED, EACH = each_of((int)sizeof(T), TENSORS), ALL = kThreads + 64;
   extern __shared__ __align__(16) unsigned char dynamic[];
   // x, then dy, then the gate on their way; and in the backward the channels' sums [rows][2][lanes][8]
@@ -240,12 +238,6 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
   }
   if (warp > kThreads / 32) {  // ---- the manager ---------------------------------------------
     const int lane = tid & 31;
-    const tc::Abort abort{&g_norm_error, epoch};
-    auto look = [&](const Item& q) {
-      unsigned int v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(w.ready + q.group) : "memory");
-      return v != 0;
-    };
     if (lane == 0) {
       items[0].set(a, p, atomicAdd(w.next, 1u));
       items[1].set(a, p, atomicAdd(w.next, 1u));
@@ -260,16 +252,7 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
       if (q.output < 0) return;
       if (q.output && q.group >= 0 && ready[i & 1] == 0) {
         if (lane == 0) {
-          int ok = 1;
-          const uint64_t began = tc::global_timer_ns();
-          for (unsigned int n = 1; !look(q); ++n) {
-            if ((n & 63) == 0 && (abort.raised() || tc::global_timer_ns() - began > tc::kWaitTimeoutNs)) {
-              abort.raise();
-              ok = 0;
-              break;
-            }
-            __nanosleep(100);
-          }
+          const bool ok = wait_at_least(w.ready + q.group, 1, LaunchAbort{w.abort, &g_norm_failures}, 100);
           result[i & 1] = __ldcg(w.pair + q.group);
           waited = ok;
         }
@@ -281,7 +264,7 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
         items[(i + 2) & 3].set(a, p, atomicAdd(w.next, 1u));
         const Item& next = items[(i + 1) & 3];
         int ok = 0;
-        if (next.output > 0 && next.group >= 0 && look(next)) {
+        if (next.output > 0 && next.group >= 0 && load_acquire(w.ready + next.group) != 0) {
           result[(i + 1) & 1] = __ldcg(w.pair + next.group);
           ok = 1;
         }
@@ -522,7 +505,8 @@ cudaError_t run(const NormArgs& a, cudaStream_t s) {
   const Layout l = layout_for(p, a.B, a.NH * a.d, BWD);
   char* ws = (char*)a.ws;
   Work w;
-  w.next = (unsigned int*)ws;
+  w.abort = (unsigned int*)ws;
+  w.next = w.abort + 1;
   w.done = w.next + 1;
   w.ready = w.done + p.groups;
   w.pair = (float2*)(ws + l.pair);
@@ -539,7 +523,7 @@ cudaError_t run(const NormArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long items = p.items(), slots = slots_of(BWD);
   norm_sequence_kernel<T, GATED, WIDE, BWD>
-      <<<(unsigned)(items < slots ? items : slots), kThreads + 64, bytes, s>>>(a, p, w, next_epoch());
+      <<<(unsigned)(items < slots ? items : slots), kThreads + 64, bytes, s>>>(a, p, w);
   e = cudaGetLastError();
   if (e != cudaSuccess || !params) return e;
   return launch_param_sums(w.param, a.B * p.slabs, a.NH * a.d, 1, a.dw, a.dbias, s);
@@ -549,6 +533,8 @@ cudaError_t by_kind(const NormArgs& a, cudaStream_t s) {
   if (a.gate.p != nullptr) return a.wide ? run<T, true, true, BWD>(a, s) : run<T, true, false, BWD>(a, s);
   return a.wide ? run<T, false, true, BWD>(a, s) : run<T, false, false, BWD>(a, s);
 }
+
+__global__ void selftest_kernel(unsigned int* words) { selftest_wait(words, &g_norm_failures); }
 
 }  // namespace
 
@@ -579,8 +565,12 @@ cudaError_t launch_norm_sequence(const NormArgs& a, bool backward, cudaStream_t 
   return a.dtype == 0 ? by_kind<bf16, false>(a, s) : by_kind<float, false>(a, s);
 }
 
+cudaError_t launch_norm_selftest(unsigned int* words, cudaStream_t s) {
+  selftest_kernel<<<1, 1, 0, s>>>(words);
+  return cudaGetLastError();
+}
 cudaError_t fetch_norm_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_norm_error, sizeof(unsigned int));
+  return cudaMemcpyFromSymbol(flag, g_norm_failures, sizeof(unsigned int));
 }
 
 }  // namespace mlstm

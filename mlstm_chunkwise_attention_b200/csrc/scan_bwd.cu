@@ -18,7 +18,6 @@
 // of shares of dB and dC).  Shared memory hands over 0.64 of what it can, 0.48 of the cycles issue, with
 // 12 warps an SM: latency between those two.  With the decays kept in registers (two CTAs an SM) 3.43 ms;
 // without segments in turn the 512 CTAs take two waves of 444.
-#include "internal.h"
 #include "scan_common.cuh"
 
 namespace mlstm {
@@ -28,7 +27,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = 16;
 constexpr int kCtas = 3;  // of an SM
 constexpr int kSlots = 148 * kCtas;
-__device__ unsigned int g_scan_bwd_error = 0;  // epoch of the last launch that gave up a wait
+__device__ unsigned int g_scan_bwd_failures = 0;  // launches that gave up a wait
 static_assert(kTile == 2 * kScanEvery, "two saved states to a tile");
 
 template <typename T, int LPC>
@@ -54,7 +53,7 @@ struct Cfg {
 };
 
 template <typename T, int LPC, bool GATE, bool WIDE>
-__global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, int tiles, unsigned int epoch) {
+__global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, int tiles) {
   using C = Cfg<T, LPC>;
   constexpr int NP = C::NP, CL = C::CL, CT = C::CT, VECS = C::VECS, UNITS = C::UNITS;
   extern __shared__ __align__(16) float sm[];
@@ -64,7 +63,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
   const int perm = (cr & 1) * 2 + (CL >= 4 ? (cr >> 1) & 1 : 0);  // and state k ^ perm as its k-th
   const int ch[2] = {cl + swap, cl + 1 - swap};
   __shared__ int box[2];
-  const tc::Abort abort{&g_scan_bwd_error, epoch};
   const int per_seg = a.B * a.G * tiles, NC = (a.T + kScanEvery - 1) / kScanEvery;
   for (bool once = true;; once = false) {
   const int work = next_item(a, blockIdx.x, once, per_seg * a.segs, box);
@@ -74,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
   const ChannelTile q = channel_tile(a, ti, tiles, CT);
   const int first = seg * a.seg_len, last = min(first + a.seg_len, a.T);
   const bool handed = a.in_turn && seg < a.segs - 1;  // the segment behind hands its gradient on
-  if (handed && !wait_turn(a, bi, a.segs - 1 - seg, abort, box + 1)) return;
+  if (handed && !wait_turn(a, bi, a.segs - 1 - seg, &g_scan_bwd_failures, box + 1)) return;
   float2 A2[2][2], G[2][2], dA[2][2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -443,7 +441,7 @@ cudaError_t bwd_kernel(const ScanArgs& a, int tiles, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long items = (long long)a.B * a.G * tiles * a.segs;
   const long long grid = a.in_turn && items > kSlots ? kSlots : items;
-  scan_bwd_kernel<T, LPC, GATE, WIDE><<<(unsigned)grid, kThreads, bytes, s>>>(a, tiles, next_epoch());
+  scan_bwd_kernel<T, LPC, GATE, WIDE><<<(unsigned)grid, kThreads, bytes, s>>>(a, tiles);
   return cudaGetLastError();
 }
 
@@ -475,6 +473,8 @@ cudaError_t by_states(const ScanArgs& a, cudaStream_t s) {
   }
 }
 
+__global__ void selftest_kernel(unsigned int* words) { selftest_wait(words, &g_scan_bwd_failures); }
+
 }  // namespace
 
 ScanSegments scan_bwd_segments(int B, int T, int D, int G, int N) {
@@ -482,8 +482,12 @@ ScanSegments scan_bwd_segments(int B, int T, int D, int G, int N) {
   return scan_cut(T, kTile, (long long)B * G * ((D / G + CT - 1) / CT), kSlots);
 }
 
+cudaError_t launch_scan_bwd_selftest(unsigned int* words, cudaStream_t s) {
+  selftest_kernel<<<1, 1, 0, s>>>(words);
+  return cudaGetLastError();
+}
 cudaError_t fetch_scan_bwd_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_scan_bwd_error, sizeof(unsigned int));
+  return cudaMemcpyFromSymbol(flag, g_scan_bwd_failures, sizeof(unsigned int));
 }
 
 ScanBwdSizes scan_bwd_sizes(int B, int T, int D, int G, int N) {

@@ -8,7 +8,6 @@
 #pragma once
 
 #include "block_common.cuh"
-#include "tc_common.cuh"
 
 namespace mlstm {
 
@@ -238,7 +237,7 @@ struct RowLoads {
 // shared memory); `only`: the CTA's one item where segments are not taken in turn.
 __device__ __forceinline__ int next_item(const ScanArgs& a, int only, bool first, int total, int* box) {
   __syncthreads();
-  if (threadIdx.x == 0) *box = a.in_turn ? (int)atomicAdd(a.turn, 1u) : first ? only : total;
+  if (threadIdx.x == 0) *box = a.in_turn ? (int)atomicAdd(a.turn + kTurnNext, 1u) : first ? only : total;
   __syncthreads();
   return *box;
 }
@@ -246,24 +245,9 @@ __device__ __forceinline__ int next_item(const ScanArgs& a, int only, bool first
 // Waits until `tile` has finished `count` segments; false if the wait was given up.  `box` is not
 // next_item's: its slow readers may not be through.
 __device__ __forceinline__ bool wait_turn(const ScanArgs& a, int tile, unsigned int count,
-                                          const tc::Abort& abort, int* box) {
-  if (threadIdx.x == 0) {
-    const unsigned int* done = a.turn + 1 + tile;
-    bool ok = true;
-    const uint64_t t0 = tc::global_timer_ns();
-    for (unsigned int i = 1;; ++i) {
-      unsigned int v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
-      if (v >= count) break;
-      if ((i & 63) == 0 && (abort.raised() || tc::global_timer_ns() - t0 > tc::kWaitTimeoutNs)) {
-        abort.raise();
-        ok = false;
-        break;
-      }
-      __nanosleep(200);
-    }
-    *box = ok;
-  }
+                                          unsigned int* failures, int* box) {
+  if (threadIdx.x == 0)
+    *box = wait_at_least(a.turn + kTurnTiles + tile, count, LaunchAbort{a.turn + kTurnAbort, failures}, 200);
   __syncthreads();
   return *box != 0;
 }
@@ -273,7 +257,7 @@ __device__ __forceinline__ void pass_turn(const ScanArgs& a, int tile) {
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0)
-    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.turn + 1 + tile) : "memory");
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.turn + kTurnTiles + tile) : "memory");
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* gmem) {

@@ -17,7 +17,6 @@
 // With few rows the sequence is cut into segments that are scanned at once.  A first pass finds
 // each segment's state from zero and its sum of delta; segment j then starts from
 // sum_i exp(A sum of delta over i + 1 .. j - 1) state_i, which each CTA adds up for itself.
-#include "internal.h"
 #include "scan_common.cuh"
 
 namespace mlstm {
@@ -29,7 +28,7 @@ constexpr int kTile = 32;
 constexpr int kThreads = 64;
 constexpr int kCtas = 8;  // of an SM
 constexpr int kSlots = 148 * kCtas;
-__device__ unsigned int g_scan_fwd_error = 0;  // epoch of the last launch that gave up a wait
+__device__ unsigned int g_scan_fwd_failures = 0;  // launches that gave up a wait
 
 template <int LPC>
 struct Shape {
@@ -59,7 +58,7 @@ struct TileLoads {
 
 template <typename T, int LPC, bool GATE, bool WIDE>
 __global__ void __launch_bounds__(kThreads, kCtas)
-    scan_fwd_kernel(ScanArgs a, int tiles, unsigned int epoch) {
+    scan_fwd_kernel(ScanArgs a, int tiles) {
   using S = Shape<LPC>;
   constexpr int NP = S::NP, CT = S::CT, VECS = S::VECS, ITEMS = S::ITEMS;
   __shared__ __align__(16) float sd[kTile * VECS * kPairUnit];  // delta, delta x
@@ -70,7 +69,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const Lanes<LPC> l(tid);
   const int nl = l.nl;
   __shared__ int box[2];
-  const tc::Abort abort{&g_scan_fwd_error, epoch};
   const int per_seg = a.B * a.G * tiles, NC = (a.T + kScanEvery - 1) / kScanEvery;
   for (bool once = true;; once = false) {
   const int work = next_item(a, blockIdx.x, once, per_seg * a.segs, box);
@@ -80,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const ChannelTile q = channel_tile(a, bi % (tiles * a.G), tiles, CT);
   const int first = seg * a.seg_len, last = min(first + a.seg_len, a.T);
   const bool handed = a.in_turn && seg > 0;  // the segment before hands its state on
-  if (handed && !wait_turn(a, bi, seg, abort, box + 1)) return;
+  if (handed && !wait_turn(a, bi, seg, &g_scan_fwd_failures, box + 1)) return;
   float2 A2[2][2], h[2][2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -497,13 +495,13 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t s) {
   }
   const int tiles = (a.D / a.G + Shape<LPC>::CT - 1) / Shape<LPC>::CT;
   const long long items = (long long)a.B * a.G * tiles * a.segs;
-  const unsigned grid = (unsigned)(a.in_turn && items > kSlots ? kSlots : items), epoch = next_epoch();
+  const unsigned grid = (unsigned)(a.in_turn && items > kSlots ? kSlots : items);
   if (a.z.p != nullptr) {
-    if (a.wide) scan_fwd_kernel<T, LPC, true, true><<<grid, kThreads, 0, s>>>(a, tiles, epoch);
-    else scan_fwd_kernel<T, LPC, true, false><<<grid, kThreads, 0, s>>>(a, tiles, epoch);
+    if (a.wide) scan_fwd_kernel<T, LPC, true, true><<<grid, kThreads, 0, s>>>(a, tiles);
+    else scan_fwd_kernel<T, LPC, true, false><<<grid, kThreads, 0, s>>>(a, tiles);
   } else {
-    if (a.wide) scan_fwd_kernel<T, LPC, false, true><<<grid, kThreads, 0, s>>>(a, tiles, epoch);
-    else scan_fwd_kernel<T, LPC, false, false><<<grid, kThreads, 0, s>>>(a, tiles, epoch);
+    if (a.wide) scan_fwd_kernel<T, LPC, false, true><<<grid, kThreads, 0, s>>>(a, tiles);
+    else scan_fwd_kernel<T, LPC, false, false><<<grid, kThreads, 0, s>>>(a, tiles);
   }
   return cudaGetLastError();
 }
@@ -543,6 +541,8 @@ cudaError_t by_type(const ScanArgs& a, cudaStream_t s) {
   return a.dtype == 0 ? by_states<P, bf16>(a, s) : by_states<P, float>(a, s);
 }
 
+__global__ void selftest_kernel(unsigned int* words) { selftest_wait(words, &g_scan_fwd_failures); }
+
 }  // namespace
 
 ScanSegments scan_cut(int T, int tile, long long ctas, int slots) {
@@ -573,8 +573,12 @@ ScanSegments scan_fwd_segments(int B, int T, int D, int G, int N) {
   return scan_cut(T, kTile, (long long)B * G * ((D / G + CT - 1) / CT), kSlots);
 }
 
+cudaError_t launch_scan_fwd_selftest(unsigned int* words, cudaStream_t s) {
+  selftest_kernel<<<1, 1, 0, s>>>(words);
+  return cudaGetLastError();
+}
 cudaError_t fetch_scan_fwd_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_scan_fwd_error, sizeof(unsigned int));
+  return cudaMemcpyFromSymbol(flag, g_scan_fwd_failures, sizeof(unsigned int));
 }
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s) { return by_type<kFwd>(a, s); }
