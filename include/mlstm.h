@@ -324,10 +324,13 @@ int mlstm_dstate_chain(const void* dstate_local, const void* dstate_out, const v
  * CUDA error, else MLSTM_OK.  Each failure is reported once.  A failure stays
  * within its own launch: each launch carries its own abort epoch, so the
  * launches after a failed one run normally whether or not this call is made
- * in between.  The call reads the kernels' failure flags without clearing
- * them, so it does not disturb kernels running on other streams; a failure of
- * a launch on another stream of the same device is reported too.  This is the
- * one call that blocks. */
+ * in between.  A captured launch of a tensor-core kernel keeps its epoch: once
+ * it has given up, its replays return at once with invalid outputs until this
+ * call has reported them, and run normally after it.  The call takes and
+ * clears the kernels' failure flags in one step; a failure of a launch on
+ * another stream of the same device is reported too, and a second time if
+ * other CTAs of that launch give up after the call.  This is the one call that
+ * blocks. */
 int mlstm_device_status(void* stream);
 
 /* Self-test of the failure report: enqueue one tiny kernel whose bounded wait

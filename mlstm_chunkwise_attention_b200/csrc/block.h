@@ -96,9 +96,10 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_reverse_segments(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t s);
-// How many launches of a family gave up a wait (see LaunchAbort), and one that does: `words` are two, zero.
-cudaError_t fetch_scan_fwd_error(unsigned int* flag);
-cudaError_t fetch_scan_bwd_error(unsigned int* flag);
+// Where a family counts its launches that gave up a wait (see LaunchAbort), and a launch that does: `words`
+// are two, zero.
+cudaError_t scan_fwd_flag(unsigned int** at);
+cudaError_t scan_bwd_flag(unsigned int** at);
 cudaError_t launch_scan_fwd_selftest(unsigned int* words, cudaStream_t s);
 cudaError_t launch_scan_bwd_selftest(unsigned int* words, cudaStream_t s);
 
@@ -122,7 +123,7 @@ cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s);
 long long norm_sequence_items(int B, int T, int NH, int d);
 size_t norm_sequence_workspace(int B, int T, int NH, int d, int dtype, bool backward);
 cudaError_t launch_norm_sequence(const NormArgs& a, bool backward, cudaStream_t s);
-cudaError_t fetch_norm_error(unsigned int* flag);
+cudaError_t norm_flag(unsigned int** at);
 cudaError_t launch_norm_selftest(unsigned int* words, cudaStream_t s);
 // Groups that fit the shared memory of a cluster (norm_resident.cu); false: norm_sequence.cu takes them.
 bool norm_resident_workspace(int B, int T, int NH, int d, int dtype, bool gated, bool backward, size_t* bytes);

@@ -112,8 +112,7 @@ cudaError_t launch_dv_simt(const Problem& p, const BwdArgs& a, cudaStream_t s);
 
 // Abort epoch for the next launch of a tensor-core kernel: a process-wide launch
 // counter, never 0 (see tc::Abort).  Each kernel family keeps a device flag that
-// holds the epoch of its last launch that gave up; fetch_tc_*_error read it
-// without clearing it.
+// holds the epoch of its last launch that gave up, or 0; *_flag give its place.
 unsigned int next_epoch();
 
 // tensor-core kernels (tc_*.cu) and their host helpers (tmap.cu)
@@ -123,11 +122,11 @@ bool make_tmap_3d_bf16_rows(void* map, const void* base, uint64_t inner, uint64_
                             uint64_t outer, uint32_t box_inner, uint32_t box_mid);
 bool output_fwd_tc_supported(const Problem& p);
 cudaError_t launch_output_fwd_tc(const Problem& p, const FwdArgs& a, cudaStream_t s);
-cudaError_t fetch_tc_fwd_error(unsigned int* flag);
+cudaError_t tc_fwd_flag(unsigned int** at);
 cudaError_t launch_selftest_timeout(cudaStream_t s);
 bool output_fwd_xl_supported(const Problem& p);
 cudaError_t launch_output_fwd_xl(const Problem& p, const FwdArgs& a, cudaStream_t s);
-cudaError_t fetch_tc_fwd_xl_error(unsigned int* flag);
+cudaError_t tc_fwd_xl_flag(unsigned int** at);
 bool intra_bwd_tc_supported(const Problem& p);
 cudaError_t launch_dq_tc(const Problem& p, const BwdArgs& a, cudaStream_t s);
 cudaError_t launch_dk_tc(const Problem& p, const BwdArgs& a, cudaStream_t s);
@@ -138,8 +137,8 @@ cudaError_t launch_bwd_xl_table(const Problem& p, const BwdArgs& a, cudaStream_t
 cudaError_t launch_dq_xl(const Problem& p, const BwdArgs& a, cudaStream_t s);
 cudaError_t launch_dk_xl(const Problem& p, const BwdArgs& a, cudaStream_t s);
 cudaError_t launch_dv_xl(const Problem& p, const BwdArgs& a, cudaStream_t s);
-cudaError_t fetch_tc_bwd_error(unsigned int* flag);
-cudaError_t fetch_tc_bwd_xl_error(unsigned int* flag);
+cudaError_t tc_bwd_flag(unsigned int** at);
+cudaError_t tc_bwd_xl_flag(unsigned int** at);
 bool state_tc_supported(const Problem& p);
 cudaError_t launch_state_fwd_tc(const Problem& p, const FwdArgs& a, cudaStream_t s);
 cudaError_t launch_state_bwd_tc(const Problem& p, const BwdArgs& a, cudaStream_t s);
@@ -147,13 +146,13 @@ cudaError_t launch_state_bwd_tc(const Problem& p, const BwdArgs& a, cudaStream_t
 bool state_split_needed(const Problem& p);
 cudaError_t launch_state_fwd_fix(const Problem& p, const FwdArgs& a, cudaStream_t s);
 cudaError_t launch_state_bwd_fix(const Problem& p, const BwdArgs& a, cudaStream_t s);
-cudaError_t fetch_tc_state_error(unsigned int* flag);
+cudaError_t tc_state_flag(unsigned int** at);
 bool bwd_walk_supported(const Problem& p);
 cudaError_t launch_bwd_walk(const Problem& p, const BwdArgs& a, cudaStream_t s);
-cudaError_t fetch_tc_walk_error(unsigned int* flag);
+cudaError_t tc_walk_flag(unsigned int** at);
 bool fwd_walk_supported(const Problem& p);
 cudaError_t launch_fwd_walk(const Problem& p, const FwdArgs& a, cudaStream_t s);
-cudaError_t fetch_tc_fwalk_error(unsigned int* flag);
+cudaError_t tc_fwalk_flag(unsigned int** at);
 
 // recurrent-form kernels (recurrent.cu)
 cudaError_t launch_final_state(const Problem& p, const void* k, const void* v, const float* b,

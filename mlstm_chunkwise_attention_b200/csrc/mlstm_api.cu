@@ -754,14 +754,23 @@ const char* mlstm_last_error(void) { return g_last_error; }
 }  // extern "C"
 
 namespace {
-// Failures already reported, per device and kernel family: the flag values
-// mlstm_device_status saw last.  A tensor-core family's flag holds the epoch of
-// its last launch that gave up, a family's of mlstm_block.h the number of those
-// launches, so a value that differs from the last one seen is a failure not yet
-// reported.
-constexpr int kFlagDevices = 64, kFlagFamilies = 10;
-std::mutex g_flag_mu;
-unsigned int g_flag_seen[kFlagDevices][kFlagFamilies] = {};
+// The failure flags of the kernel families: a tensor-core family's holds the
+// epoch of its last launch that gave up, one's of mlstm_block.h the number of
+// its launches that did; 0: none.  They are taken and cleared in one step, so no
+// failure is lost or reported twice, and a captured launch, which keeps its
+// epoch, is not taken for failed when it is replayed after the report.
+struct Flags {
+  unsigned int* at[10];
+};
+constexpr int kFlags = sizeof(Flags) / sizeof(unsigned int*);
+__device__ unsigned int g_found;  // whether the last take_flags_kernel found one raised
+std::mutex g_found_mu;            // from that kernel to the copy of what it found
+
+__global__ void take_flags_kernel(Flags f) {
+  const unsigned int v = threadIdx.x < kFlags ? atomicExch(f.at[threadIdx.x], 0u) : 0u;
+  const bool any = __any_sync(0xffffffffu, v != 0);
+  if (threadIdx.x == 0) g_found = any;
+}
 }  // namespace
 
 extern "C" {
@@ -769,31 +778,27 @@ extern "C" {
 int mlstm_device_status(void* stream) {
   int st = cuda_status(cudaStreamSynchronize((cudaStream_t)stream), "stream synchronize");
   if (st != MLSTM_OK) return st;
-  int dev = 0;
-  st = cuda_status(cudaGetDevice(&dev), "device");
-  if (st != MLSTM_OK) return st;
-  if (dev < 0 || dev >= kFlagDevices) return MLSTM_ERR_UNSUPPORTED;
-  // read every flag before deciding anything; nothing is cleared
-  typedef cudaError_t (*Fetch)(unsigned int*);
-  const Fetch fetch[kFlagFamilies] = {mlstm::fetch_tc_fwd_error,    mlstm::fetch_tc_bwd_error,
-                                      mlstm::fetch_tc_state_error,  mlstm::fetch_tc_fwd_xl_error,
-                                      mlstm::fetch_tc_walk_error,   mlstm::fetch_tc_fwalk_error,
-                                      mlstm::fetch_tc_bwd_xl_error, mlstm::fetch_scan_fwd_error,
-                                      mlstm::fetch_scan_bwd_error, mlstm::fetch_norm_error};
-  unsigned int flag[kFlagFamilies] = {};
-  for (int i = 0; i < kFlagFamilies; ++i) {
-    st = cuda_status(fetch[i](&flag[i]), "device error flag");
+  typedef cudaError_t (*Place)(unsigned int**);
+  const Place place[kFlags] = {mlstm::tc_fwd_flag,   mlstm::tc_bwd_flag,    mlstm::tc_state_flag,
+                               mlstm::tc_fwd_xl_flag, mlstm::tc_walk_flag,  mlstm::tc_fwalk_flag,
+                               mlstm::tc_bwd_xl_flag, mlstm::scan_fwd_flag, mlstm::scan_bwd_flag,
+                               mlstm::norm_flag};
+  Flags f;
+  for (int i = 0; i < kFlags; ++i) {
+    st = cuda_status(place[i](&f.at[i]), "device error flag");
     if (st != MLSTM_OK) return st;
   }
-  bool fresh = false;
+  unsigned int found = 0;
   {
-    std::lock_guard<std::mutex> lock(g_flag_mu);
-    for (int i = 0; i < kFlagFamilies; ++i) {
-      if (flag[i] != g_flag_seen[dev][i]) fresh = true;
-      g_flag_seen[dev][i] = flag[i];
-    }
+    // on the stream that the copy is ordered with, whatever the caller's stream
+    std::lock_guard<std::mutex> lock(g_found_mu);
+    take_flags_kernel<<<1, 32>>>(f);
+    st = cuda_status(cudaGetLastError(), "device error flags");
+    if (st == MLSTM_OK)
+      st = cuda_status(cudaMemcpyFromSymbol(&found, g_found, sizeof(found)), "device error flags");
   }
-  if (fresh) {
+  if (st != MLSTM_OK) return st;
+  if (found) {
     snprintf(g_last_error, sizeof(g_last_error), "a kernel timed out waiting");
     return MLSTM_ERR_TIMEOUT;
   }

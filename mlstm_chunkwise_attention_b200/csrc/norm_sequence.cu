@@ -569,8 +569,6 @@ cudaError_t launch_norm_selftest(unsigned int* words, cudaStream_t s) {
   selftest_kernel<<<1, 1, 0, s>>>(words);
   return cudaGetLastError();
 }
-cudaError_t fetch_norm_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_norm_failures, sizeof(unsigned int));
-}
+cudaError_t norm_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_norm_failures); }
 
 }  // namespace mlstm

@@ -486,9 +486,7 @@ cudaError_t launch_scan_bwd_selftest(unsigned int* words, cudaStream_t s) {
   selftest_kernel<<<1, 1, 0, s>>>(words);
   return cudaGetLastError();
 }
-cudaError_t fetch_scan_bwd_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_scan_bwd_failures, sizeof(unsigned int));
-}
+cudaError_t scan_bwd_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_scan_bwd_failures); }
 
 ScanBwdSizes scan_bwd_sizes(int B, int T, int D, int G, int N) {
   const int NP = scan_pad(N), CT = kWarps * 2 * 32 * 4 / NP;

@@ -577,9 +577,7 @@ cudaError_t launch_scan_fwd_selftest(unsigned int* words, cudaStream_t s) {
   selftest_kernel<<<1, 1, 0, s>>>(words);
   return cudaGetLastError();
 }
-cudaError_t fetch_scan_fwd_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_scan_fwd_failures, sizeof(unsigned int));
-}
+cudaError_t scan_fwd_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_scan_fwd_failures); }
 
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s) { return by_type<kFwd>(a, s); }
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t s) { return by_type<kStep>(a, s); }

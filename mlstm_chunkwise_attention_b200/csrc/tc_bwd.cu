@@ -707,8 +707,6 @@ cudaError_t launch_dv_tc(const Problem& p, const BwdArgs& a, cudaStream_t s) {
   return p.exp_variant() ? dispatch_kind<KDV, true>(p, a, s) : dispatch_kind<KDV, false>(p, a, s);
 }
 
-cudaError_t fetch_tc_bwd_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_tc_bwd_error, sizeof(unsigned int));
-}
+cudaError_t tc_bwd_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_tc_bwd_error); }
 
 }  // namespace mlstm

@@ -688,8 +688,6 @@ cudaError_t launch_bwd_walk(const Problem& p, const BwdArgs& a, cudaStream_t s) 
   return p.exp_variant() ? launch_walk<true>(p, a, s) : launch_walk<false>(p, a, s);
 }
 
-cudaError_t fetch_tc_walk_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_tc_walk_error, sizeof(unsigned int));
-}
+cudaError_t tc_walk_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_tc_walk_error); }
 
 }  // namespace mlstm

@@ -842,8 +842,6 @@ cudaError_t launch_dv_xl(const Problem& p, const BwdArgs& a, cudaStream_t s) {
   return p.exp_variant() ? launch_xl_kind<BX_DV, true>(p, a, s) : launch_xl_kind<BX_DV, false>(p, a, s);
 }
 
-cudaError_t fetch_tc_bwd_xl_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_tc_bwd_xl_error, sizeof(unsigned int));
-}
+cudaError_t tc_bwd_xl_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_tc_bwd_xl_error); }
 
 }  // namespace mlstm

@@ -405,8 +405,6 @@ cudaError_t launch_selftest_timeout(cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t fetch_tc_fwd_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_tc_fwd_error, sizeof(unsigned int));
-}
+cudaError_t tc_fwd_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_tc_fwd_error); }
 
 }  // namespace mlstm

@@ -642,8 +642,6 @@ cudaError_t launch_fwd_walk(const Problem& p, const FwdArgs& a, cudaStream_t s) 
   return p.exp_variant() ? launch_fwalk<true>(p, a, s) : launch_fwalk<false>(p, a, s);
 }
 
-cudaError_t fetch_tc_fwalk_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_tc_fwalk_error, sizeof(unsigned int));
-}
+cudaError_t tc_fwalk_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_tc_fwalk_error); }
 
 }  // namespace mlstm

@@ -692,8 +692,6 @@ cudaError_t launch_output_fwd_xl(const Problem& p, const FwdArgs& a, cudaStream_
   return cudaErrorInvalidValue;
 }
 
-cudaError_t fetch_tc_fwd_xl_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_tc_fwd_xl_error, sizeof(unsigned int));
-}
+cudaError_t tc_fwd_xl_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_tc_fwd_xl_error); }
 
 }  // namespace mlstm

@@ -633,8 +633,6 @@ cudaError_t launch_state_bwd_fix(const Problem& p, const BwdArgs& a, cudaStream_
   return launch_fix<true, false>(p, (bf16*)a.dC, nullptr, a.b, a.m, a.init, a.dC0, nullptr, s);
 }
 
-cudaError_t fetch_tc_state_error(unsigned int* flag) {
-  return cudaMemcpyFromSymbol(flag, g_tc_state_error, sizeof(unsigned int));
-}
+cudaError_t tc_state_flag(unsigned int** at) { return cudaGetSymbolAddress((void**)at, g_tc_state_error); }
 
 }  // namespace mlstm
