@@ -28,6 +28,15 @@ __device__ __forceinline__ float2 softplus_pair(float2 v) {
 }
 __device__ __forceinline__ float softplusf(float v) { return softplus_pair(make_float2(v, v)).x; }
 
+// A (or A log2 e) kept finite, NaN for NaN.  A = -inf is a decay of 0, which -FLT_MAX is as well, but the
+// tokens behind the end, and empty steps between segments, have a delta of 0, and 0 times infinity would
+// be NaN where such a step must leave the state as it is.
+__device__ __forceinline__ float finite_rate(float v) {
+  asm("max.NaN.f32 %0, %0, 0fFF7FFFFF;" : "+f"(v));
+  asm("min.NaN.f32 %0, %0, 0f7F7FFFFF;" : "+f"(v));
+  return v;
+}
+
 // A unit is eight channels of one token in shared memory, written by one thread with 16-byte
 // stores and read by a warp along the channels.  The padding (16 bytes to a unit) spreads eight
 // threads' 16-byte accesses over all 32 banks.

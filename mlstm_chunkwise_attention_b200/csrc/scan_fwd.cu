@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       const int n = nl * 4 + k;
       const bool on = l.ch[e] < q.n && n < a.N;
       const long long row = q.c0 + l.ch[e];
-      av[k] = on ? a.A[row * a.N + n] * kLog2e : 0.f;
+      av[k] = on ? finite_rate(a.A[row * a.N + n] * kLog2e) : 0.f;
       hv[k] = on && a.state_in != nullptr ? a.state_in[((long long)b * a.D + row) * a.N + n] : 0.f;
     }
 #pragma unroll
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_segment_kernel(ScanArgs 
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       av[k] = l.ch[e] < q.n && nl * 4 + k < a.N
-                  ? a.A[(long long)(q.c0 + l.ch[e]) * a.N + nl * 4 + k] * kLog2e
+                  ? finite_rate(a.A[(long long)(q.c0 + l.ch[e]) * a.N + nl * 4 + k] * kLog2e)
                   : 0.f;
     A2[e][0] = make_float2(av[0], av[1]);
     A2[e][1] = make_float2(av[2], av[3]);
@@ -457,6 +457,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a, unsigned per
     expand(cr[k], C);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
+      A[p] = make_float2(finite_rate(A[p].x), finite_rate(A[p].y));
       h[p] = fma2(exp2_pair(mul2(dd, A[p])), h[p], mul2(ww, B[p]));
       // Past N an infinite delta or x would add the product of infinity and nought.
       if (WIDE ? left > 0 : left > 2 * p) acc = fmaf(h[p].x, C[p].x, acc);

@@ -1,0 +1,70 @@
+"""The selective scan where its numbers leave the ordinary range: decays of 0, infinite inputs, states that
+grow or shrink by more than fp32's range within a segment, and cut forms at full width."""
+
+import pytest
+import torch
+
+from mlstm_chunkwise_attention_b200 import binding, block
+from _block_ref import close, scan64
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+INF = float("inf")
+
+
+def inputs(B, T, D, N, G=1, dtype=F32, seed=0):
+    """x, dt, A, B, C of a call, on the host."""
+    g = torch.Generator().manual_seed(seed + T + D)
+    r = lambda *s: torch.randn(*s, generator=g)
+    return [r(B, T, D).to(dtype), (0.5 * r(B, T, D)).to(dtype), -torch.exp(r(D, N)),
+            r(B, T, G, N).to(dtype), r(B, T, G, N).to(dtype)]
+
+
+def both_ways(x, dt, A, Bm, Cm, **kw):
+    y, saved, end = block.selective_scan_forward(x, dt, A, Bm, Cm, want_state=True, **kw)
+    got = block.selective_scan_backward(x, dt, A, Bm, Cm, x, saved, want_dstate=True, **kw)
+    binding.check_device()
+    return {"y": y, "end": end, **{k: v for k, v in got.items() if v is not None}}
+
+
+# ---- a decay of 0 ----------------------------------------------------------------------------------
+
+# B, T, D, N, G: less than a tile, whole tiles, several segments at once, and segments in turn
+CLOSED = [(1, 20, 16, 16, 1), (1, 32, 16, 16, 1), (2, 9, 24, 5, 2), (1, 300, 24, 16, 1), (5, 530, 256, 4, 256)]
+
+
+@pytest.mark.parametrize("size", CLOSED, ids=["b%dt%dd%dn%dg%d" % s for s in CLOSED])
+@pytest.mark.parametrize("rate", [-INF, -3e38], ids=["inf", "overflows_in_base_two"])
+def test_an_infinite_rate_is_a_decay_of_zero(size, rate):
+    """A = -inf, and a finite A whose product with log2 e is not: what A = -1e30 gives, whose decays are 0
+    as well, for every step above 1e-28 (all of these are)."""
+    t = [v.cuda() for v in inputs(*size)]
+    res = []
+    for v in (rate, -1e30):
+        A = t[2].clone()
+        A[:, size[3] // 2] = v
+        res.append(both_ways(t[0], t[1], A, *t[3:]))
+    for k in res[0]:
+        assert torch.isfinite(res[0][k]).all(), k
+        assert torch.equal(res[0][k], res[1][k]), k
+
+
+def test_an_infinite_rate_in_steps_is_that_of_a_prompt():
+    B, T, D, N = 2, 5, 24, 12
+    x, dt, A, Bm, Cm = (v.cuda() for v in inputs(B, T, D, N))
+    A[:, 3] = -INF
+    dt[:, 2] = -200.0  # softplus underflows: a step of exactly 0, which leaves the states
+    y, _, end = block.selective_scan_forward(x, dt, A, Bm, Cm, want_state=True)
+    st = torch.zeros(B, D, N, device="cuda")
+    steps = [block.selective_scan_step(x[:, i], dt[:, i], A, Bm[:, i], Cm[:, i], st) for i in range(T)]
+    binding.check_device()
+    ref = inputs(B, T, D, N)
+    ref[2][:, 3] = -1e30
+    ref[1][:, 2] = -200.0
+    want = scan64(*(v.double() for v in ref))
+    # delta of the third token is 1e-87 in 64 bits and 0 in fp32: times -1e30 no decay in either
+    for got in (y, torch.stack(steps, 1)):
+        close(got, *want["y"], 64 + T + N, "y")
+    for got in (end, st):
+        close(got, *want["state"], 64 + T + N, "state")
