@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
     for (int k = 0; k < 4; ++k) {
       const int n = nl * 4 + (k ^ perm);
       const bool on = ch[e] < q.n && n < a.N;
-      av[k] = on ? finite_rate(a.A[(long long)(q.c0 + ch[e]) * a.N + n] * kLog2e) : 0.f;
+      av[k] = on ? a.A[(long long)(q.c0 + ch[e]) * a.N + n] * kLog2e : 0.f;
       gv[k] = on && a.dstate_out != nullptr
                   ? a.dstate_out[((long long)b * a.D + q.c0 + ch[e]) * a.N + n]
                   : 0.f;
@@ -151,6 +151,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
 #pragma unroll
   for (int i = 0; i < 2; ++i)  // channels that do not exist keep a state of zero
     *reinterpret_cast<float4*>(sm + C::SAVED + (i * kThreads + tid) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+  // Where this is done moves the compiler's registers: for the gated form once before the loop took 2655 us,
+  // every eight tokens 2502 (B8 T4096 D4096 N16 bf16); for the ungated 1136 and 1160 (T2048).
+  auto finite_rates = [&] {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) A2[e][p] = make_float2(finite_rate(A2[e][p].x), finite_rate(A2[e][p].y));
+  };
+  if (!GATE) finite_rates();
   const int top = (last - 1 - first) / kTile * kTile + first;
   // the upper eight tokens of the first tile may lie behind the end; then the lower come first
   fetch_saved(top + kScanEvery < last ? top + kScanEvery : top);
@@ -192,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
       }
       fetch_saved(t0 + sub - kScanEvery);
       copies_commit();
+      if (GATE) finite_rates();
       const float* bcs = sm + C::BC + perm * C::ORDER + sub * 2 * NP + nl * 4;
       const float* dxs[2] = {sm + C::DX + (sub * VECS + cl / 8) * kPairUnit + (ch[0] % 8) * 2,
                              sm + C::DX + (sub * VECS + cl / 8) * kPairUnit + (ch[1] % 8) * 2};
@@ -320,8 +330,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
           for (int i = 0; i < 4; ++i) {
             float2 val, slope;
             slope_pair<kActSilu>(z[i], &val, &slope);
-            o[i] = mul2(mul2(g[i], fma2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), x[i], y[i])),
-                        slope);
+            if (a.skip != nullptr)
+              y[i] = fma2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), x[i], y[i]);
+            o[i] = mul2(mul2(g[i], y[i]), slope);
           }
           store_pairs<WIDE, 8>((T*)a.dz.p + b * a.dz.sb + t * a.dz.st + q.c0 + cv, o, n);
         }
@@ -335,8 +346,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
             const float2 rw = add2(d[i], *reinterpret_cast<const float2*>(sm + C::BIAS + cv + 2 * i));
             v[i] = mul2(v[i], sigmoid_pair(rw));
           }
-          o[i] = fma2(make_float2(pair.x, pair.z), sgb[i],
-                      mul2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), dy[i]));
+          o[i] = mul2(make_float2(pair.x, pair.z), sgb[i]);
+          if (a.skip != nullptr)
+            o[i] = fma2(*reinterpret_cast<const float2*>(sm + C::SKIP + cv + 2 * i), dy[i], o[i]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

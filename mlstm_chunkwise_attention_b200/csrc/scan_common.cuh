@@ -104,9 +104,10 @@ __device__ __forceinline__ void stage_pairs(const ScanArgs& a, const float2* w, 
   for (int i = 0; i < 4; ++i)
     reinterpret_cast<float4*>(unit)[i] = make_float4(d[i].x, w[i].x, d[i].y, w[i].y);
 }
-// A unit of pairs (delta, delta x).  Absent elements of x were loaded as zero.
-template <typename T>
-__device__ __forceinline__ void stage_delta(const ScanArgs& a, const Raw<T, 8>& x, const Raw<T, 8>& dt,
+// A unit of pairs (delta, delta x).  Absent elements of x were loaded as zero.  LOOK: false if one of them is
+// infinite or NaN.
+template <typename T, bool LOOK = false>
+__device__ __forceinline__ bool stage_delta(const ScanArgs& a, const Raw<T, 8>& x, const Raw<T, 8>& dt,
                                             const float* bias, bool in, int n, float* unit) {
   float2 d[4], v[4];
   expand(x, v);
@@ -115,6 +116,22 @@ __device__ __forceinline__ void stage_delta(const ScanArgs& a, const Raw<T, 8>& 
   for (int i = 0; i < 4; ++i) {
     const float2 w = mul2(d[i], v[i]);
     reinterpret_cast<float4*>(unit)[i] = make_float4(d[i].x, w.x, d[i].y, w.y);
+    v[i] = w;
+  }
+  if (!LOOK) return true;
+  // 0 times each product, NaN if one is not finite; and it is not where its delta is not
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s = fma2(v[i], make_float2(0.f, 0.f), s);
+  return s.x + s.y == 0.f;
+}
+
+// The states of a lane that do not exist are zero.
+__device__ __forceinline__ void clear_padding(float2* h, int nl, int N) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    if (nl * 4 + 2 * p >= N) h[p].x = 0.f;
+    if (nl * 4 + 2 * p + 1 >= N) h[p].y = 0.f;
   }
 }
 
@@ -132,6 +149,8 @@ __device__ __forceinline__ void enter_segment(const ScanArgs& a, int b, int c, i
                                               const float2* A2, float2* h, int perm = 0) {
   constexpr int BATCH = 6;  // segments whose loads are in flight together
   const int count = REVERSE ? a.segs - 1 - seg : seg;
+  const float2 r0 = make_float2(finite_rate(A2[0].x), finite_rate(A2[0].y)),
+               r1 = make_float2(finite_rate(A2[1].x), finite_rate(A2[1].y));
   for (int i0 = 0; i0 < count; i0 += BATCH) {
     float4 s[BATCH];
     float sum[BATCH];
@@ -150,7 +169,7 @@ __device__ __forceinline__ void enter_segment(const ScanArgs& a, int b, int c, i
     for (int k = 0; k < BATCH; ++k) {
       const float4 v = permuted(s[k], perm);
       const float2 by = make_float2(sum[k], sum[k]);
-      const float2 e0 = exp2_pair(mul2(by, A2[0])), e1 = exp2_pair(mul2(by, A2[1]));
+      const float2 e0 = exp2_pair(mul2(by, r0)), e1 = exp2_pair(mul2(by, r1));
       // a state of zero stays zero, however far a growing mode (A > 0) would have grown
       h[0].x = (h[0].x == 0.f ? 0.f : e0.x * h[0].x) + v.x;
       h[0].y = (h[0].y == 0.f ? 0.f : e0.y * h[0].y) + v.y;

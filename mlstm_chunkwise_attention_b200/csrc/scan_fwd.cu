@@ -56,7 +56,52 @@ struct TileLoads {
   Raw<T, 8> x[ITEMS], dt[ITEMS];
 };
 
-template <typename T, int LPC, bool GATE, bool WIDE>
+// The walk through a tile in which a delta or delta x is not finite, where N < NP: infinity times a B or a
+// rate of nought would make the padded states NaN, and with them y where the sum over the N states is
+// infinite.  So they are cleared after every token; otherwise the operations of scan_fwd_kernel's loop in
+// their order.  A function of its own: such tiles are rare, and a second loop in the kernel took 12 % of
+// its speed (1075 us instead of 956 at B8 T4096 D4096 N16) by the registers it left to the first.
+struct Lane {
+  float2 A2[2][2], h[2][2];
+};
+template <int LPC>
+__device__ __noinline__ Lane walk_masked(Lane s, int nl, int N, const float* d0, const float* d1, const float* bc,
+                                         float* ydst, float* keep0, float* keep1, long long keep_step, int tokens) {
+  using S = Shape<LPC>;
+  constexpr int AT_ONCE = LPC / 2;
+  float* keep[2] = {keep0, keep1};
+  const float* dsrc[2] = {d0, d1};
+#pragma unroll 1
+  for (int tg = 0; tg < kTile; tg += AT_ONCE) {
+    float acc[AT_ONCE];
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const int t = tg + u;
+      float yv[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (t % kScanEvery == 0 && t < tokens && keep[e] != nullptr)
+          *reinterpret_cast<float4*>(keep[e] + t / kScanEvery * keep_step) =
+              make_float4(s.h[e][0].x, s.h[e][0].y, s.h[e][1].x, s.h[e][1].y);
+        const float2 d = *reinterpret_cast<const float2*>(dsrc[e] + t * S::VECS * kPairUnit);
+        const float2 dd = make_float2(d.x, d.x), w = make_float2(d.y, d.y);
+        const float4 Bv = *reinterpret_cast<const float4*>(bc + t * 2 * S::NP);
+        const float4 Cv = *reinterpret_cast<const float4*>(bc + t * 2 * S::NP + S::NP);
+        s.h[e][0] = fma2(exp2_pair(mul2(dd, s.A2[e][0])), s.h[e][0], mul2(w, make_float2(Bv.x, Bv.y)));
+        s.h[e][1] = fma2(exp2_pair(mul2(dd, s.A2[e][1])), s.h[e][1], mul2(w, make_float2(Bv.z, Bv.w)));
+        clear_padding(s.h[e], nl, N);
+        const float2 v = fma2(s.h[e][1], make_float2(Cv.z, Cv.w), mul2(s.h[e][0], make_float2(Cv.x, Cv.y)));
+        yv[e] = v.x + v.y;
+      }
+      acc[u] = yv[0] + __shfl_xor_sync(0xffffffffu, yv[1], 1);
+    }
+    scatter_sum<AT_ONCE, AT_ONCE, 2>(acc, nl >> 1);
+    ydst[tg * S::VECS * kFloatUnit] = acc[0];
+  }
+  return s;
+}
+
+template <typename T, int LPC, bool GATE, bool WIDE, bool PAD>
 __global__ void __launch_bounds__(kThreads, kCtas)
     scan_fwd_kernel(ScanArgs a, int tiles) {
   using S = Shape<LPC>;
@@ -103,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       h[e][1] = make_float2(v.z, v.w);
     } else if (l.ch[e] < q.n && !a.in_turn) {
       enter_segment<NP, false>(a, b, q.c0 + l.ch[e], nl, seg, A2[e], h[e]);
+      if (PAD) clear_padding(h[e], nl, a.N);  // which an infinite input in an earlier segment made NaN
     }
   }
   for (int i = tid; i < CT; i += kThreads) {
@@ -137,11 +183,13 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   for (int t0 = first; t0 < last; t0 += kTile) {
     const TileLoads<T, ITEMS> now = next;
     Raw<T, 8> zr[ITEMS];
+    bool finite = true;
 #pragma unroll
     for (int m = 0; m < ITEMS; ++m) {
       const int item = tid + m * kThreads, t = item / VECS, cv = (item % VECS) * 8;
       if (item < kTile * VECS)
-        stage_delta<T>(a, now.x[m], now.dt[m], sbias + cv, t0 + t < last, q.n - cv, sd + item * kPairUnit);
+        finite &= stage_delta<T, PAD>(a, now.x[m], now.dt[m], sbias + cv, t0 + t < last, q.n - cv,
+                                      sd + item * kPairUnit);
     }
     if (vectors) {
       bc.store(&sbc[0][0], tid);
@@ -158,14 +206,35 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         if (item < kTile * VECS && t < last && n > 0) load_raw<WIDE>(zp + t * a.z.st + cv, zr[m], n);
       }
     }
-    __syncthreads();
+    // whether padded states need care: an infinite delta or delta x, rare
+    bool mask = false;
+    if (PAD)
+      mask = __syncthreads_or(!finite);
+    else
+      __syncthreads();
     // eight tokens, between two saved states, at a time
     constexpr int AT_ONCE = LPC / 2;  // tokens whose sums are taken together
     const float* dsrc[2] = {sd + (l.cl / 8) * kPairUnit + (l.ch[0] % 8) * 2,
                             sd + (l.cl / 8) * kPairUnit + (l.ch[1] % 8) * 2};
     float* ydst = sy + ((nl >> 1) * VECS + l.cl / 8) * kFloatUnit + l.ch[0] % 8;
+    if (PAD && mask) {
+      Lane lane = {{{A2[0][0], A2[0][1]}, {A2[1][0], A2[1][1]}}, {{h[0][0], h[0][1]}, {h[1][0], h[1][1]}}};
+      float* keep[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        keep[e] = a.saved != nullptr && l.ch[e] < q.n
+                      ? a.saved + (((long long)b * NC + t0 / kScanEvery) * a.D + q.c0 + l.ch[e]) * NP + nl * 4
+                      : nullptr;
+      lane = walk_masked<LPC>(lane, nl, a.N, dsrc[0], dsrc[1], &sbc[0][nl * 4], ydst, keep[0], keep[1],
+                              (long long)a.D * NP, last - t0);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        h[e][0] = lane.h[e][0];
+        h[e][1] = lane.h[e][1];
+      }
+    }
 #pragma unroll 1
-    for (int tg = 0; tg < kTile; tg += kScanEvery) {
+    for (int tg = PAD && mask ? kTile : 0; tg < kTile; tg += kScanEvery) {
       if (a.saved != nullptr && t0 + tg < last) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -230,12 +299,13 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         float2 x[4], o[4], z[4];
         expand(now.x[m], x);
         load_unit(sy + item * kFloatUnit, o);
-        if (GATE) expand(zr[m], z);
+        if (a.skip != nullptr)  // without one nothing is added, not 0 times an infinite x
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[i] = fma2(*reinterpret_cast<const float2*>(sskip + cv + 2 * i), x[i], o[i]);
-          if (GATE)
-            o[i] = mul2(o[i], act_pair<kActSilu>(z[i]));
+          for (int i = 0; i < 4; ++i) o[i] = fma2(*reinterpret_cast<const float2*>(sskip + cv + 2 * i), x[i], o[i]);
+        if (GATE) {
+          expand(zr[m], z);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = mul2(o[i], act_pair<kActSilu>(z[i]));
         }
         store_pairs<WIDE, 8>(yp + t * a.y.st + cv, o, n);
       }
@@ -497,12 +567,14 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t s) {
   const int tiles = (a.D / a.G + Shape<LPC>::CT - 1) / Shape<LPC>::CT;
   const long long items = (long long)a.B * a.G * tiles * a.segs;
   const unsigned grid = (unsigned)(a.in_turn && items > kSlots ? kSlots : items);
+  auto run = [&](auto* kernel) { kernel<<<grid, kThreads, 0, s>>>(a, tiles); };
+  const bool pad = a.N != Shape<LPC>::NP;
   if (a.z.p != nullptr) {
-    if (a.wide) scan_fwd_kernel<T, LPC, true, true><<<grid, kThreads, 0, s>>>(a, tiles);
-    else scan_fwd_kernel<T, LPC, true, false><<<grid, kThreads, 0, s>>>(a, tiles);
+    if (a.wide) run(pad ? scan_fwd_kernel<T, LPC, true, true, true> : scan_fwd_kernel<T, LPC, true, true, false>);
+    else run(pad ? scan_fwd_kernel<T, LPC, true, false, true> : scan_fwd_kernel<T, LPC, true, false, false>);
   } else {
-    if (a.wide) scan_fwd_kernel<T, LPC, false, true><<<grid, kThreads, 0, s>>>(a, tiles);
-    else scan_fwd_kernel<T, LPC, false, false><<<grid, kThreads, 0, s>>>(a, tiles);
+    if (a.wide) run(pad ? scan_fwd_kernel<T, LPC, false, true, true> : scan_fwd_kernel<T, LPC, false, true, false>);
+    else run(pad ? scan_fwd_kernel<T, LPC, false, false, true> : scan_fwd_kernel<T, LPC, false, false, false>);
   }
   return cudaGetLastError();
 }

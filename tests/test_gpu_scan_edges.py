@@ -68,3 +68,70 @@ def test_an_infinite_rate_in_steps_is_that_of_a_prompt():
         close(got, *want["y"], 64 + T + N, "y")
     for got in (end, st):
         close(got, *want["state"], 64 + T + N, "state")
+
+
+# ---- infinite inputs -------------------------------------------------------------------------------
+
+def close_where_finite(got, ref, mag, K, what):
+    """Infinities and NaN where the 64-bit form has them, the usual bound elsewhere."""
+    g = got.double().cpu()
+    assert torch.equal(g.isnan(), ref.isnan()), what
+    wild = ~torch.isfinite(ref)
+    assert torch.equal(g[wild].nan_to_num(0.0, INF, -INF), ref[wild].nan_to_num(0.0, INF, -INF)), what
+    assert torch.isfinite(mag[~wild]).all(), what
+    close(got.cpu()[~wild], ref[~wild], mag[~wild], K, what)
+
+
+@pytest.mark.parametrize("where", ["x", "dt"])
+@pytest.mark.parametrize("gate", [False, True], ids=["ungated", "gated"])
+@pytest.mark.parametrize("size", [(1, 40, 16, 1, 1), (2, 40, 24, 5, 2), (1, 70, 16, 12, 1), (1, 40, 16, 16, 1),
+                                  (1, 300, 24, 12, 1), (5, 530, 256, 3, 256)],
+                         ids=lambda s: "b%dt%dd%dn%dg%d" % s)
+def test_an_infinite_input_stays_infinite(size, gate, where):
+    """x or the step infinite at one token, no skip: B and C of one sign, so the formula has infinities and
+    no NaN in y and the state, in the prompt and in steps, whatever N is padded to."""
+    B, T, D, N, G = size
+    x, dt, A, Bm, Cm = inputs(*size)
+    Bm, Cm = Bm.abs() + 0.1, Cm.abs() + 0.1
+    x = x.abs() + 0.1
+    (x if where == "x" else dt)[0, 10, 3] = INF
+    z = torch.randn(B, T, D, generator=torch.Generator().manual_seed(1)) + 3.0 if gate else None
+    t = [v.cuda() for v in (x, dt, A, Bm, Cm)]
+    zd = None if z is None else z.cuda()
+    y, _, end = block.selective_scan_forward(*t, z=zd, want_state=True)
+    st = torch.zeros(B, D, N, device="cuda")
+    steps = [block.selective_scan_step(t[0][:, i], t[1][:, i], t[2], t[3][:, i], t[4][:, i], st,
+                                       z=None if z is None else zd[:, i]) for i in range(min(T, 60))]
+    binding.check_device()
+    ref = scan64(*(v.double() for v in (x, dt, A, Bm, Cm)), z=None if z is None else z.double())
+    assert ref["y"][0].isinf().any() and not ref["y"][0].isnan().any()
+    K = 64 + T + N
+    close_where_finite(y, *ref["y"], K, "y")
+    close_where_finite(end, *ref["state"], K, "state")
+    n = len(steps)
+    close_where_finite(torch.stack(steps, 1), *(v[:, :n] for v in ref["y"]), K, "steps")
+
+
+@pytest.mark.parametrize("gate", [False, True], ids=["ungated", "gated"])
+def test_an_infinite_input_without_skip_leaves_its_dx_finite(gate):
+    """dx and dz of the token whose x is infinite: no skip, so nothing is added to dx (0 times dy) and y in
+    dz is the infinite sum over states alone."""
+    B, T, D, N = 1, 40, 16, 16
+    x, dt, A, Bm, Cm = inputs(B, T, D, N)
+    Bm, Cm = Bm.abs() + 0.1, Cm.abs() + 0.1
+    x = x.abs() + 0.1
+    x[0, 10, 3] = INF
+    g = torch.Generator().manual_seed(2)
+    dy = torch.rand(B, T, D, generator=g) + 0.1
+    dy[0, 5, 7] = INF  # another channel's
+    z = torch.rand(B, T, D, generator=g) + 0.5 if gate else None
+    t = [v.cuda() for v in (x, dt, A, Bm, Cm)]
+    zd = None if z is None else z.cuda()
+    _, saved, _ = block.selective_scan_forward(*t, z=zd)
+    got = block.selective_scan_backward(*t, dy.cuda(), saved, z=zd)
+    binding.check_device()
+    ref = scan64(*(v.double() for v in (x, dt, A, Bm, Cm)), z=None if z is None else z.double(),
+                 dy=dy.double())
+    for name in ("dx", "dz") if gate else ("dx",):
+        assert not ref[name][0].isnan().any() and ref[name][0].isinf().any()
+        close_where_finite(got[name], *ref[name], 2 * (64 + T + N), name)
