@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(ScanArgs a, i
     for (int k = 0; k < 4; ++k) {
       const int n = nl * 4 + (k ^ perm);
       const bool on = ch[e] < q.n && n < a.N;
-      av[k] = on ? a.A[(long long)(q.c0 + ch[e]) * a.N + n] * kLog2e : 0.f;
+      av[k] = on ? a.A[(long long)(q.c0 + ch[e]) * a.N + n] * kLog2e : kPadRate;
       gv[k] = on && a.dstate_out != nullptr
                   ? a.dstate_out[((long long)b * a.D + q.c0 + ch[e]) * a.N + n]
                   : 0.f;

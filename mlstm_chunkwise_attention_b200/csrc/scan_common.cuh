@@ -4,7 +4,7 @@
 //
 // The exponent is kept in base two: A2 = A log2 e once per thread, one multiplication and
 // one ex2 per state and token.  Four states lie in a lane and LPC lanes (2, 4, 8 or 16) hold
-// a channel, so N is padded to 8, 16, 32 or 64; padded states have A = B = C = 0 and stay zero.
+// a channel, so N is padded to 8, 16, 32 or 64; padded states have B = C = 0 and stay zero.
 #pragma once
 
 #include "block_common.cuh"
@@ -36,6 +36,10 @@ __device__ __forceinline__ float finite_rate(float v) {
   asm("min.NaN.f32 %0, %0, 0f7F7FFFFF;" : "+f"(v));
   return v;
 }
+
+// A2 of padded states and absent channels: negative, so that an infinite delta is a decay of 0 there too
+// (with a rate of 0 it made the gradients that earlier tokens get NaN).
+constexpr float kPadRate = -1.f;
 
 // A unit is eight channels of one token in shared memory, written by one thread with 16-byte
 // stores and read by a warp along the channels.  The padding (16 bytes to a unit) spreads eight

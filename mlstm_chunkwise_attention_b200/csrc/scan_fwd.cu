@@ -56,8 +56,8 @@ struct TileLoads {
   Raw<T, 8> x[ITEMS], dt[ITEMS];
 };
 
-// The walk through a tile in which a delta or delta x is not finite, where N < NP: infinity times a B or a
-// rate of nought would make the padded states NaN, and with them y where the sum over the N states is
+// The walk through a tile in which a delta or delta x is not finite, where N < NP: infinity times a B of
+// nought would make the padded states NaN, and with them y where the sum over the N states is
 // infinite.  So they are cleared after every token; otherwise the operations of scan_fwd_kernel's loop in
 // their order.  A function of its own: such tiles are rare, and a second loop in the kernel took 12 % of
 // its speed (1075 us instead of 956 at B8 T4096 D4096 N16) by the registers it left to the first.
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       const int n = nl * 4 + k;
       const bool on = l.ch[e] < q.n && n < a.N;
       const long long row = q.c0 + l.ch[e];
-      av[k] = on ? finite_rate(a.A[row * a.N + n] * kLog2e) : 0.f;
+      av[k] = on ? finite_rate(a.A[row * a.N + n] * kLog2e) : kPadRate;
       hv[k] = on && a.state_in != nullptr ? a.state_in[((long long)b * a.D + row) * a.N + n] : 0.f;
     }
 #pragma unroll
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) scan_segment_kernel(ScanArgs 
     for (int k = 0; k < 4; ++k)
       av[k] = l.ch[e] < q.n && nl * 4 + k < a.N
                   ? finite_rate(a.A[(long long)(q.c0 + l.ch[e]) * a.N + nl * 4 + k] * kLog2e)
-                  : 0.f;
+                  : kPadRate;
     A2[e][0] = make_float2(av[0], av[1]);
     A2[e][1] = make_float2(av[2], av[3]);
   }

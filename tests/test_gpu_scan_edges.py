@@ -135,3 +135,29 @@ def test_an_infinite_input_without_skip_leaves_its_dx_finite(gate):
     for name in ("dx", "dz") if gate else ("dx",):
         assert not ref[name][0].isnan().any() and ref[name][0].isinf().any()
         close_where_finite(got[name], *ref[name], 2 * (64 + T + N), name)
+
+
+@pytest.mark.parametrize("gate", [False, True], ids=["ungated", "gated"])
+@pytest.mark.parametrize("size", [(1, 40, 16, 5, 1), (2, 40, 24, 12, 1), (1, 300, 24, 12, 1), (1, 40, 16, 16, 1)],
+                         ids=lambda s: "b%dt%dd%dn%dg%d" % s)
+def test_an_infinite_step_hands_nothing_back(size, gate):
+    """An infinite step forgets the state (its decay is 0), so the tokens before it have the gradients of the
+    sequence that ends there, however N is padded."""
+    B, T, D, N, G = size
+    at = T - 15
+    x, dt, A, Bm, Cm = inputs(*size)
+    dt[:, at] = INF
+    g = torch.Generator().manual_seed(4)
+    dy = torch.randn(B, T, D, generator=g)
+    z = torch.randn(B, T, D, generator=g) if gate else None
+    t = [v.cuda() for v in (x, dt, A, Bm, Cm)]
+    zd = None if z is None else z.cuda()
+    _, saved, _ = block.selective_scan_forward(*t, z=zd)
+    got = block.selective_scan_backward(*t, dy.cuda(), saved, z=zd)
+    binding.check_device()
+    cut = lambda v: v[:, :at].double()
+    ref = scan64(cut(x), cut(dt), A.double(), cut(Bm), cut(Cm), z=None if z is None else cut(z), dy=cut(dy))
+    for name in ("dx", "ddt", "dz", "dB", "dC"):
+        if got[name] is not None:
+            r = [v.reshape(got[name][:, :at].shape) for v in ref[name]]
+            close(got[name][:, :at].contiguous(), *r, 2 * (64 + T + N) + D // G, name)
