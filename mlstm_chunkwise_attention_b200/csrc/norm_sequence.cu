@@ -90,11 +90,18 @@ struct Work {
   float* param;  // [B, slabs, 2, NH d], or null
 };
 
-// Joins (count, mean, m2) pairs: Chan, Golub and LeVeque's pairwise update.
+// Joins (count, mean, m2) pairs: Chan, Golub and LeVeque's pairwise update.  A side without values is left
+// out: its mean says nothing, and the square of the distance to it may overflow (from 2^64 in fp32).
 template <typename F>
 __device__ __forceinline__ void join(F& n, F& mean, F& m2, F nb, F meanb, F m2b) {
+  if (nb == F(0)) return;
+  if (n == F(0)) {
+    n = nb;
+    mean = meanb;
+    m2 = m2b;
+    return;
+  }
   const F tot = n + nb;
-  if (tot == F(0)) return;
   const F d = meanb - mean, f = nb / tot;
   mean += d * f;
   m2 += m2b + d * d * n * f;
