@@ -172,13 +172,15 @@ __device__ __forceinline__ void enter_segment(const ScanArgs& a, int b, int c, i
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const float4 v = permuted(s[k], perm);
-      const float2 by = make_float2(sum[k], sum[k]);
+      const float2 by = make_float2(0.5f * sum[k], 0.5f * sum[k]);
       const float2 e0 = exp2_pair(mul2(by, r0)), e1 = exp2_pair(mul2(by, r1));
-      // a state of zero stays zero, however far a growing mode (A > 0) would have grown
-      h[0].x = (h[0].x == 0.f ? 0.f : e0.x * h[0].x) + v.x;
-      h[0].y = (h[0].y == 0.f ? 0.f : e0.y * h[0].y) + v.y;
-      h[1].x = (h[1].x == 0.f ? 0.f : e1.x * h[1].x) + v.z;
-      h[1].y = (h[1].y == 0.f ? 0.f : e1.y * h[1].y) + v.w;
+      // The decay in two halves: a whole segment's may leave fp32's range (2^-126 .. 2^128) although the state
+      // is inside it before and after; half of it does not.  And a state of zero stays zero, however far a
+      // growing mode (A > 0) would have grown.
+      h[0].x = (h[0].x == 0.f ? 0.f : e0.x * h[0].x * e0.x) + v.x;
+      h[0].y = (h[0].y == 0.f ? 0.f : e0.y * h[0].y * e0.y) + v.y;
+      h[1].x = (h[1].x == 0.f ? 0.f : e1.x * h[1].x * e1.x) + v.z;
+      h[1].y = (h[1].y == 0.f ? 0.f : e1.y * h[1].y * e1.y) + v.w;
     }
   }
 }

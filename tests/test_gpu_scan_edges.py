@@ -161,3 +161,37 @@ def test_an_infinite_step_hands_nothing_back(size, gate):
         if got[name] is not None:
             r = [v.reshape(got[name][:, :at].shape) for v in ref[name]]
             close(got[name][:, :at].contiguous(), *r, 2 * (64 + T + N) + D // G, name)
+
+
+# ---- decays beyond fp32's range --------------------------------------------------------------------
+
+@pytest.mark.parametrize("log2_decay,state", [(4.1, 2.0 ** -66), (-4.1, 2.0 ** 60)], ids=["grows", "shrinks"])
+@pytest.mark.parametrize("backwards", [False, True], ids=["state", "gradient"])
+def test_a_segments_decay_beyond_the_range_of_fp32(log2_decay, state, backwards):
+    """32 tokens, a segment where a short scan is cut at once, multiply a state by 2^131 or 2^-131 (or 16, a
+    segment of the backward, from the other end the state's gradient): more than one fp32 number holds,
+    but the state starts and ends inside its range."""
+    T, D, N, on = 128, 8, 8, 16 if backwards else 32
+    lib = binding.load()
+    assert lib.mlstm_scan_fwd_workspace_size(1, T, D, 1, N, binding.FP32) > 0, "cut into segments"
+    x = torch.zeros(1, T, D)
+    A = torch.full((D, N), 1.0 if log2_decay > 0 else -1.0)
+    one = torch.ones(1, T, 1, N)
+    dt = torch.zeros(1, T, D)
+    (dt[:, T - on:] if backwards else dt[:, :on]).fill_(abs(log2_decay) * 32 / on * 0.6931472)
+    given = torch.full((1, D, N), state)
+    t = [v.cuda() for v in (x, dt, A, one[:, :, 0], one[:, :, 0])]
+    kw = dict(softplus=False, state_in=None if backwards else given.cuda())
+    y, saved, end = block.selective_scan_forward(*t, **kw, want_state=True)
+    got = block.selective_scan_backward(*t, torch.zeros_like(y), saved, **kw, want_dstate=True,
+                                        dstate_out=given.cuda() if backwards else None)
+    binding.check_device()
+    ref = scan64(*(v.double() for v in (x, dt, A, one, one)), softplus=False,
+                 state=None if backwards else given.double(), dy=torch.zeros(1, T, D, dtype=torch.float64),
+                 dstate_out=given.double() if backwards else None)
+    K = 64 + T + N
+    if backwards:
+        close(got["dstate_in"], *ref["dstate_in"], 2 * K, "dstate_in")
+    else:
+        close(end, *ref["state"], K, "state")
+        close(y, *ref["y"], K, "y")
