@@ -29,3 +29,36 @@ def test_norm_of_values_scaled_by_a_power_of_two(T, NH, d):
     binding.check_device()
     for a, b in zip(*res):
         assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 2056])
+def test_statistics_of_values_far_from_zero_and_from_each_other(d):
+    """Group 0: one vector 2^12 from the rest.  Group 1: all values near 2^12.  The statistics against 64 bits:
+
+    - the mean is joined in 64 bits and rounded once, 2^-24 of itself, from sums whose terms are distances
+      (at most 300 additions in a row: 300 2^-24 of their mean size);
+    - the squared distances are sums of at most 300 positive terms, 2^-16 of the variance and half of it of
+      1 / deviation; but for d = 2056 a warp takes distances from one of its vectors, of which it has 512
+      at most, so where that vector is the far one (group 0) 512 times that, 2^-8.
+
+    y differs by 1 / deviation times the mean's error, that of 1 / deviation, and four roundings."""
+    B, T, NH = 1, 200, 2
+    g = torch.Generator().manual_seed(12)
+    x = torch.randn(B, T, NH * d, generator=g)
+    x[:, 0, :8] += 4096.0
+    x[:, :, d:] += 4096.0
+    y, stats = block.group_norm_forward(x.cuda(), groups=NH, scope=SEQ)
+    binding.check_device()
+    v = x.double().view(T, NH, d)
+    mean = v.mean((0, 2))
+    size = (v - mean[:, None]).abs().mean((0, 2))
+    rstd = 1 / torch.sqrt(((v - mean[:, None]) ** 2).mean((0, 2)) + 1e-5)
+    got = stats.double().cpu()[0]
+    off = 2.0 ** -24 * (mean.abs() + 300 * size)
+    rel = torch.tensor([2.0 ** -8 if d > 2048 else 2.0 ** -17, 2.0 ** -17], dtype=torch.float64) + 2.0 ** -22
+    assert ((got[:, 0] - mean).abs() <= off).all(), (got[:, 0] - mean, off)
+    assert ((got[:, 1] - rstd).abs() <= rel * rstd).all(), (got[:, 1] / rstd - 1, rel)
+    xhat = (v - mean[:, None]) * rstd[:, None]
+    bound = (rstd * off)[:, None] + (rel[:, None] + 2.0 ** -22) * (xhat.abs() + (rstd * off)[:, None])
+    err = (y.double().cpu().view(T, NH, d) - xhat).abs()
+    assert (err <= bound).all(), float((err - bound).max())

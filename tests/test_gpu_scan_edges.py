@@ -195,3 +195,69 @@ def test_a_segments_decay_beyond_the_range_of_fp32(log2_decay, state, backwards)
     else:
         close(end, *ref["state"], K, "state")
         close(y, *ref["y"], K, "y")
+
+
+# ---- the cut forms and the wide accesses -----------------------------------------------------------
+
+def test_segments_in_turn_at_full_width():
+    """16-byte accesses, many live channels to a tile, B and C shared by all tiles: the training form, long
+    enough for segments in turn in both directions (1280 tiles forward, 640 backward; two segments, the last
+    one ragged).  The 64-bit form runs on the GPU."""
+    B, T, D, N, G = 10, 530, 4096, 16, 1
+    lib = binding.load()
+    # in turn: the handed state [B, D, 16] and the counters; at once would hold two segments' states
+    assert lib.mlstm_scan_fwd_workspace_size(B, T, D, G, N, binding.BF16) == B * D * 16 * 4 + 5376  # 1282 words
+    g = torch.Generator("cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, dt, z, dy = r(B, T, D).to(BF), (0.5 * r(B, T, D)).to(BF), r(B, T, D).to(BF), r(B, T, D).to(BF)
+    A, Bm, Cm = -torch.exp(r(D, N)), r(B, T, G, N).to(BF), r(B, T, G, N).to(BF)
+    skip, bias, st, dso = r(D), r(D) - 2.0, r(B, D, N), r(B, D, N)
+    kw = dict(skip=skip, z=z, dt_bias=bias, state_in=st)
+    y, saved, end = block.selective_scan_forward(x, dt, A, Bm, Cm, **kw, want_state=True)
+    got = block.selective_scan_backward(x, dt, A, Bm, Cm, dy, saved, **kw, dstate_out=dso, want_dstate=True)
+    binding.check_device()
+    d = torch.Tensor.double
+    ref = scan64(d(x), d(dt), d(A), d(Bm), d(Cm), d(skip), d(z), d(bias), True, d(st), d(dy), d(dso))
+    ref = {k: (v.cpu(), m.cpu()) for k, (v, m) in ref.items()}
+    K = 64 + T + N
+    close(y, *ref["y"], K, "y")
+    close(end, *ref["state"], K, "state")
+    for name in ("dx", "ddt", "dstate_in", "dz"):
+        close(got[name], *ref[name], 2 * K, name)
+    for name in ("dB", "dC"):
+        close(got[name], *ref[name], 2 * K + D // G, name)
+    for name in ("dA", "dskip", "ddt_bias"):
+        close(got[name], *ref[name], 2 * K + B * T, name)
+
+
+# B, T, D, N, G, gate, dtype: more than 16 states with 16-byte accesses, whole and padded
+MANY = [(2, 100, 128, 32, 1, True, BF), (2, 100, 128, 64, 2, True, BF), (1, 300, 64, 24, 1, False, BF),
+        (1, 333, 64, 40, 1, True, BF), (2, 70, 64, 64, 1, True, F32), (1, 400, 96, 48, 2, False, F32)]
+
+
+@pytest.mark.parametrize("case", MANY, ids=["b%dt%dd%dn%dg%d" % c[:5] for c in MANY])
+def test_many_states_with_wide_accesses(case):
+    B, T, D, N, G, gate, dtype = case
+    x, dt, A, Bm, Cm = inputs(B, T, D, N, G, dtype)
+    g = torch.Generator().manual_seed(6)
+    r = lambda *s: torch.randn(*s, generator=g)
+    dy, z, skip, bias = r(B, T, D).to(dtype), r(B, T, D).to(dtype) if gate else None, r(D), r(D) - 2.0
+    st, dso = r(B, D, N), r(B, D, N)
+    cuda = lambda v: None if v is None else v.cuda()
+    t = [v.cuda() for v in (x, dt, A, Bm, Cm)]
+    kw = dict(skip=cuda(skip), z=cuda(z), dt_bias=cuda(bias), state_in=cuda(st))
+    y, saved, end = block.selective_scan_forward(*t, **kw, want_state=True)
+    got = block.selective_scan_backward(*t, dy.cuda(), saved, **kw, dstate_out=dso.cuda(), want_dstate=True)
+    binding.check_device()
+    d = lambda v: None if v is None else v.double()
+    ref = scan64(d(x), d(dt), d(A), d(Bm), d(Cm), d(skip), d(z), d(bias), True, d(st), d(dy), d(dso))
+    K = 64 + T + N
+    close(y, *ref["y"], K, "y")
+    close(end, *ref["state"], K, "state")
+    for name in ("dx", "ddt", "dstate_in", "dz"):
+        if got[name] is not None:
+            close(got[name], *ref[name], 2 * K, name)
+    for name in ("dB", "dC"):
+        close(got[name], *ref[name], 2 * K + D // G, name)
+    for name in ("dA", "dskip", "ddt_bias"):
+        close(got[name], *ref[name], 2 * K + B * T, name)
