@@ -382,7 +382,9 @@ __global__ void __launch_bounds__(kThreads + 64, BWD ? 2 : 3)
         const float off = cnt > 0.f ? sum / cnt : 0.f;
         red[i & 1][warp][0] = cnt;
         red[i & 1][warp][1] = off - neg.x;
-        red[i & 1][warp][2] = fmaxf(sq - off * sum, 0.f);
+        // squares beyond fp32's range stay infinite, as in the other kernels: their difference would be NaN,
+        // and fmaxf would make that a variance of 0
+        red[i & 1][warp][2] = sq < INFINITY ? fmaxf(sq - off * sum, 0.f) : sq;
       }
     } else if (!BWD) {
       // -- forward, second reading

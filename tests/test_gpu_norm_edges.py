@@ -62,3 +62,16 @@ def test_statistics_of_values_far_from_zero_and_from_each_other(d):
     bound = (rstd * off)[:, None] + (rel[:, None] + 2.0 ** -22) * (xhat.abs() + (rstd * off)[:, None])
     err = (y.double().cpu().view(T, NH, d) - xhat).abs()
     assert (err <= bound).all(), float((err - bound).max())
+
+
+@pytest.mark.parametrize("T,d", [(40, 64), (3, 2056), (300, 4096)])
+def test_norm_of_squares_beyond_the_range_of_fp32(T, d):
+    """Distances from the mean near 2^66: the variance is infinite in fp32 and 1 / deviation 0, in the kernel
+    for large groups as in the one for small ones, and the output is the bias."""
+    x = torch.full((1, T, d), 2.0 ** 66, device="cuda")
+    x[:, 0, :8] = 0.0  # the vector from which a warp takes its distances
+    x[:, T // 2:, ::2] = 0.0
+    b = torch.linspace(-1, 1, d, device="cuda")
+    y, stats = block.group_norm_forward(x, None, b, groups=1, scope=SEQ)
+    binding.check_device()
+    assert float(stats[0, 0, 1]) == 0.0 and torch.equal(y, b.expand_as(y))
