@@ -146,6 +146,16 @@ __device__ __forceinline__ float4 permuted(float4 v, int perm) {
   return v;
 }
 
+// v held to -126 .. 127, the exponents of fp32's normal numbers; NaN for NaN.
+__device__ __forceinline__ float held_exponent(float v) {
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(v));
+  asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(v));
+  return v;
+}
+__device__ __forceinline__ float2 held_exponents(float2 v) {
+  return make_float2(held_exponent(v.x), held_exponent(v.y));
+}
+
 // The state (or, REVERSE, the state's gradient) that enters segment `seg`, from what enters the
 // first (last) one in h and the segments between; A2 and h hold state i ^ perm at i.
 template <int NP, bool REVERSE>
@@ -153,8 +163,9 @@ __device__ __forceinline__ void enter_segment(const ScanArgs& a, int b, int c, i
                                               const float2* A2, float2* h, int perm = 0) {
   constexpr int BATCH = 6;  // segments whose loads are in flight together
   const int count = REVERSE ? a.segs - 1 - seg : seg;
-  const float2 r0 = make_float2(finite_rate(A2[0].x), finite_rate(A2[0].y)),
-               r1 = make_float2(finite_rate(A2[1].x), finite_rate(A2[1].y));
+  const float2 half = make_float2(0.5f, 0.5f),
+               r0 = mul2(make_float2(finite_rate(A2[0].x), finite_rate(A2[0].y)), half),
+               r1 = mul2(make_float2(finite_rate(A2[1].x), finite_rate(A2[1].y)), half);
   for (int i0 = 0; i0 < count; i0 += BATCH) {
     float4 s[BATCH];
     float sum[BATCH];
@@ -172,15 +183,14 @@ __device__ __forceinline__ void enter_segment(const ScanArgs& a, int b, int c, i
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const float4 v = permuted(s[k], perm);
-      const float2 by = make_float2(0.5f * sum[k], 0.5f * sum[k]);
-      const float2 e0 = exp2_pair(mul2(by, r0)), e1 = exp2_pair(mul2(by, r1));
+      const float2 by = make_float2(sum[k], sum[k]);
       // The decay in two halves: a whole segment's may leave fp32's range (2^-126 .. 2^128) although the state
-      // is inside it before and after; half of it does not.  And a state of zero stays zero, however far a
-      // growing mode (A > 0) would have grown.
-      h[0].x = (h[0].x == 0.f ? 0.f : e0.x * h[0].x * e0.x) + v.x;
-      h[0].y = (h[0].y == 0.f ? 0.f : e0.y * h[0].y * e0.y) + v.y;
-      h[1].x = (h[1].x == 0.f ? 0.f : e1.x * h[1].x * e1.x) + v.z;
-      h[1].y = (h[1].y == 0.f ? 0.f : e1.y * h[1].y * e1.y) + v.w;
+      // is inside it before and after; half of it does not.  Held at 2^-252 and 2^254 in all, so that a state
+      // of zero stays zero, however far it would have grown, and an infinite one infinite.
+      const float2 e0 = exp2_pair(held_exponents(mul2(by, r0))),
+                   e1 = exp2_pair(held_exponents(mul2(by, r1)));
+      h[0] = fma2(mul2(e0, h[0]), e0, make_float2(v.x, v.y));
+      h[1] = fma2(mul2(e1, h[1]), e1, make_float2(v.z, v.w));
     }
   }
 }

@@ -261,3 +261,20 @@ def test_many_states_with_wide_accesses(case):
         close(got[name], *ref[name], 2 * K + D // G, name)
     for name in ("dA", "dskip", "ddt_bias"):
         close(got[name], *ref[name], 2 * K + B * T, name)
+
+
+def test_an_infinite_state_crosses_segments():
+    """A decay of 2^-43 a token leaves an infinite state infinite in every token, so in every segment too,
+    although a segment's decay is far below fp32's smallest number."""
+    B, T, D, N = 1, 300, 24, 16
+    x, dt, _, Bm, Cm = inputs(B, T, D, N)
+    x, Bm, Cm = x.abs() + 0.1, Bm.abs() + 0.1, Cm.abs() + 0.1
+    x[0, 3, 5] = INF
+    A, dt = torch.full((D, N), -30.0), torch.ones(B, T, D)
+    y, _, end = block.selective_scan_forward(*(v.cuda() for v in (x, dt, A, Bm, Cm)), softplus=False,
+                                             want_state=True)
+    binding.check_device()
+    ref = scan64(*(v.double() for v in (x, dt, A, Bm, Cm)), softplus=False)
+    assert ref["y"][0][0, 3:, 5].isinf().all() and ref["y"][0].isinf().sum() == T - 3
+    close_where_finite(y, *ref["y"], 64 + T + N, "y")
+    close_where_finite(end, *ref["state"], 64 + T + N, "state")
