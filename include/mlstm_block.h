@@ -23,7 +23,11 @@
  *
  * Types.  Activations and their gradients are in the one I/O dtype
  * (MLSTM_BF16 or MLSTM_FP32); parameters, their gradients and the scan's
- * states are fp32.  All arithmetic is fp32, rounded once to the I/O dtype.
+ * states are fp32.  All arithmetic is fp32, rounded once to the I/O dtype; sums
+ * over tokens are fp32 too, of partial sums over some hundred tokens each.
+ * Exponentials are the hardware's (relative error 2^-22) of an argument
+ * rounded to fp32: a decay of the scan, exp(delta A), is good to
+ * (1 + 2 |delta A|) 2^-22.
  *
  * Strided tensors.  Activations are passed with their strides, so a slice of
  * a projection or a head-major tensor is read or written in place.  The last
@@ -105,6 +109,9 @@ int mlstm_conv_step(const mlstm_rows_t* x, const float* weight, const float* bia
  * NULL: no gate.  state_in, state_out [B, D, N] fp32 contiguous, the state
  * before the first and after the last token; NULL: zeros / not wanted.  States,
  * saved and workspaces are 16-byte aligned.
+ * a may be -infinity: a decay of 0.  Infinite and NaN inputs reach y and the
+ * states as the formula in fp32 has them, and no other channel or batch but through b
+ * and c; gradients that the formula makes infinite may be NaN.
  * ------------------------------------------------------------------------- */
 typedef struct {
   mlstm_rows_t x, dt, z, b, c;
@@ -114,7 +121,8 @@ typedef struct {
 } mlstm_scan_t;
 
 /* Bytes of `saved` that mlstm_scan_fwd fills and mlstm_scan_bwd reads: the
- * states entering every eighth token, fp32 (0 on an argument error). */
+ * states entering every eighth token, fp32, N rounded up to 8, 16, 32 or 64
+ * (0 on an argument error). */
 size_t mlstm_scan_saved_size(int B, int T, int D, int G, int N, int dtype);
 
 /* Bytes of workspace mlstm_scan_fwd needs; may be 0, and then the workspace
@@ -127,7 +135,10 @@ size_t mlstm_scan_fwd_workspace_size(int B, int T, int D, int G, int N, int dtyp
 int mlstm_scan_fwd(const mlstm_scan_t* p, const mlstm_rows_t* y, void* saved, float* state_out,
                    void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace mlstm_scan_bwd needs (0 on an argument error). */
+/* Bytes of workspace mlstm_scan_bwd needs (0 on an argument error).  Most of
+ * it holds shares of db and dc, fp32, one for each tile of channels (64 of them
+ * for 9 to 16 states; 128, 32, 16 for up to 8, 32, 64): 8 bytes for each token,
+ * tile and rounded-up state. */
 size_t mlstm_scan_bwd_workspace_size(int B, int T, int D, int G, int N, int dtype);
 
 /* Gradients of the scan; NULL data: that output is not wanted, except dx, ddt,
@@ -164,7 +175,8 @@ int mlstm_scan_step(const mlstm_scan_t* p, const mlstm_rows_t* y, float* state_o
  *
  * weight, bias [NH d] or NULL (1 / 0).  eps > 0.  stats: fp32 pairs (mean,
  * 1 / sqrt(var + eps)), [B, T, NH, 2] or [B, NH, 2], written by the forward
- * (NULL: not wanted) and read by the backward.
+ * (NULL: not wanted) and read by the backward; T = 0 leaves them as they were.
+ * Over a sequence a variance beyond fp32's range gives 1 / sqrt(var) = 0.
  * ------------------------------------------------------------------------- */
 size_t mlstm_group_norm_stats_size(int B, int T, int NH, int d, int scope);
 

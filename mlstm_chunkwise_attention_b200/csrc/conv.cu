@@ -13,16 +13,18 @@
 // projection is read in place, and y can be written head-major.
 //
 // Measured on one B200 at B8 T4096 D4096 W4 bf16 with SiLU: forward 103 us, 5.2 TB/s or 0.80 of
-// a plain copy; backward with its parameter sums 176 us, 4.6 TB/s or 0.71: there the fp32 pipe
-// (16 multiply-adds and a sigmoid's slope an element) is the next bound.
+// a plain copy; backward with its parameter sums 176 us, 4.6 TB/s or 0.71, where 0.57 of the cycles issue
+// and the fp32 pipe stands at 0.47: few warps (126 registers) between memory and the arithmetic.  fp32: 177
+// and 260 us, 6.1 and 6.2 TB/s.
 #include "block_common.cuh"
 
 namespace mlstm {
 
 namespace {
 
-// A thread's channels: two packed pairs.  Four channels keep a thread's registers low enough for
-// half the SM's warps (eight took 128 registers, 22 % of the warps and 2.2 TB/s).
+// A thread's channels: two packed pairs.  With eight the forward took 128 registers, 22 % of the SM's warps
+// and 2.2 TB/s; with four it takes 70 and has 37 % of them.  The backward, with windows of x and dp and its
+// sums, takes 126 (23 %) with four.
 constexpr int kC = 4, kPairs = kC / 2;
 
 // Channels c0 .. c0 + 3 of token t, where t < 0 is the carried state (or zero).

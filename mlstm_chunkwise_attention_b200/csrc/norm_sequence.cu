@@ -4,16 +4,19 @@
 // Bound by HBM: the statistics need every value before the first output, so x (in the backward x and
 // dy) is read twice, and a plain second pass reads it from memory again.  Here one persistent kernel
 // works through a queue: the sums of one chunk of groups, then the next chunk's sums, then the first
-// chunk's outputs, and so on, so that the second reading of a chunk finds it in L2 (two chunks and what
-// is written between them stay far below its 126 MB).  CTAs take items from a counter in this order.
+// chunk's outputs, and so on, so that the second reading of a chunk finds some of it in L2.  Between a
+// chunk's two readings lie the next chunk's, and the last chunk's second reading and output: at T8192 d256
+// bf16 (chunks of 448 items of 64 KB) about 117 MB, and the 126 MB of L2 served half of the forward's
+// second readings and two thirds of the backward's (198 MB read for a tensor of 134, 357 for 268).  A
+// single group larger than L2 is read from memory twice.  CTAs take items from a counter in this order.
 // An output item waits for its group's sums, all of which were taken earlier by CTAs that run, so some
 // CTA can always go on; the wait is bounded like those of the tensor-core kernels.
 //
 // Means and variances are joined as (count, mean, sum of squared distances), never as a difference of
 // squares, and in a fixed order whoever comes last.
 //
-// Measured on one B200 at B4 T8192 NH16 d256 bf16 with SiLU: forward 150 us, backward 304 us (0.55 and
-// 0.41 of a plain copy of the tensors moved once).  A second pass over memory took 165 and 324 us at
+// Measured on one B200 at B4 T8192 NH16 d256 bf16 with SiLU: forward 144 us, backward 299 us (0.57 and
+// 0.42 of a plain copy of the tensors moved once); one group of 268 MB (T32768 d4096): 214 and 450 us.  A second pass over memory took 165 and 324 us at
 // its best; a chunk of half or twice as many items as CTAs 206 / 349 and 175 / 327 us (waits; L2).
 // What bounds it now is the issue of instructions between the barriers (0.5 to 0.6 of the cycles).
 #include "norm_common.cuh"

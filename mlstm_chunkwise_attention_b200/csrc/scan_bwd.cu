@@ -14,10 +14,11 @@
 // Each CTA writes its share of dB, dC and the parameters' gradients; a second kernel adds the shares in
 // a fixed order.
 //
-// Measured on one B200 at B8 T4096 D4096 N16 bf16 with a gate: 2.59 ms, and 0.06 for the sums (268 MB
-// of shares of dB and dC).  Shared memory hands over 0.64 of what it can, 0.48 of the cycles issue, with
-// 12 warps an SM: latency between those two.  With the decays kept in registers (two CTAs an SM) 3.43 ms;
-// without segments in turn the 512 CTAs take two waves of 444.
+// Measured on one B200 at B8 T4096 D4096 N16 bf16 with a gate: 2.44 ms, and 0.06 for the sums (268 MB
+// of shares of dB and dC; they grow with N, 4.3 GB at N = 64); the exponentials alone would take 0.46.
+// Shared memory hands over 0.65 of what it can, 0.51 of the cycles issue, with 12 warps an SM: no pipe is
+// full, the warps are too few to cover latencies.  fp32, with two CTAs an SM: 2.99 ms.  With the decays
+// kept in registers (two CTAs an SM) 3.43 ms; without segments in turn the 512 CTAs take two waves of 444.
 #include "scan_common.cuh"
 
 namespace mlstm {
@@ -25,7 +26,10 @@ namespace mlstm {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kTile = 16;
-constexpr int kCtas = 3;  // of an SM
+// CTAs of an SM, by registers.  Shared memory holds three of 9 to 32 states in bf16 and of 17 to 32 in fp32;
+// else two (more than 32 states; fp32 from 9 to 16; bf16 up to 8), or one (fp32 up to 8).  scan_cut counts
+// three for all: there it makes more segments than run at once.
+constexpr int kCtas = 3;
 constexpr int kSlots = 148 * kCtas;
 __device__ unsigned int g_scan_bwd_failures = 0;  // launches that gave up a wait
 static_assert(kTile == 2 * kScanEvery, "two saved states to a tile");

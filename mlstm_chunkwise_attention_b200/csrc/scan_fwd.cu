@@ -7,11 +7,11 @@
 // the channels' lanes by a transposing reduction (each lane ends with one token of one
 // channel), then gated and stored with 16-byte stores.
 //
-// One ex2 per state, channel and token is the floor (16 a cycle and SM: 477 us at B8 T4096 D4096 N16,
-// 19 % more with softplus and the gate).  Measured there on one B200, bf16: 890 us, 941 us with the
-// states kept for the backward.  What binds is latency: 32768 channels are 14 warps an SM, too few to
-// fill the exponentials' pipe (0.59), what shared memory hands over (0.73) and the issue (0.55)
-// at once.  Measured and not kept: one channel to a lane (28 warps, but 10 bytes from shared memory
+// One ex2 per state, channel and token is the floor (16 a cycle and SM at 1.965 GHz: 461 us at B8 T4096
+// D4096 N16, 19 % more with softplus and the gate).  Measured there on one B200, bf16: 903 us, 953 us with
+// the states kept for the backward; fp32 1075 with them.  No pipe is full: the exponentials' 0.57, what
+// shared memory hands over 0.68, the issue 0.54.  32768 channels are 14 warps an SM, all that 128
+// registers a thread leave room for, and they do not cover each other's latencies.  Measured and not kept: one channel to a lane (28 warps, but 10 bytes from shared memory
 // for each state and token: 963 us); tiles staged by warps of their own (1078 us, 80 registers).
 //
 // With few rows the sequence is cut into segments that are scanned at once.  A first pass finds
@@ -26,7 +26,9 @@ namespace {
 constexpr int kTile = 32;
 
 constexpr int kThreads = 64;
-constexpr int kCtas = 8;  // of an SM
+// CTAs of an SM, by registers.  Shared memory holds as many from 9 states on, but 6 of up to 8 states
+// (34.5 KB each), for which scan_cut so counts more slots than there are.
+constexpr int kCtas = 8;
 constexpr int kSlots = 148 * kCtas;
 __device__ unsigned int g_scan_fwd_failures = 0;  // launches that gave up a wait
 
@@ -60,7 +62,9 @@ struct TileLoads {
 // nought would make the padded states NaN, and with them y where the sum over the N states is
 // infinite.  So they are cleared after every token; otherwise the operations of scan_fwd_kernel's loop in
 // their order.  A function of its own: such tiles are rare, and a second loop in the kernel took 12 % of
-// its speed (1075 us instead of 956 at B8 T4096 D4096 N16) by the registers it left to the first.
+// its speed (1075 us instead of 956 at B8 T4096 D4096 N16) by the registers it left to the first.  The
+// kernels for N == NP have neither this nor the check of each tile, which costs 4 % (B8 T2048 D4096 N12
+// bf16: 695 us instead of 667).
 struct Lane {
   float2 A2[2][2], h[2][2];
 };

@@ -1,9 +1,9 @@
 """The operators around the recurrence on the GPU against their 64-bit forms.
 
 Every output and gradient of every case is held to ``_block_ref.close``: half a step of its type plus
-K roundings of its terms' magnitudes.  K counts, for the longest chain of a case: 16 roundings per
-token for the scan (the exponential's four, its argument's product, the update's two, twice over in the
-backward), one per added term for sums taken one after another, and 64 for everything else.
+K roundings of its terms' magnitudes.  K counts, for the longest chain of a case, one rounding per added
+term for sums taken one after another and 64 for everything else; for the scan 64 + T + N, twice that in
+the backward (its magnitudes carry each token's own roundings through the recursion).
 """
 
 import numpy as np
