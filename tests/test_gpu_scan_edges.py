@@ -278,3 +278,28 @@ def test_an_infinite_state_crosses_segments():
     assert ref["y"][0][0, 3:, 5].isinf().all() and ref["y"][0].isinf().sum() == T - 3
     close_where_finite(y, *ref["y"], 64 + T + N, "y")
     close_where_finite(end, *ref["state"], 64 + T + N, "state")
+
+
+def test_backward_offsets_beyond_32_bits():
+    """The backward of a scan over more than 2^31 elements: its last tokens have the gradients of a call that
+    starts there (with the state there), in other segments: to two bf16 steps of the largest."""
+    T, T0, D = 280000, 279900, 8192
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.empty(1, T, D, dtype=BF, device="cuda").normal_(generator=g)
+    assert x.numel() > 2 ** 31
+    A, one = -torch.ones(D, 1, device="cuda"), torch.ones(1, T, 1, dtype=BF, device="cuda")
+    _, saved, _ = block.selective_scan_forward(x, x, A, one, one)
+    got = block.selective_scan_backward(x, x, A, one, one, x, saved)
+    got = {k: got[k][:, T0:].float() for k in ("dx", "ddt", "dB", "dC")}
+    del saved
+    # a step of softplus(x) on average forgets e^-0.8 a token: 400 tokens before T0 decide the state there
+    lead, tail = slice(T0 - 400, T0), slice(T0, T)
+    _, _, st = block.selective_scan_forward(x[:, lead], x[:, lead], A, one[:, lead], one[:, lead],
+                                            keep_saved=False, want_state=True)
+    args = (x[:, tail], x[:, tail], A, one[:, tail], one[:, tail])
+    _, saved, _ = block.selective_scan_forward(*args, state_in=st)
+    want = block.selective_scan_backward(*args, x[:, tail], saved, state_in=st)
+    binding.check_device()
+    for k in got:
+        w = want[k].float()
+        assert float((got[k] - w).abs().max()) <= 2.0 ** -7 * float(w.abs().max()), k
