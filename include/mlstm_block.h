@@ -110,8 +110,8 @@ int mlstm_conv_step(const mlstm_rows_t* x, const float* weight, const float* bia
  * before the first and after the last token; NULL: zeros / not wanted.  States,
  * saved and workspaces are 16-byte aligned.
  * a may be -infinity: a decay of 0.  Infinite and NaN inputs reach y and the
- * states as the formula in fp32 has them, and no other channel or batch but through b
- * and c; gradients that the formula makes infinite may be NaN.
+ * states as the formula in fp32 has them; gradients that the formula makes
+ * infinite may be NaN.
  * ------------------------------------------------------------------------- */
 typedef struct {
   mlstm_rows_t x, dt, z, b, c;
@@ -136,9 +136,9 @@ int mlstm_scan_fwd(const mlstm_scan_t* p, const mlstm_rows_t* y, void* saved, fl
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace mlstm_scan_bwd needs (0 on an argument error).  Most of
- * it holds shares of db and dc, fp32, one for each tile of channels (64 of them
- * for 9 to 16 states; 128, 32, 16 for up to 8, 32, 64): 8 bytes for each token,
- * tile and rounded-up state. */
+ * it holds shares of db and dc, one for each tile of 64 channels (128, 32 and 16
+ * for up to 8, 32 and 64 states): 8 bytes for each token, tile and rounded-up
+ * state, 268 MB at B8 T4096 D4096 N16. */
 size_t mlstm_scan_bwd_workspace_size(int B, int T, int D, int G, int N, int dtype);
 
 /* Gradients of the scan; NULL data: that output is not wanted, except dx, ddt,

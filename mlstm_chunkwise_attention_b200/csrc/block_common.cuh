@@ -222,7 +222,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // The abort state of one launch whose CTAs wait for one another.  `word` lies in the launch's workspace
 // and is zeroed with its counters, by a memset that a graph captures too, so a replayed launch starts
 // clean whatever became of the ones before it.  `failures` is the kernel family's count of launches that
-// gave up; it only grows, so a second failure of the same graph is news as well.
+// gave up since mlstm_device_status last took it, so a second failure of the same graph is news as well.
 struct LaunchAbort {
   unsigned int *word, *failures;
   __device__ __forceinline__ bool raised() const { return *reinterpret_cast<volatile unsigned int*>(word) != 0; }

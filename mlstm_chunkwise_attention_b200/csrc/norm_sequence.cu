@@ -16,9 +16,10 @@
 // squares, and in a fixed order whoever comes last.
 //
 // Measured on one B200 at B4 T8192 NH16 d256 bf16 with SiLU: forward 144 us, backward 299 us (0.57 and
-// 0.42 of a plain copy of the tensors moved once); one group of 268 MB (T32768 d4096): 214 and 450 us.  A second pass over memory took 165 and 324 us at
-// its best; a chunk of half or twice as many items as CTAs 206 / 349 and 175 / 327 us (waits; L2).
-// What bounds it now is the issue of instructions between the barriers (0.5 to 0.6 of the cycles).
+// 0.42 of a plain copy of the tensors moved once); one group of 268 MB (T32768 d4096): 214 and 450 us.  A
+// second pass over memory took 165 and 324 us at its best; a chunk of half or twice as many items as CTAs
+// 206 / 349 and 175 / 327 us (waits; L2).  The issue of instructions between the barriers takes 0.5 to 0.6
+// of the cycles; the rest waits for the second readings that miss L2 and at the barriers.
 #include "norm_common.cuh"
 
 namespace mlstm {

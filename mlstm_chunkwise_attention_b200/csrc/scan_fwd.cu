@@ -11,8 +11,9 @@
 // D4096 N16, 19 % more with softplus and the gate).  Measured there on one B200, bf16: 903 us, 953 us with
 // the states kept for the backward; fp32 1075 with them.  No pipe is full: the exponentials' 0.57, what
 // shared memory hands over 0.68, the issue 0.54.  32768 channels are 14 warps an SM, all that 128
-// registers a thread leave room for, and they do not cover each other's latencies.  Measured and not kept: one channel to a lane (28 warps, but 10 bytes from shared memory
-// for each state and token: 963 us); tiles staged by warps of their own (1078 us, 80 registers).
+// registers a thread leave room for, and they do not cover each other's latencies.  Measured and not kept:
+// one channel to a lane (28 warps, but 10 bytes from shared memory for each state and token: 963 us); tiles
+// staged by warps of their own (1078 us, 80 registers).
 //
 // With few rows the sequence is cut into segments that are scanned at once.  A first pass finds
 // each segment's state from zero and its sum of delta; segment j then starts from
